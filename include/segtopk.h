@@ -88,7 +88,7 @@ typedef enum {
   SEGTOPK_ERROR_INVALID_VALUE = 1,       /* bad enum, null pointer, negative size, k < 0 */
   SEGTOPK_ERROR_INVALID_COMBINATION = 2, /* determinism / tie_break pair not allowed */
   SEGTOPK_ERROR_NOT_SUPPORTED = 3,       /* size or k outside this library's limits */
-  SEGTOPK_ERROR_MISALIGNED = 4,          /* keys pointer not aligned to its element size */
+  SEGTOPK_ERROR_MISALIGNED = 4,          /* a pointer not aligned to its element size */
   SEGTOPK_ERROR_CUDA = 5,                /* a CUDA runtime call failed: see segtopk_last_cuda_error */
   SEGTOPK_ERROR_DEVICE = 6               /* current device is not an sm_103 GPU */
 } segtopk_status;
@@ -335,7 +335,8 @@ SEGTOPK_API int segtopk_last_cuda_error(void);
  * Reads and clears the device-side error word of the current device. The
  * kernels bound every wait on an asynchronous copy; a wait that gives up
  * sets this word (bit 0: copy wait timed out; bit 1: a segment longer than
- * the launch was planned for). Synchronises the device. Returns a status;
+ * the launch was planned for; bit 2: an expert or token id past the last
+ * one, see SEGTOPK_DEVICE_ERROR_INDEX). Synchronises the device. Returns a status;
  * the word is stored in *error_word.
  */
 SEGTOPK_API int segtopk_read_device_error(uint32_t* error_word);
@@ -389,6 +390,153 @@ SEGTOPK_API int segtopk_set_test_hooks(long long wait_limit_cycles, uint32_t fir
  */
 SEGTOPK_API int segtopk_test_device_prep(int n, const int* devices, const uint32_t* smem_bytes,
                                          const int* cluster_widths, uint32_t* actions);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Row operators: expert routing, tokens sorted by expert and back, embedding
+ * ---------------------------------------------------------------------------
+ * The selection's neighbours in a model (the source pages have no counterpart):
+ * the k best experts of every token with their weights; the tokens' rows in
+ * the order of their experts and, weighted, back; the rows of a token
+ * embedding; and the gradients of all three. Sorting is stable and there are
+ * no atomics on results, so every result is the same from run to run.
+ *
+ * Common to all: device pointers unless stated; float types are F16, BF16 and
+ * F32 (others: SEGTOPK_ERROR_NOT_SUPPORTED); sums are held in 32 bits and
+ * rounded once, when they are written. A stride counts elements from one row
+ * to the next, is not negative, and may be smaller than the width for inputs
+ * (0: the same row for all); rows themselves are contiguous, and outputs are
+ * dense. Pointers need the alignment of their elements; rows that start on
+ * 16-byte boundaries and hold a multiple of 16 bytes move fastest. Calls are
+ * asynchronous on `stream`, allocate nothing, may be captured in a graph, and
+ * check their arguments before any launch. Outputs must not overlap inputs.
+ */
+
+/* Bit of the device error word (segtopk_read_device_error): an expert id not
+ * below num_experts or a token not below the table's rows. Such an id counts
+ * as none, like a negative one; negative ids are legitimate and set nothing. */
+#define SEGTOPK_DEVICE_ERROR_INDEX 4u
+
+/* Largest number of experts, and of experts chosen by segtopk_route. */
+#define SEGTOPK_MAX_EXPERTS 1024
+#define SEGTOPK_ROUTE_MAX_K 32
+
+/* Scores of a token's experts. */
+typedef enum {
+  SEGTOPK_SOFTMAX = 0, /* exp(l_e - max) / sum over all experts */
+  SEGTOPK_SIGMOID = 1  /* 1 / (1 + exp(-l_e)) */
+} segtopk_score;
+
+/*
+ * The k best experts of each token, best first, and their weights.
+ *
+ * Chosen by score + bias (bias: `experts` float values, or NULL: none), ties
+ * to the lower expert. Without a bias the logits are compared, which order
+ * as the scores do; +0.0 and -0.0 are equal, and NaN ranks above +inf.
+ * Weights: scale * score, or with renormalize (0 or 1) scale * score / (sum
+ * of the k chosen scores). The bias chooses only and is in no weight.
+ *
+ * An expert whose logit is -inf (or whose bias is) is never chosen: where
+ * fewer than k are left, the last places get expert id -1 and weight 0. NaN
+ * or +inf logits give the weights that the formula gives (NaN).
+ *
+ * logits: tokens rows of `experts` values of `dtype`, row_stride apart.
+ * expert_ids, weights: tokens x k. Limits: 1 <= k <= experts, experts <=
+ * SEGTOPK_MAX_EXPERTS, k <= SEGTOPK_ROUTE_MAX_K, tokens * k < 2^31.
+ */
+SEGTOPK_API int segtopk_route(segtopk_dtype dtype, const void* logits, int64_t tokens, int32_t experts,
+                              int64_t row_stride, int32_t k, segtopk_score score, int renormalize, float scale,
+                              const float* bias, int32_t* expert_ids, float* weights, void* stream);
+
+/*
+ * Gradient of the logits from that of the weights (tokens x k): dense,
+ * tokens x experts of `dtype`. expert_ids are the ones segtopk_route chose
+ * (distinct per token; those outside 0 .. experts - 1 contribute nothing, as
+ * if their weight were not there); score, renormalize and scale as there.
+ */
+SEGTOPK_API int segtopk_route_backward(segtopk_dtype dtype, const float* grad_weights, const void* logits,
+                                       int64_t tokens, int32_t experts, int64_t row_stride, int32_t k,
+                                       const int32_t* expert_ids, segtopk_score score, int renormalize,
+                                       float scale, void* grad_logits, void* stream);
+
+/*
+ * Sorts token slots by expert, stably. expert_ids: `slots` ids (tokens x k,
+ * in that order) of id_bytes 4 (int32) or 8 (int64); a negative one marks a
+ * slot without an expert. Writes
+ *   offsets      experts + 1 int64: expert e has the sorted rows
+ *                [offsets[e], offsets[e + 1]) (usable as segment_offsets);
+ *   row_of_slot  slots int32: the sorted row of each slot, or -1 for none;
+ *   slot_of_row  slots int32: the slot of each sorted row; -1 from row
+ *                offsets[experts] on.
+ * workspace: at least segtopk_group_workspace_bytes(slots, experts) bytes
+ * (which may be 0; host-only arithmetic), 4-byte aligned. experts <=
+ * SEGTOPK_MAX_EXPERTS, slots < 2^31.
+ */
+SEGTOPK_API size_t segtopk_group_workspace_bytes(int64_t slots, int32_t experts);
+SEGTOPK_API int segtopk_group(const void* expert_ids, int32_t id_bytes, int64_t slots, int32_t experts,
+                              int64_t* offsets, int32_t* row_of_slot, int32_t* slot_of_row, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * Copies the tokens' rows into sorted order: rows[r] = x[t] for the row r of
+ * each of token t's k slots. Elements of 1, 2, 4 or 8 bytes are moved as they
+ * are. rows: tokens * k dense rows; from row kept[0] (the last of
+ * segtopk_group's offsets) on they are zeros.
+ */
+SEGTOPK_API int segtopk_dispatch(const void* x, int32_t element_bytes, int64_t tokens, int32_t k, int64_t width,
+                                 int64_t x_stride, const int32_t* row_of_slot, const int64_t* kept, void* rows,
+                                 void* stream);
+
+/*
+ * out[t] = sum over the slots j of token t that have a row r of weights[t, j]
+ * * rows[r], in the order of the slots; weights (tokens x k) NULL: all 1,
+ * which is the gradient of segtopk_dispatch. A token without a row gets
+ * zeros, and rows that no slot has are not read.
+ */
+SEGTOPK_API int segtopk_combine(segtopk_dtype dtype, const void* rows, int64_t tokens, int32_t k, int64_t width,
+                                int64_t row_stride, const int32_t* row_of_slot, const float* weights, void* out,
+                                void* stream);
+
+/*
+ * Gradients of segtopk_combine with weights: grad_rows[r] = weights[t, j] *
+ * grad_out[t] (tokens * k dense rows, zeros from kept[0] on) and
+ * grad_weights[t, j] = the product of rows[r] and grad_out[t] (0 for a slot
+ * without a row).
+ */
+SEGTOPK_API int segtopk_combine_backward(segtopk_dtype dtype, const void* grad_out, int64_t grad_stride,
+                                         const void* rows, int64_t row_stride, int64_t tokens, int32_t k,
+                                         int64_t width, const int32_t* row_of_slot, const int64_t* kept,
+                                         const float* weights, void* grad_rows, float* grad_weights, void* stream);
+
+/*
+ * Embedding: out[i] = scale * table[tokens[i]], computed in 32 bits and
+ * written as out_dtype. table: vocab rows of `width` values, row_stride
+ * apart; tokens: num_tokens ids of token_bytes 4 (int32) or 8 (int64). A
+ * token outside the table gives a row of zeros (a negative one on purpose,
+ * as in a shard of a vocabulary; one past the last row also sets the device
+ * error word). width <= 2^20, vocab < 2^31 - 1, num_tokens < 2^31.
+ */
+SEGTOPK_API int segtopk_embedding(segtopk_dtype dtype, const void* table, int64_t vocab, int64_t width,
+                                  int64_t row_stride, const void* tokens, int32_t token_bytes, int64_t num_tokens,
+                                  float scale, segtopk_dtype out_dtype, void* out, void* stream);
+
+/*
+ * Gradient of the table: grad_table[v] = scale * (sum of grad_out[i] over the
+ * i with tokens[i] = v, in the order of i), as table_dtype; rows without a
+ * token are zeros. With accumulate (0 or 1) that sum is added to grad_table
+ * instead, and only the rows of tokens in the batch are read and written.
+ * padding_token: a token that gets no gradient, or negative for none; tokens
+ * outside the table get none either.
+ *
+ * workspace: at least segtopk_embedding_backward_workspace_bytes(...) bytes,
+ * 256-byte aligned (host-only arithmetic; 0 for sizes out of range).
+ */
+SEGTOPK_API size_t segtopk_embedding_backward_workspace_bytes(int64_t num_tokens, int64_t vocab, int64_t width);
+SEGTOPK_API int segtopk_embedding_backward(segtopk_dtype dtype, const void* grad_out, int64_t grad_stride,
+                                           const void* tokens, int32_t token_bytes, int64_t num_tokens,
+                                           int64_t vocab, int64_t width, int64_t padding_token, float scale,
+                                           segtopk_dtype table_dtype, void* grad_table, int accumulate,
+                                           void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -117,6 +117,8 @@ def _open(path):
     L.segtopk_test_device_prep.restype = c_int
     L.segtopk_test_device_prep.argtypes = [c_int, ctypes.POINTER(c_int), ctypes.POINTER(ctypes.c_uint32),
                                            ctypes.POINTER(c_int), ctypes.POINTER(ctypes.c_uint32)]
+    from . import _rows
+    _rows.declare(L)
     return L
 
 

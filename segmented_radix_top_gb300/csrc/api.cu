@@ -1,5 +1,5 @@
-// C ABI of the segmented top-k library: argument validation, launch planning
-// and dispatch to the per-key-type kernels. See include/segtopk.h.
+// C ABI of the segmented top-k entry points: argument validation, launch
+// planning and dispatch to the per-key-type kernels. See include/segtopk.h.
 #include <algorithm>
 #include <cstring>
 #include <map>
@@ -11,6 +11,7 @@
 #include "block_select.cuh"
 #include "device_prep.h"
 #include "dispatch.h"
+#include "entry.h"
 #include "stream_topk.cuh"
 #include "warp_topk.cuh"
 
@@ -454,6 +455,21 @@ int run_topk(segtopk_dtype key_dtype, const void* keys, const void* values, int 
 // the library's other translation units); returns SEGTOPK_ERROR_CUDA.
 int record_cuda_error(cudaError_t e) { return cuda_fail(e); }
 
+// The rest of what an entry point of another translation unit shares (entry.h).
+void record_launch_count(int launches) { t_last_launch_count = launches; }
+
+int check_device(int* sms)
+{
+  DeviceInfo dev;
+  const cudaError_t e = device_info(&dev);
+  if (e != cudaSuccess)
+    return cuda_fail(e);
+  if (dev.major != 10 || dev.minor != 3)
+    return SEGTOPK_ERROR_DEVICE;
+  *sms = dev.sms;
+  return SEGTOPK_SUCCESS;
+}
+
 } // namespace segtopk
 
 using namespace segtopk;
@@ -621,7 +637,7 @@ extern "C" const char* segtopk_status_string(int status)
   case SEGTOPK_ERROR_INVALID_VALUE: return "invalid argument value";
   case SEGTOPK_ERROR_INVALID_COMBINATION: return "determinism / tie_break combination not allowed";
   case SEGTOPK_ERROR_NOT_SUPPORTED: return "request outside the supported limits";
-  case SEGTOPK_ERROR_MISALIGNED: return "keys pointer is not aligned to its element size";
+  case SEGTOPK_ERROR_MISALIGNED: return "a pointer is not aligned to its element size";
   case SEGTOPK_ERROR_CUDA: return "CUDA runtime error";
   case SEGTOPK_ERROR_DEVICE: return "unsupported device (needs sm_103)";
   default: return "unknown status";
@@ -645,6 +661,13 @@ extern "C" int segtopk_read_device_error(uint32_t* error_word)
   for (const KeyOps* o : list) {
     uint32_t w = 0;
     e = o->read_error(&w);
+    if (e != cudaSuccess)
+      return cuda_fail(e);
+    all |= w;
+  }
+  for (auto read : {&read_group_error, &read_embedding_error}) {
+    uint32_t w = 0;
+    e = read(&w);
     if (e != cudaSuccess)
       return cuda_fail(e);
     all |= w;

@@ -1,0 +1,94 @@
+// Token slots sorted by expert (segtopk_group in include/segtopk.h): a stable
+// counting sort with one digit, the expert; slots without an expert come
+// last and get no row.
+#include "rank_sort.cuh"
+
+namespace segtopk {
+namespace {
+using namespace rows;
+
+__device__ uint32_t g_error;
+
+template <class I>
+struct SlotSource {
+  const I* ids;
+  int experts;
+  struct Item {
+    uint32_t digit;
+  };
+  __device__ __forceinline__ uint32_t digit(uint32_t i) const
+  {
+    const I e = *(ids + i);
+    if (e >= (I)experts)
+      atomicOr(&g_error, (uint32_t)SEGTOPK_DEVICE_ERROR_INDEX);
+    return e >= 0 && e < (I)experts ? (uint32_t)e : (uint32_t)experts;
+  }
+  __device__ __forceinline__ Item load(uint32_t i) const { return {digit(i)}; }
+};
+
+struct SlotSink {
+  int experts;
+  int64_t* offsets;
+  int32_t* row_of_slot;
+  int32_t* slot_of_row;
+  template <class Item>
+  __device__ __forceinline__ void put(uint32_t i, Item item, uint32_t place) const
+  {
+    const bool some = item.digit < (uint32_t)experts;
+    row_of_slot[i] = some ? (int32_t)place : -1;
+    slot_of_row[place] = some ? (int32_t)i : -1;
+  }
+  __device__ __forceinline__ void start(int d, uint32_t first) const { offsets[d] = first; }
+};
+
+} // namespace
+
+cudaError_t read_group_error(uint32_t* word)
+{
+  const uint32_t zero = 0;
+  const cudaError_t e = cudaMemcpyFromSymbol(word, g_error, sizeof(zero));
+  return e != cudaSuccess ? e : cudaMemcpyToSymbol(g_error, &zero, sizeof(zero));
+}
+
+} // namespace segtopk
+
+using namespace segtopk;
+
+extern "C" size_t segtopk_group_workspace_bytes(int64_t slots, int32_t experts)
+{
+  if (slots <= 0 || slots > 2147483647LL || experts < 1 || experts > SEGTOPK_MAX_EXPERTS)
+    return 0;
+  return count_bytes(tiling(slots), experts + 1);
+}
+
+extern "C" int segtopk_group(const void* expert_ids, int32_t id_bytes, int64_t slots, int32_t experts,
+                             int64_t* offsets, int32_t* row_of_slot, int32_t* slot_of_row, void* workspace,
+                             size_t workspace_bytes, void* stream)
+{
+  record_launch_count(0);
+  if ((id_bytes != 4 && id_bytes != 8) || slots < 0 || experts < 1 || !offsets)
+    return SEGTOPK_ERROR_INVALID_VALUE;
+  if (experts > SEGTOPK_MAX_EXPERTS || slots > 2147483647LL)
+    return SEGTOPK_ERROR_NOT_SUPPORTED;
+  if (slots > 0 && (!expert_ids || !row_of_slot || !slot_of_row))
+    return SEGTOPK_ERROR_INVALID_VALUE;
+  if (!aligned(expert_ids, id_bytes) || !aligned(offsets, 8) || !aligned(row_of_slot, 4) ||
+      !aligned(slot_of_row, 4) || !aligned(workspace, 4))
+    return SEGTOPK_ERROR_MISALIGNED;
+  const size_t need = segtopk_group_workspace_bytes(slots, experts);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return SEGTOPK_ERROR_INVALID_VALUE;
+  int sms;
+  const int rc = check_device(&sms);
+  if (rc != SEGTOPK_SUCCESS)
+    return rc;
+  const SlotSink sink = {experts, offsets, row_of_slot, slot_of_row};
+  auto pass = [&](auto zero) {
+    using I = decltype(zero);
+    cudaError_t e = cudaSuccess;
+    const int launches = rank_pass(SlotSource<I>{(const I*)expert_ids, experts}, sink, (uint32_t)slots, tiling(slots),
+                                   experts + 1, (uint32_t*)workspace, (cudaStream_t)stream, &e);
+    return finish(e, launches);
+  };
+  return id_bytes == 4 ? pass(int32_t{}) : pass(int64_t{});
+}

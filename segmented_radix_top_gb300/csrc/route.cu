@@ -1,0 +1,361 @@
+// Expert routing: the k best experts of each token from its router logits,
+// their weights, and the logits' gradient (segtopk_route and
+// segtopk_route_backward in include/segtopk.h).
+//
+// Scores of the logits l of one token: softmax s_e = exp(l_e - m) / sum, or
+// sigmoid s_e = 1 / (1 + exp(-l_e)). Chosen: the k best by (s_e + b_e
+// descending, e ascending); without a bias b the logits themselves are
+// compared, which order alike and, unlike scores rounded to 32 bits, make no
+// new ties. Weights: c s_i, or c s_i / (sum of the chosen scores).
+//
+// One warp serves a token: its lanes hold the row in registers (NV
+// consecutive logits each), so the row is read once, and every step is a
+// register reduction over the warp.
+#include "rows.cuh"
+
+namespace segtopk {
+namespace {
+using namespace rows;
+
+constexpr int kWarps = 8; // tokens of a block
+
+// Order-preserving code of a score: larger is better; +-0 equal; any NaN
+// above +inf; kNone and below for -inf and for places past the row's end,
+// which are never chosen.
+constexpr uint32_t kNone = 0x007fffffu; // code of -inf
+__device__ __forceinline__ uint32_t code_of(float x)
+{
+  const uint32_t b = __float_as_uint(x + 0.0f); // -0 + 0 = +0
+  const uint32_t c = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  return isnan(x) ? 0xffffffffu : c;
+}
+
+__device__ __forceinline__ float warp_sum(float x)
+{
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    x += __shfl_xor_sync(kAll, x, o);
+  return x;
+}
+__device__ __forceinline__ float warp_fmax(float x)
+{
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    x = fmaxf(x, __shfl_xor_sync(kAll, x, o));
+  return x;
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+// NV consecutive logits of a lane, in 32 bits; -inf past the row's end.
+template <class T, int NV, bool VECTOR>
+__device__ __forceinline__ void load_share(float (&x)[NV], const T* row, int first, int experts)
+{
+  if constexpr (VECTOR) {
+    constexpr int V = NV * (int)sizeof(T) > 16 ? 16 / (int)sizeof(T) : NV;
+#pragma unroll
+    for (int v = 0; v < NV; v += V) {
+      if (first + v < experts) { // experts is a multiple of V
+        const Vec<T, V> got = load<T, V>(row + first + v);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          x[v + i] = to_f32(got.at[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          x[v + i] = -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      x[i] = first + i < experts ? to_f32(row[first + i]) : -INFINITY;
+  }
+}
+
+// exp(x_i - m) summed over the row. NaN or +inf among the logits give NaN, as
+// the formula does; a row of -inf alone has no weights and its sum no use.
+template <int NV>
+__device__ __forceinline__ float softmax_sum(const float (&x)[NV], float* top)
+{
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i < NV; ++i)
+    m = fmaxf(m, x[i]);
+  m = warp_fmax(m);
+  float s = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    s += expf(x[i] - m);
+  *top = m;
+  return warp_sum(s);
+}
+
+// The weights of the chosen logits, one per lane (`on`: this lane has one),
+// before the scale. Renormalised sigmoids are taken relative to the largest
+// chosen one when all are small, s_i / s = e^(l_i - h) / (1 + e^(l_i)) with
+// h = min(0, largest l), so that they neither vanish nor divide by zero.
+template <bool SIGMOID>
+__device__ __forceinline__ float chosen_weight(float l, bool on, bool renormalize, float top, float sum)
+{
+  if (!renormalize)
+    return !on ? 0.0f : SIGMOID ? sigmoid(l) : expf(l - top) / sum;
+  const float most = warp_fmax(on ? l : -INFINITY);
+  float s;
+  if (SIGMOID)
+    s = l > 0 ? 1.0f / (1.0f + expf(-l)) : expf(l - fminf(most, 0.0f)) / (1.0f + expf(l));
+  else
+    s = expf(l - most);
+  s = on ? s : 0.0f;
+  const float total = warp_sum(s);
+  return on ? s / total : 0.0f;
+}
+
+template <class T, int NV, bool VECTOR, bool SIGMOID>
+__global__ void __launch_bounds__(kWarps * 32)
+route_kernel(const T* logits, uint32_t tokens, int experts, int64_t stride, int k, bool renormalize, float scale,
+             const float* bias, int32_t* ids, float* weights)
+{
+  wait_for_previous();
+  allow_next();
+  const int lane = threadIdx.x & 31;
+  const uint32_t t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (t >= tokens)
+    return;
+  const T* row = logits + (int64_t)t * stride;
+  const int first = lane * NV;
+  float x[NV];
+  load_share<T, NV, VECTOR>(x, row, first, experts);
+  float top = 0, sum = 1;
+  if (!SIGMOID && (!renormalize || bias))
+    sum = softmax_sum(x, &top);
+  uint32_t code[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float s = x[i];
+    if (bias && first + i < experts && s != -INFINITY)
+      s = (SIGMOID ? sigmoid(s) : expf(s - top) / sum) + bias[first + i];
+    code[i] = code_of(s);
+  }
+  // k rounds: the best code of all lanes; the lowest lane that holds it and
+  // there the lowest place, since lanes hold consecutive experts in order
+  int id = -1; // lane j: the j-th choice
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = code[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i)
+      best = max(best, code[i]);
+    const uint32_t m = __reduce_max_sync(kAll, best);
+    if (m <= kNone)
+      break; // the same for all lanes
+    const int src = __ffs(__ballot_sync(kAll, best == m)) - 1;
+    int at = 0;
+    if (lane == src) {
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (!found && code[i] == m) {
+          found = true;
+          code[i] = 0;
+          at = i;
+        }
+    }
+    const int e = __shfl_sync(kAll, first + at, src);
+    if (lane == j)
+      id = e;
+  }
+  const bool on = id >= 0;
+  const float w = chosen_weight<SIGMOID>(on ? to_f32(row[id]) : 0.0f, on, renormalize, top, sum);
+  if (lane < k) {
+    ids[(int64_t)t * k + lane] = id;
+    weights[(int64_t)t * k + lane] = on ? scale * w : 0.0f;
+  }
+}
+
+// The gradient of the logits, dense: with u_i the weight before the scale c
+// and h_i = c g_i,
+//   softmax, renormalised  d_i = u_i (h_i - sum_j u_j h_j)       else 0
+//   softmax                d_e = s_e (h_e [e chosen] - sum_j s_j h_j)
+//   sigmoid, renormalised  d_i = u_i (1 - s_i) (h_i - sum_j u_j h_j)  else 0
+//   sigmoid                d_i = h_i s_i (1 - s_i)               else 0
+// Only the plain softmax reads the whole row of logits. The row is put
+// together in shared memory and written once.
+template <class T, int NV, bool VECTOR, bool SIGMOID>
+__global__ void __launch_bounds__(kWarps * 32)
+route_backward_kernel(const float* grad, const T* logits, uint32_t tokens, int experts, int64_t stride, int k,
+                      const int32_t* ids, bool renormalize, float scale, T* out)
+{
+  __shared__ float rows_sh[kWarps][NV * 32 + NV];
+  wait_for_previous();
+  allow_next();
+  const int lane = threadIdx.x & 31;
+  const uint32_t t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (t >= tokens)
+    return;
+  float* d = rows_sh[threadIdx.x >> 5];
+  const T* row = logits + (int64_t)t * stride;
+  const int first = lane * NV;
+  int id = lane < k ? ids[(int64_t)t * k + lane] : -1;
+  const bool on = id >= 0 && id < experts;
+  const float g = on ? scale * grad[(int64_t)t * k + lane] : 0.0f;
+  const float l = on ? to_f32(row[id]) : 0.0f;
+  float x[NV];
+  float top = 0, sum = 1;
+  if (!SIGMOID && !renormalize) {
+    load_share<T, NV, VECTOR>(x, row, first, experts);
+    sum = softmax_sum(x, &top);
+  }
+  const float u = chosen_weight<SIGMOID>(l, on, renormalize, top, sum);
+  float dot = 0, part;
+  if (renormalize || !SIGMOID)
+    dot = warp_sum(on ? u * g : 0.0f);
+  if (renormalize)
+    part = u * (g - dot) * (SIGMOID ? 1.0f / (1.0f + expf(l)) : 1.0f); // 1 - sigmoid(l) = sigmoid(-l)
+  else if (SIGMOID)
+    part = g * u * (1.0f / (1.0f + expf(l)));
+  else
+    part = g * u;
+  // a token without choices gets zeros, whatever its logits are
+  const bool dense = !SIGMOID && !renormalize && __any_sync(kAll, on);
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    d[first + i] = dense && first + i < experts ? -(expf(x[i] - top) / sum) * dot : 0.0f;
+  __syncwarp();
+  if (on)
+    atomicAdd(&d[id], part); // ids of a token are distinct: one addition each
+  __syncwarp();
+  T* to = out + (int64_t)t * experts;
+  if constexpr (VECTOR) {
+    constexpr int V = NV * (int)sizeof(T) > 16 ? 16 / (int)sizeof(T) : NV;
+    for (int e = lane * V; e < experts; e += 32 * V) {
+      float y[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        y[i] = d[e + i];
+      store_f32<T, V>(to + e, y);
+    }
+  } else {
+    for (int e = lane; e < experts; e += 32)
+      to[e] = from_f32<T>(d[e]);
+  }
+}
+
+int check(segtopk_dtype dtype, const void* logits, int64_t tokens, int32_t experts, int64_t stride, int32_t k,
+          int score, int renormalize)
+{
+  if (dtype < SEGTOPK_F16 || dtype > SEGTOPK_I32 || (score != SEGTOPK_SOFTMAX && score != SEGTOPK_SIGMOID) ||
+      (renormalize != 0 && renormalize != 1) || tokens < 0 || experts < 1 || k < 1 || k > experts ||
+      stride < 0)
+    return SEGTOPK_ERROR_INVALID_VALUE;
+  if ((dtype != SEGTOPK_F16 && dtype != SEGTOPK_BF16 && dtype != SEGTOPK_F32) || experts > SEGTOPK_MAX_EXPERTS ||
+      k > SEGTOPK_ROUTE_MAX_K || tokens > 2147483647LL / k)
+    return SEGTOPK_ERROR_NOT_SUPPORTED;
+  if (tokens > 0) {
+    if (!logits)
+      return SEGTOPK_ERROR_INVALID_VALUE;
+    if (!aligned(logits, dtype == SEGTOPK_F32 ? 4 : 2))
+      return SEGTOPK_ERROR_MISALIGNED;
+  }
+  return SEGTOPK_SUCCESS;
+}
+
+// Calls f with the share of a lane (a power of two) and whether rows move as
+// vectors.
+template <class F>
+cudaError_t with_share(int experts, bool vector, F&& f)
+{
+  auto one = [&](auto nv) {
+    return vector ? f(nv, std::true_type{}) : f(nv, std::false_type{});
+  };
+  if (experts <= 32)
+    return one(std::integral_constant<int, 1>{});
+  if (experts <= 64)
+    return one(std::integral_constant<int, 2>{});
+  if (experts <= 128)
+    return one(std::integral_constant<int, 4>{});
+  if (experts <= 256)
+    return one(std::integral_constant<int, 8>{});
+  if (experts <= 512)
+    return one(std::integral_constant<int, 16>{});
+  return one(std::integral_constant<int, 32>{});
+}
+
+int share_of(int experts)
+{
+  int nv = 1;
+  while (nv * 32 < experts)
+    nv *= 2;
+  return nv;
+}
+
+} // namespace
+} // namespace segtopk
+
+using namespace segtopk;
+
+extern "C" int segtopk_route(segtopk_dtype dtype, const void* logits, int64_t tokens, int32_t experts,
+                             int64_t row_stride, int32_t k, segtopk_score score, int renormalize, float scale,
+                             const float* bias, int32_t* expert_ids, float* weights, void* stream)
+{
+  record_launch_count(0);
+  int rc = check(dtype, logits, tokens, experts, row_stride, k, score, renormalize);
+  if (rc != SEGTOPK_SUCCESS)
+    return rc;
+  if (tokens == 0)
+    return SEGTOPK_SUCCESS;
+  if (!expert_ids || !weights)
+    return SEGTOPK_ERROR_INVALID_VALUE;
+  if (!aligned(expert_ids, 4) || !aligned(weights, 4) || !aligned(bias, 4))
+    return SEGTOPK_ERROR_MISALIGNED;
+  int sms;
+  if ((rc = check_device(&sms)) != SEGTOPK_SUCCESS)
+    return rc;
+  return with_float_type(dtype, [&](auto zero) {
+    using T = decltype(zero);
+    const int n = std::min<int>(share_of(experts), 16 / (int)sizeof(T));
+    const bool vector = rows_fit(logits, row_stride, experts, sizeof(T), n);
+    return finish(with_share(experts, vector, [&](auto nv, auto vec) {
+      constexpr int NV = decltype(nv)::value;
+      constexpr bool V = decltype(vec)::value;
+      auto kernel = score == SEGTOPK_SIGMOID ? route_kernel<T, NV, V, true> : route_kernel<T, NV, V, false>;
+      return launch(kernel, dim3((unsigned)((tokens + kWarps - 1) / kWarps)), kWarps * 32, 0, (cudaStream_t)stream,
+                    (const T*)logits, (uint32_t)tokens, experts, row_stride, k, renormalize != 0, scale, bias,
+                    expert_ids, weights);
+    }), 1);
+  });
+}
+
+extern "C" int segtopk_route_backward(segtopk_dtype dtype, const float* grad_weights, const void* logits,
+                                      int64_t tokens, int32_t experts, int64_t row_stride, int32_t k,
+                                      const int32_t* expert_ids, segtopk_score score, int renormalize, float scale,
+                                      void* grad_logits, void* stream)
+{
+  record_launch_count(0);
+  int rc = check(dtype, logits, tokens, experts, row_stride, k, score, renormalize);
+  if (rc != SEGTOPK_SUCCESS)
+    return rc;
+  if (tokens == 0)
+    return SEGTOPK_SUCCESS;
+  if (!grad_weights || !expert_ids || !grad_logits)
+    return SEGTOPK_ERROR_INVALID_VALUE;
+  if (!aligned(expert_ids, 4) || !aligned(grad_weights, 4) || !aligned(grad_logits, dtype == SEGTOPK_F32 ? 4 : 2))
+    return SEGTOPK_ERROR_MISALIGNED;
+  int sms;
+  if ((rc = check_device(&sms)) != SEGTOPK_SUCCESS)
+    return rc;
+  return with_float_type(dtype, [&](auto zero) {
+    using T = decltype(zero);
+    const int n = std::min<int>(share_of(experts), 16 / (int)sizeof(T));
+    const bool vector = rows_fit(logits, row_stride, experts, sizeof(T), n) &&
+                        rows_fit(grad_logits, experts, experts, sizeof(T), n);
+    return finish(with_share(experts, vector, [&](auto nv, auto vec) {
+      constexpr int NV = decltype(nv)::value;
+      constexpr bool V = decltype(vec)::value;
+      auto kernel =
+        score == SEGTOPK_SIGMOID ? route_backward_kernel<T, NV, V, true> : route_backward_kernel<T, NV, V, false>;
+      return launch(kernel, dim3((unsigned)((tokens + kWarps - 1) / kWarps)), kWarps * 32, 0, (cudaStream_t)stream,
+                    grad_weights, (const T*)logits, (uint32_t)tokens, experts, row_stride, k, expert_ids,
+                    renormalize != 0, scale, (T*)grad_logits);
+    }), 1);
+  });
+}

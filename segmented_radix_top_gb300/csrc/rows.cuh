@@ -1,0 +1,136 @@
+// Shared pieces of the row operators (routing, sorting tokens by expert,
+// embedding): element types, vectors of them held in 32 bits, launches.
+#pragma once
+
+#include <algorithm>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/segtopk.h"
+#include "entry.h"
+
+namespace segtopk {
+namespace rows {
+
+constexpr uint32_t kAll = 0xffffffffu;
+
+// ---------------------------------------------------------------------------
+// Launch order
+// ---------------------------------------------------------------------------
+// Every row kernel is launched as a programmatic dependent of the kernel
+// before it on its stream: its blocks may be scheduled while that kernel
+// drains, and wait_for_previous() (the first thing each of them does, before
+// any access to global memory) holds them until that kernel has completed
+// and its writes are visible. A chain of such kernels stays in order, since
+// none completes before its own wait has ended. allow_next() lets the next
+// kernel's blocks be scheduled; it promises nothing about memory.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;"); }
+
+template <class... P, class... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, A... args)
+{
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+// ---------------------------------------------------------------------------
+// Elements
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+// rounded to nearest, ties to even
+template <class T> __device__ __forceinline__ T from_f32(float x);
+template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// N consecutive elements, moved as one access where N * sizeof(T) is 2, 4, 8
+// or 16 bytes (32 bytes: two), from an address aligned to that size (16 at
+// most).
+template <class T, int N>
+struct alignas(sizeof(T) * N > 16 ? 16 : sizeof(T) * N) Vec {
+  T at[N];
+};
+
+template <class T, int N>
+__device__ __forceinline__ Vec<T, N> load(const T* p)
+{
+  return *reinterpret_cast<const Vec<T, N>*>(p);
+}
+template <class T, int N>
+__device__ __forceinline__ void store(T* p, const Vec<T, N>& v)
+{
+  *reinterpret_cast<Vec<T, N>*>(p) = v;
+}
+template <class T, int N>
+__device__ __forceinline__ void store_f32(T* p, const float (&x)[N])
+{
+  Vec<T, N> v;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    v.at[i] = from_f32<T>(x[i]);
+  store<T, N>(p, v);
+}
+
+// ---------------------------------------------------------------------------
+// Host helpers
+// ---------------------------------------------------------------------------
+// Calls f with a value of the element type of `dtype`; NOT_SUPPORTED for a
+// type the row operators do not take.
+template <class F>
+int with_float_type(int dtype, F&& f)
+{
+  switch (dtype) {
+  case SEGTOPK_F16: return f(__half{});
+  case SEGTOPK_BF16: return f(__nv_bfloat16{});
+  case SEGTOPK_F32: return f(float{});
+  case SEGTOPK_F64:
+  case SEGTOPK_U32:
+  case SEGTOPK_I32: return SEGTOPK_ERROR_NOT_SUPPORTED;
+  default: return SEGTOPK_ERROR_INVALID_VALUE;
+  }
+}
+
+inline bool aligned(const void* p, size_t bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
+
+// Whether rows of `width` elements of `size` bytes, `stride` elements apart
+// from p on, can be moved as vectors of `n` elements.
+inline bool rows_fit(const void* p, int64_t stride, int64_t width, size_t size, int n)
+{
+  const size_t bytes = std::min<size_t>(16, size * (size_t)n);
+  return width % n == 0 && aligned(p, bytes) && ((size_t)stride * size) % bytes == 0;
+}
+
+// Threads that share one row: the smallest power of two that covers `vectors`
+// (at least 1), up to `most`.
+inline int lanes_for(int64_t vectors, int most)
+{
+  int l = 1;
+  while (l < most && l < vectors)
+    l *= 2;
+  return l;
+}
+
+inline int finish(cudaError_t e, int launches)
+{
+  if (e != cudaSuccess)
+    return record_cuda_error(e);
+  record_launch_count(launches);
+  return SEGTOPK_SUCCESS;
+}
+
+} // namespace rows
+} // namespace segtopk
