@@ -20,6 +20,7 @@ using namespace rows;
 
 constexpr int kThreads = 256;
 constexpr int kSms = 152;
+constexpr int kInFlight = 4; // vectors of a row that a thread has in flight
 constexpr int kDigitBits = 9; // of a radix pass: 512 counters a warp in shared memory
 
 __device__ uint32_t g_error;
@@ -48,15 +49,23 @@ lookup_kernel(const T* table, int64_t stride, int64_t vocab, const I* tokens, ui
   if (i >= n)
     return;
   const int64_t v = row_of_token(tokens, i, vocab);
-  for (int64_t c = (int64_t)lane * N; c < width; c += (int64_t)lanes * N) {
-    float y[N] = {};
-    if (v >= 0) {
-      const Vec<T, N> got = load<T, N>(table + v * stride + c);
+  constexpr int U = kInFlight;
+  const int64_t step = (int64_t)lanes * N;
+  for (int64_t c0 = (int64_t)lane * N; c0 < width; c0 += U * step) {
+    Vec<T, N> got[U] = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (v >= 0 && c0 + u * step < width)
+        got[u] = load<T, N>(table + v * stride + c0 + u * step);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float y[N];
 #pragma unroll
       for (int e = 0; e < N; ++e)
-        y[e] = scale * to_f32(got.at[e]);
+        y[e] = v >= 0 ? scale * got[u].f32(e) : 0.0f;
+      if (c0 + u * step < width)
+        store_f32<O, N>(out + (int64_t)i * width + c0 + u * step, y);
     }
-    store_f32<O, N>(out + (int64_t)i * width + c, y);
   }
 }
 
@@ -121,19 +130,47 @@ struct Merge {
   int32_t *head_row, *carry_row; // [shares]: their rows, or -1
 };
 
-// The number of positions among the first d steps of the merge, in which
-// position a comes before the end of row r if keys[a] <= r.
-__device__ __forceinline__ uint32_t positions_before(const Merge& m, uint64_t d)
+// The number of positions among the first d[i] steps of the merge, in which
+// position a comes before the end of row r if keys[a] <= r, for both ends of
+// a share. The group's lanes (those of a warp at most) try as many places a
+// round, so a search takes two or three dependent loads instead of a dozen.
+__device__ __forceinline__ void positions_before(const Merge& m, const uint64_t (&d)[2], uint32_t (&a)[2])
 {
-  uint64_t lo = d > m.vocab ? d - m.vocab : 0, hi = d < m.n ? d : m.n;
-  while (lo < hi) {
-    const uint64_t mid = (lo + hi) / 2;
-    if ((uint64_t)m.keys[mid] + mid < d)
-      lo = mid + 1;
-    else
-      hi = mid;
+  const uint32_t g = min(m.lanes, 32), lane = threadIdx.x & 31, mine = lane & (g - 1);
+  const unsigned mask = (g == 32 ? kAll : ((1u << g) - 1)) << (lane - mine);
+  uint32_t lo[2], hi[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    lo[i] = (uint32_t)(d[i] > m.vocab ? d[i] - m.vocab : 0);
+    hi[i] = (uint32_t)(d[i] < m.n ? d[i] : m.n);
   }
-  return (uint32_t)lo;
+  while (lo[0] < hi[0] || lo[1] < hi[1]) {
+    uint32_t at[2];
+    bool less[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t span = hi[i] - lo[i];
+      // `mine`-th of g places, all different while there are so many
+      at[i] = lo[i] + (span <= g ? mine : (uint32_t)((uint64_t)span * (mine + 1) / (g + 1)));
+      less[i] = at[i] < hi[i] && (uint64_t)m.keys[at[i]] + at[i] < d[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t span = hi[i] - lo[i];
+      const uint32_t n = __popc(__ballot_sync(mask, less[i]));
+      if (span <= g) {
+        lo[i] = hi[i] = lo[i] + n;
+      } else {
+        const uint32_t low = lo[i];
+        if (n > 0)
+          lo[i] = low + (uint32_t)((uint64_t)span * n / (g + 1)) + 1;
+        if (n < g)
+          hi[i] = low + (uint32_t)((uint64_t)span * (n + 1) / (g + 1));
+      }
+    }
+  }
+  a[0] = lo[0];
+  a[1] = lo[1];
 }
 
 // DENSE: every row of the table is written, rows without tokens as zeros, and
@@ -148,14 +185,18 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
   const int lane = threadIdx.x & (m.lanes - 1);
   const uint32_t p = blockIdx.x * (kThreads / m.lanes) + threadIdx.x / m.lanes;
   const int64_t c = ((int64_t)blockIdx.y * m.lanes + lane) * N;
-  if (p >= m.shares || c >= m.width)
+  if (p >= m.shares)
     return;
   const uint64_t steps = (uint64_t)m.n + (DENSE ? m.vocab : 0);
-  const uint64_t d0 = steps * p / m.shares, d1 = steps * (p + 1) / m.shares;
-  const uint32_t a0 = DENSE ? positions_before(m, d0) : (uint32_t)d0;
-  const uint32_t a1 = DENSE ? positions_before(m, d1) : (uint32_t)d1;
-  const uint32_t r1 = DENSE ? (uint32_t)(d1 - a1) : m.vocab;
-  uint32_t row = DENSE ? (uint32_t)(d0 - a0) : (a0 < a1 ? m.keys[a0] : m.vocab);
+  const uint64_t d[2] = {steps * p / m.shares, steps * (p + 1) / m.shares};
+  uint32_t a[2] = {(uint32_t)d[0], (uint32_t)d[1]};
+  if (DENSE)
+    positions_before(m, d, a);
+  if (c >= m.width)
+    return;
+  const uint32_t a0 = a[0], a1 = a[1];
+  const uint32_t r1 = DENSE ? (uint32_t)(d[1] - a1) : m.vocab;
+  uint32_t row = DENSE ? (uint32_t)(d[0] - a0) : (a0 < a1 ? m.keys[a0] : m.vocab);
   bool begun = a0 > 0 && row < m.vocab && m.keys[a0 - 1] == row; // by an earlier share
   bool any = false;
   int32_t head_row = -1, carry_row = -1;
@@ -176,7 +217,7 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
         const Vec<W, N> was = load<W, N>(to);
 #pragma unroll
         for (int e = 0; e < N; ++e)
-          y[e] += to_f32(was.at[e]);
+          y[e] += was.f32(e);
       }
       store_f32<W, N>(to, y);
     }
@@ -187,14 +228,14 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
   };
 
   constexpr int U = 4; // rows in flight
-  for (uint32_t a = a0; a < a1; a += U) {
+  for (uint32_t i = a0; i < a1; i += U) {
     uint32_t key[U];
     Vec<G, N> v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      key[u] = a + u < a1 ? m.keys[a + u] : m.vocab;
+      key[u] = i + u < a1 ? m.keys[i + u] : m.vocab;
       if (key[u] < m.vocab)
-        v[u] = load<G, N>(grad + (int64_t)m.at[a + u] * stride + c);
+        v[u] = load<G, N>(grad + (int64_t)m.at[i + u] * stride + c);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -209,7 +250,7 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
       }
 #pragma unroll
       for (int e = 0; e < N; ++e)
-        acc[e] += to_f32(v[u].at[e]);
+        acc[e] += v[u].f32(e);
       any = true;
     }
   }
@@ -230,44 +271,88 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
 }
 
 // A row that began in shares before p and ended in p: the parts that those
-// left, in their order, and p's own.
+// left, in their order, and p's own. A block serves one share and kJoinCols
+// columns. A frequent token leaves its row's parts in many shares; from
+// kJoinSplit parts on the block's warps sum a run of them each, and the runs'
+// sums are added in order.
+constexpr int kJoinCols = kThreads * 4;
+constexpr uint32_t kJoinSplit = 16;
+
 template <class W, int N, bool DENSE>
 __global__ void __launch_bounds__(kThreads) join_kernel(Merge m, W* out)
 {
+  __shared__ float part[kThreads / 32][32 * N];
   wait_for_previous();
   allow_next();
-  const int lane = threadIdx.x & (m.lanes - 1);
-  const uint32_t p = blockIdx.x * (kThreads / m.lanes) + threadIdx.x / m.lanes;
-  const int64_t c = ((int64_t)blockIdx.y * m.lanes + lane) * N;
-  if (p >= m.shares || c >= m.width)
-    return;
+  const uint32_t p = blockIdx.x;
   const int32_t row = m.head_row[p];
   if (row < 0)
     return;
-  uint32_t q = p;
-  while (q > 0 && m.carry_row[q - 1] == row)
-    --q;
-  float acc[N] = {};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t first = p; // of the shares that hold a part
+  for (bool more = true; more;) {
+    const bool held = first > (uint32_t)lane && m.carry_row[first - 1 - lane] == row;
+    const uint32_t n = __ffs(~__ballot_sync(kAll, held)) - 1u; // all ones: none, so -1
+    more = n > 31;
+    first -= more ? 32 : n;
+  }
+
+  auto sum = [&](uint32_t q, uint32_t end, int64_t c, float (&acc)[N]) {
 #pragma unroll 4
-  for (; q < p; ++q) {
-    const Vec<float, N> v = load<float, N>(m.carry + (int64_t)q * m.width + c);
+    for (; q < end; ++q) {
+      const Vec<float, N> v = load<float, N>(m.carry + (int64_t)q * m.width + c);
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        acc[e] += v.f32(e);
+    }
+  };
+  auto write = [&](int64_t c, const float (&acc)[N]) {
+    const Vec<float, N> v = load<float, N>(m.head + (int64_t)p * m.width + c);
+    W* to = out + (int64_t)row * m.width + c;
+    float y[N];
 #pragma unroll
     for (int e = 0; e < N; ++e)
-      acc[e] += v.at[e];
-  }
-  const Vec<float, N> v = load<float, N>(m.head + (int64_t)p * m.width + c);
-  W* to = out + (int64_t)row * m.width + c;
-  float y[N];
+      y[e] = m.scale * (acc[e] + v.f32(e));
+    if constexpr (!DENSE) {
+      const Vec<W, N> was = load<W, N>(to);
 #pragma unroll
-  for (int e = 0; e < N; ++e)
-    y[e] = m.scale * (acc[e] + v.at[e]);
-  if constexpr (!DENSE) {
-    const Vec<W, N> was = load<W, N>(to);
+      for (int e = 0; e < N; ++e)
+        y[e] += was.f32(e);
+    }
+    store_f32<W, N>(to, y);
+  };
+
+  const int64_t c0 = (int64_t)blockIdx.y * kJoinCols, c1 = min(m.width, c0 + kJoinCols);
+  const uint32_t parts = p - first;
+  if (parts < kJoinSplit) {
+    for (int64_t c = c0 + (int64_t)threadIdx.x * N; c < c1; c += (int64_t)kThreads * N) {
+      float acc[N] = {};
+      sum(first, p, c, acc);
+      write(c, acc);
+    }
+    return;
+  }
+  constexpr uint32_t kWarps = kThreads / 32;
+  const uint32_t q0 = first + (uint32_t)((uint64_t)parts * warp / kWarps);
+  const uint32_t q1 = first + (uint32_t)((uint64_t)parts * (warp + 1) / kWarps);
+  for (int64_t t = c0; t < c1; t += 32 * N) {
+    const int64_t c = t + lane * N;
+    float acc[N] = {};
+    if (c < c1)
+      sum(q0, q1, c, acc);
 #pragma unroll
     for (int e = 0; e < N; ++e)
-      y[e] += to_f32(was.at[e]);
+      part[warp][lane * N + e] = acc[e];
+    __syncthreads();
+    if (warp == 0 && c < c1) {
+      for (uint32_t w = 1; w < kWarps; ++w)
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          acc[e] += part[w][lane * N + e];
+      write(c, acc);
+    }
+    __syncthreads();
   }
-  store_f32<W, N>(to, y);
 }
 
 // ---------------------------------------------------------------------------
@@ -276,9 +361,17 @@ __global__ void __launch_bounds__(kThreads) join_kernel(Merge m, W* out)
 struct Layout {
   int passes, digit_bits;
   Tiling tiles;
-  uint32_t shares;
+  uint32_t most_shares; // of any call with these sizes
   size_t pairs, counts, parts, rows, total; // bytes of each piece
 };
+
+// Shares of the merge: at most twice as many groups as are resident, of 16
+// steps at least (a share costs a search and up to two parts of rows).
+uint32_t shares_of(int64_t steps, int64_t width)
+{
+  const int64_t most = 2 * (int64_t)kSms * 2048 / std::max<int64_t>(1, std::min<int64_t>((width + 7) / 8, 2048));
+  return (uint32_t)std::max<int64_t>(1, std::min<int64_t>(most, (steps + 15) / 16));
+}
 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -291,13 +384,11 @@ Layout layout_of(int64_t n, int64_t vocab, int64_t width)
   l.passes = (bits + kDigitBits - 1) / kDigitBits;
   l.digit_bits = (bits + l.passes - 1) / l.passes;
   l.tiles = tiling(n);
-  // shares: twice as many groups as are resident, of eight steps at least
-  const int64_t most = 2 * (int64_t)kSms * 2048 / std::max<int64_t>(1, std::min<int64_t>((width + 7) / 8, 2048));
-  l.shares = (uint32_t)std::max<int64_t>(1, std::min<int64_t>(most, (n + vocab + 7) / 8));
+  l.most_shares = shares_of(n + vocab, width);
   l.pairs = round_up((size_t)n * 4);
   l.counts = round_up(count_bytes(l.tiles, 1 << l.digit_bits));
-  l.parts = round_up((size_t)l.shares * (size_t)width * 4);
-  l.rows = round_up((size_t)l.shares * 4);
+  l.parts = round_up((size_t)l.most_shares * (size_t)width * 4);
+  l.rows = round_up((size_t)l.most_shares * 4);
   l.total = 4 * l.pairs + l.counts + 2 * l.parts + 2 * l.rows;
   return l;
 }
@@ -350,7 +441,7 @@ extern "C" int segtopk_embedding(segtopk_dtype dtype, const void* table, int64_t
       auto go = [&](auto n, auto id) {
         constexpr int V = decltype(n)::value;
         using I = decltype(id);
-        const int lanes = lanes_for(width / V, kThreads);
+        const int lanes = lanes_for((width / V + kInFlight - 1) / kInFlight, kThreads);
         const int64_t per_block = kThreads / lanes;
         return finish(launch(lookup_kernel<T, O, V, I>, dim3((unsigned)((num_tokens + per_block - 1) / per_block)),
                              kThreads, 0, (cudaStream_t)stream, (const T*)table, row_stride, vocab, (const I*)tokens,
@@ -443,8 +534,7 @@ extern "C" int segtopk_embedding_backward(segtopk_dtype dtype, const void* grad_
         m.vocab = (uint32_t)vocab;
         m.width = width;
         // no share without a step: a row's shares have to be neighbours
-        const int64_t steps = (int64_t)n + (DENSE ? vocab : 0);
-        m.shares = (uint32_t)std::min<int64_t>(l.shares, (steps + 7) / 8);
+        m.shares = shares_of((int64_t)n + (DENSE ? vocab : 0), width);
         m.lanes = lanes_for(width / V, kThreads);
         m.scale = scale;
         m.head = (float*)piece(l.parts);
@@ -456,8 +546,10 @@ extern "C" int segtopk_embedding_backward(segtopk_dtype dtype, const void* grad_
         const dim3 grid((m.shares + per_block - 1) / per_block, (unsigned)((width + cols - 1) / cols));
         e = launch(merge_kernel<G, W, V, DENSE>, grid, kThreads, 0, st, m, (const G*)grad_out, grad_stride,
                    (W*)grad_table);
+        constexpr int J = V > 4 ? 4 : V; // columns of a thread: 16 bytes of the parts
+        const dim3 joins(m.shares, (unsigned)((width + kJoinCols - 1) / kJoinCols));
         if (e == cudaSuccess)
-          e = launch(join_kernel<W, V, DENSE>, grid, kThreads, 0, st, m, (W*)grad_table);
+          e = launch(join_kernel<W, J, DENSE>, joins, kThreads, 0, st, m, (W*)grad_table);
         return finish(e, launches + 2);
       };
       const bool vector = rows_fit(grad_out, grad_stride, width, sizeof(G), N) &&

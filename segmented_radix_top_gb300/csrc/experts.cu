@@ -40,14 +40,14 @@ __device__ __forceinline__ uint32_t group_token(const Shape& s, int* lane)
 
 // Rows past the last kept one are zeros: group t clears every tokens-th of
 // them from its own on.
-template <class T, int N>
-__device__ __forceinline__ void clear_tail(const Shape& s, const int64_t* kept, uint32_t t, int lane, T* rows)
+template <class U>
+__device__ __forceinline__ void clear_tail(const Shape& s, const int64_t* kept, uint32_t t, int lane, int64_t units,
+                                           U* rows)
 {
   const int64_t slots = (int64_t)s.tokens * s.k;
-  Vec<T, N> zero = {};
   for (int64_t r = max(*kept, (int64_t)0) + t; r < slots; r += s.tokens)
-    for (int64_t c = (int64_t)lane * N; c < s.width; c += (int64_t)s.lanes * N)
-      store<T, N>(rows + r * s.width + c, zero);
+    for (int64_t c = lane; c < units; c += s.lanes)
+      rows[r * units + c] = U{};
 }
 
 // Elements are moved as they are: T is an unsigned integer of their size or
@@ -72,11 +72,11 @@ dispatch_kernel(const T* x, int64_t stride, Shape s, const int32_t* row_of_slot,
         rows[(int64_t)r * s.width + c] = v;
     }
   }
-  clear_tail<T, 1>(s, kept, t, lane, rows);
+  clear_tail(s, kept, t, lane, s.width, rows);
 }
 
 template <class T, int N, bool WEIGHTED>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 combine_kernel(const T* rows, int64_t stride, Shape s, const int32_t* row_of_slot, const float* weights, T* out)
 {
   wait_for_previous();
@@ -107,7 +107,7 @@ combine_kernel(const T* rows, int64_t stride, Shape s, const int32_t* row_of_slo
         const float wj = WEIGHTED ? *(w + j0 + j) : 1.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          acc[i] = fmaf(wj, to_f32(v[j].at[i]), acc[i]);
+          acc[i] = fmaf(wj, v[j].f32(i), acc[i]);
       }
     }
     store_f32<T, N>(out + (int64_t)t * s.width + c, acc);
@@ -115,7 +115,7 @@ combine_kernel(const T* rows, int64_t stride, Shape s, const int32_t* row_of_slo
 }
 
 template <class T, int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 combine_backward_kernel(const T* grad, int64_t grad_stride, const T* rows, int64_t stride, Shape s,
                         const int32_t* row_of_slot, const float* weights, const int64_t* kept, T* grad_rows,
                         float* grad_weights)
@@ -145,7 +145,7 @@ combine_backward_kernel(const T* grad, int64_t grad_stride, const T* rows, int64
         const Vec<T, N> got = load<T, N>(grad + (int64_t)t * grad_stride + c);
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          g[i] = to_f32(got.at[i]);
+          g[i] = got.f32(i);
         Vec<T, N> v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -158,7 +158,7 @@ combine_backward_kernel(const T* grad, int64_t grad_stride, const T* rows, int64
           float y[N];
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            dot[j] = fmaf(to_f32(v[j].at[i]), g[i], dot[j]);
+            dot[j] = fmaf(v[j].f32(i), g[i], dot[j]);
             y[i] = wj[j] * g[i];
           }
           store_f32<T, N>(grad_rows + r[j] * s.width + c, y);
@@ -192,7 +192,7 @@ combine_backward_kernel(const T* grad, int64_t grad_stride, const T* rows, int64
     }
   }
   if (some)
-    clear_tail<T, N>(s, kept, t, lane, grad_rows);
+    clear_tail(s, kept, t, lane, s.width / N, reinterpret_cast<Vec<T, N>*>(grad_rows));
 }
 
 dim3 grid_of(const Shape& s)

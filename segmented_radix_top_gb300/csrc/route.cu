@@ -59,7 +59,7 @@ __device__ __forceinline__ void load_share(float (&x)[NV], const T* row, int fir
         const Vec<T, V> got = load<T, V>(row + first + v);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          x[v + i] = to_f32(got.at[i]);
+          x[v + i] = got.f32(i);
       } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -59,29 +60,75 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
 
 // N consecutive elements, moved as one access where N * sizeof(T) is 2, 4, 8
 // or 16 bytes (32 bytes: two), from an address aligned to that size (16 at
-// most).
+// most). They are kept as the 32-bit words they came in, two 16-bit elements
+// to a register, until each is used: held as elements, a vector of eight
+// takes eight registers, and kernels that keep eight vectors in flight had
+// 100 registers a thread and half the occupancy.
 template <class T, int N>
 struct alignas(sizeof(T) * N > 16 ? 16 : sizeof(T) * N) Vec {
-  T at[N];
+  static constexpr int kWords = (int)sizeof(T) * N / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ float f32(int i) const // i known when compiling
+  {
+    if constexpr (sizeof(T) == 4)
+      return __uint_as_float(w[i]);
+    else if constexpr (std::is_same_v<T, __nv_bfloat16>)
+      return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    else
+      return __half2float(__ushort_as_half((unsigned short)(w[i / 2] >> (16 * (i & 1)))));
+  }
+  __device__ __forceinline__ void set(const float (&x)[N])
+  {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        w[i] = __float_as_uint(x[i]);
+      } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+  }
+};
+template <class T>
+struct Vec<T, 1> {
+  T one;
+  __device__ __forceinline__ float f32(int) const { return to_f32(one); }
+  __device__ __forceinline__ void set(const float (&x)[1]) { one = from_f32<T>(x[0]); }
 };
 
 template <class T, int N>
 __device__ __forceinline__ Vec<T, N> load(const T* p)
 {
-  return *reinterpret_cast<const Vec<T, N>*>(p);
+  Vec<T, N> v;
+  if constexpr (sizeof(v) % 16 == 0) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(v) / 16; ++i)
+      reinterpret_cast<uint4*>(&v)[i] = reinterpret_cast<const uint4*>(p)[i];
+  } else {
+    v = *reinterpret_cast<const Vec<T, N>*>(p);
+  }
+  return v;
 }
 template <class T, int N>
 __device__ __forceinline__ void store(T* p, const Vec<T, N>& v)
 {
-  *reinterpret_cast<Vec<T, N>*>(p) = v;
+  if constexpr (sizeof(v) % 16 == 0) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(v) / 16; ++i)
+      reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(&v)[i];
+  } else {
+    *reinterpret_cast<Vec<T, N>*>(p) = v;
+  }
 }
 template <class T, int N>
 __device__ __forceinline__ void store_f32(T* p, const float (&x)[N])
 {
   Vec<T, N> v;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    v.at[i] = from_f32<T>(x[i]);
+  v.set(x);
   store<T, N>(p, v);
 }
 
