@@ -23,14 +23,12 @@ constexpr int kSms = 152;
 constexpr int kInFlight = 4; // vectors of a row that a thread has in flight
 constexpr int kDigitBits = 9; // of a radix pass: 512 counters a warp in shared memory
 
-__device__ uint32_t g_error;
-
 template <class I>
 __device__ __forceinline__ int64_t row_of_token(const I* tokens, uint32_t i, int64_t vocab)
 {
   const int64_t v = (int64_t)*(tokens + i);
   if (v >= vocab)
-    atomicOr(&g_error, (uint32_t)SEGTOPK_DEVICE_ERROR_INDEX);
+    raise_error(SEGTOPK_DEVICE_ERROR_INDEX);
   return v >= 0 && v < vocab ? v : -1;
 }
 
@@ -78,41 +76,12 @@ template <class I>
 struct TokenSource {
   const I* tokens;
   int64_t vocab, padding;
-  uint32_t mask;
-  struct Item {
-    uint32_t digit, key, at;
-  };
   __device__ __forceinline__ uint32_t key(uint32_t i) const
   {
     const int64_t v = row_of_token(tokens, i, vocab);
     return v < 0 || v == padding ? (uint32_t)vocab : (uint32_t)v;
   }
-  __device__ __forceinline__ uint32_t digit(uint32_t i) const { return key(i) & mask; }
-  __device__ __forceinline__ Item load(uint32_t i) const
-  {
-    const uint32_t k = key(i);
-    return {k & mask, k, i};
-  }
-};
-struct PairSource {
-  const uint32_t *keys, *at;
-  int shift;
-  uint32_t mask;
-  struct Item {
-    uint32_t digit, key, at;
-  };
-  __device__ __forceinline__ uint32_t digit(uint32_t i) const { return (keys[i] >> shift) & mask; }
-  __device__ __forceinline__ Item load(uint32_t i) const { return {digit(i), keys[i], at[i]}; }
-};
-struct PairSink {
-  uint32_t *keys, *at;
-  template <class Item>
-  __device__ __forceinline__ void put(uint32_t, Item item, uint32_t place) const
-  {
-    keys[place] = item.key;
-    at[place] = item.at;
-  }
-  __device__ __forceinline__ void start(int, uint32_t) const {}
+  __device__ __forceinline__ uint32_t at(uint32_t i) const { return i; }
 };
 
 // ---------------------------------------------------------------------------
@@ -176,8 +145,50 @@ __device__ __forceinline__ void positions_before(const Merge& m, const uint64_t 
 // DENSE: every row of the table is written, rows without tokens as zeros, and
 // a share is a part of the positions and rows together. Otherwise only the
 // tokens' rows are added to, and a share is a part of the positions.
+//
+// A row is written by the share that holds its last position; if that share
+// does not hold the row's first one too, its part goes to `head`, and the
+// parts of the shares before it to their `carry`.
+//
+// Bound by the latency of the gathered rows unless enough of them are under
+// way: every thread copies its part of the next kAhead positions' rows (and,
+// when adding, of the table rows that they complete) into shared memory of
+// its own with asynchronous copies, which takes no registers and, as no
+// thread reads another's part, no barrier. Elements too badly aligned for
+// that (N = 1) go in batches of eight through registers.
+constexpr int kRingBytes = 48 << 10; // of a block; four blocks an SM
 template <class G, class W, int N, bool DENSE>
-__global__ void __launch_bounds__(kThreads)
+struct Ring {
+  static constexpr bool kUsed = N > 1;
+  static constexpr int kGrad = N * (int)sizeof(G), kRow = DENSE ? 0 : N * (int)sizeof(W); // bytes of a position
+  static constexpr int kFit = kRingBytes / (kThreads * (kGrad + kRow));
+  static constexpr int kAhead = kFit < 16 ? kFit : 16;
+  static constexpr int kBytes = kUsed ? kAhead * kThreads * (kGrad + kRow) : 0;
+  char* memory;
+  __device__ __forceinline__ char* grad(int slot) const { return memory + (slot * kThreads + threadIdx.x) * kGrad; }
+  __device__ __forceinline__ char* row(int slot) const
+  {
+    return memory + kAhead * kThreads * kGrad + (slot * kThreads + threadIdx.x) * kRow;
+  }
+};
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from)
+{
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(to)), "l"(from), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_for_copies() // all but the last N groups
+{
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <class G, class W, int N, bool DENSE>
+__global__ void __launch_bounds__(kThreads, 4)
 merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
 {
   wait_for_previous();
@@ -194,76 +205,117 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
     positions_before(m, d, a);
   if (c >= m.width)
     return;
+  out += c;
   const uint32_t a0 = a[0], a1 = a[1];
-  const uint32_t r1 = DENSE ? (uint32_t)(d[1] - a1) : m.vocab;
-  uint32_t row = DENSE ? (uint32_t)(d[0] - a0) : (a0 < a1 ? m.keys[a0] : m.vocab);
-  bool begun = a0 > 0 && row < m.vocab && m.keys[a0 - 1] == row; // by an earlier share
-  bool any = false;
-  int32_t head_row = -1, carry_row = -1;
-  float acc[N] = {};
+  const uint32_t before = a0 > 0 ? m.keys[a0 - 1] : m.vocab;
+  bool begun = a0 < a1 && m.keys[a0] == before; // the first position's row, by an earlier share
+  uint32_t empty = 0;                           // DENSE: the next row that may have no position
+  if (DENSE) {
+    empty = (uint32_t)(d[0] - a0);
+    empty += empty == before;
+  }
+  auto clear_to = [&](uint32_t row) {
+    W* to = out + (int64_t)empty * m.width;
+    const Vec<W, N> zero = {};
+#pragma unroll 4
+    for (; empty < row; ++empty, to += m.width)
+      store<W, N>(to, zero);
+    empty = row + 1;
+  };
 
-  auto finish_row = [&]() {
+  float acc[N] = {};
+  int32_t head_row = -1, carry_row = -1;
+  // one position: its key, the next one's, its gradient, and the row it adds
+  // to if the keys differ
+  auto take = [&](uint32_t key, uint32_t next, const Vec<G, N>& v, const Vec<W, N>& was) {
+    if (DENSE)
+      clear_to(key);
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      acc[e] += v.f32(e);
+    carry_row = (int32_t)key;
+    if (next == key)
+      return;
     if (begun) {
       store_f32<float, N>(m.head + (int64_t)p * m.width + c, acc);
-      head_row = (int32_t)row;
-      begun = false;
+      head_row = carry_row;
     } else {
-      W* to = out + (int64_t)row * m.width + c;
-      float y[N];
 #pragma unroll
       for (int e = 0; e < N; ++e)
-        y[e] = m.scale * acc[e];
-      if constexpr (!DENSE) {
-        const Vec<W, N> was = load<W, N>(to);
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-          y[e] += was.f32(e);
-      }
-      store_f32<W, N>(to, y);
+        acc[e] = DENSE ? m.scale * acc[e] : fmaf(m.scale, acc[e], was.f32(e));
+      store_f32<W, N>(out + (int64_t)key * m.width, acc);
     }
+    begun = false;
+    carry_row = -1;
 #pragma unroll
     for (int e = 0; e < N; ++e)
       acc[e] = 0;
-    any = false;
   };
+  auto key_at = [&](uint32_t i) { return i < m.n ? m.keys[i] : m.vocab; };
+  grad += c;
 
-  constexpr int U = 4; // rows in flight
-  for (uint32_t i = a0; i < a1; i += U) {
-    uint32_t key[U];
-    Vec<G, N> v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      key[u] = i + u < a1 ? m.keys[i + u] : m.vocab;
-      if (key[u] < m.vocab)
-        v[u] = load<G, N>(grad + (int64_t)m.at[i + u] * stride + c);
+  using R = Ring<G, W, N, DENSE>;
+  if constexpr (R::kUsed) {
+    extern __shared__ uint4 ring_memory[];
+    const R ring = {reinterpret_cast<char*>(ring_memory)};
+    constexpr int A = R::kAhead;
+    uint32_t ahead = key_at(a0); // key of the next position to copy
+    auto copy = [&](uint32_t i, int slot) {
+      if (i < a1) {
+        const uint32_t key = ahead;
+        ahead = key_at(i + 1);
+        if (key < m.vocab) {
+          copy_async<R::kGrad>(ring.grad(slot), grad + (int64_t)m.at[i] * stride);
+          if constexpr (!DENSE)
+            if (ahead != key)
+              copy_async<R::kRow>(ring.row(slot), out + (int64_t)key * m.width);
+        }
+      }
+      commit_copies(); // a group for every position, empty past the end
+    };
+    for (int u = 0; u < A; ++u)
+      copy(a0 + u, u);
+    uint32_t key = key_at(a0);
+    int slot = 0;
+    for (uint32_t i = a0; i < a1; ++i) {
+      const uint32_t next = key_at(i + 1);
+      wait_for_copies<A - 1>();
+      if (key < m.vocab) {
+        Vec<W, N> was = {};
+        if constexpr (!DENSE)
+          was = load<W, N>(reinterpret_cast<const W*>(ring.row(slot)));
+        take(key, next, load<G, N>(reinterpret_cast<const G*>(ring.grad(slot))), was);
+      }
+      copy(i + A, slot);
+      slot = slot + 1 == A ? 0 : slot + 1;
+      key = next;
     }
+  } else {
+    constexpr int U = 8;
+    for (uint32_t i = a0; i < a1; i += U) {
+      uint32_t key[U + 1]; // vocab: none
+      Vec<G, N> v[U];
+      Vec<W, N> was[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (key[u] >= m.vocab)
-        continue;
-      if (DENSE) {
-        for (; row < key[u]; ++row)
-          finish_row();
-      } else if (row != key[u]) {
-        finish_row();
-        row = key[u];
+      for (int u = 0; u <= U; ++u)
+        key[u] = key_at(i + u);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (i + u < a1 && key[u] < m.vocab)
+          v[u] = load<G, N>(grad + (int64_t)m.at[i + u] * stride);
+        if (!DENSE && i + u < a1 && key[u] < m.vocab && key[u + 1] != key[u])
+          was[u] = load<W, N>(out + (int64_t)key[u] * m.width);
       }
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        acc[e] += v[u].f32(e);
-      any = true;
+      for (int u = 0; u < U; ++u)
+        if (i + u < a1 && key[u] < m.vocab)
+          take(key[u], key[u + 1], v[u], was[u]);
     }
   }
-  if (DENSE) {
-    for (; row < r1; ++row)
-      finish_row();
-  } else if (any && !(a1 < m.n && m.keys[a1] == row)) {
-    finish_row();
-  }
-  if (any) {
+  if (DENSE)
+    clear_to((uint32_t)(d[1] - a1));
+  if (carry_row >= 0)
     store_f32<float, N>(m.carry + (int64_t)p * m.width + c, acc);
-    carry_row = (int32_t)row;
-  }
   if (c == 0) {
     m.head_row[p] = head_row;
     m.carry_row[p] = carry_row;
@@ -272,16 +324,18 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
 
 // A row that began in shares before p and ended in p: the parts that those
 // left, in their order, and p's own. A block serves one share and kJoinCols
-// columns. A frequent token leaves its row's parts in many shares; from
-// kJoinSplit parts on the block's warps sum a run of them each, and the runs'
-// sums are added in order.
+// columns, a thread four of them. The row of a frequent token has parts in
+// many shares: from kJoinSplit on, each warp sums a run of them over all the
+// block's columns, and the runs' sums are added in order.
 constexpr int kJoinCols = kThreads * 4;
-constexpr uint32_t kJoinSplit = 16;
+constexpr uint32_t kJoinSplit = 48;
 
 template <class W, int N, bool DENSE>
 __global__ void __launch_bounds__(kThreads) join_kernel(Merge m, W* out)
 {
-  __shared__ float part[kThreads / 32][32 * N];
+  constexpr int kWarps = kThreads / 32;
+  constexpr int kTiles = kJoinCols / (32 * N); // a warp's accesses for the block's columns
+  __shared__ float part[kWarps][kJoinCols];
   wait_for_previous();
   allow_next();
   const uint32_t p = blockIdx.x;
@@ -296,62 +350,69 @@ __global__ void __launch_bounds__(kThreads) join_kernel(Merge m, W* out)
     more = n > 31;
     first -= more ? 32 : n;
   }
-
-  auto sum = [&](uint32_t q, uint32_t end, int64_t c, float (&acc)[N]) {
-#pragma unroll 4
-    for (; q < end; ++q) {
-      const Vec<float, N> v = load<float, N>(m.carry + (int64_t)q * m.width + c);
-#pragma unroll
-      for (int e = 0; e < N; ++e)
-        acc[e] += v.f32(e);
-    }
-  };
-  auto write = [&](int64_t c, const float (&acc)[N]) {
-    const Vec<float, N> v = load<float, N>(m.head + (int64_t)p * m.width + c);
-    W* to = out + (int64_t)row * m.width + c;
+  const int64_t c0 = (int64_t)blockIdx.y * kJoinCols;
+  const int cols = (int)min((int64_t)kJoinCols, m.width - c0);
+  const float* carry = m.carry + c0;
+  auto write = [&](int c, const float (&sum)[N]) {
+    const Vec<float, N> v = load<float, N>(m.head + (int64_t)p * m.width + c0 + c);
+    W* to = out + (int64_t)row * m.width + c0 + c;
+    Vec<W, N> was = {};
+    if constexpr (!DENSE)
+      was = load<W, N>(to);
     float y[N];
 #pragma unroll
     for (int e = 0; e < N; ++e)
-      y[e] = m.scale * (acc[e] + v.f32(e));
-    if constexpr (!DENSE) {
-      const Vec<W, N> was = load<W, N>(to);
-#pragma unroll
-      for (int e = 0; e < N; ++e)
-        y[e] += was.f32(e);
-    }
+      y[e] = DENSE ? m.scale * (sum[e] + v.f32(e)) : fmaf(m.scale, sum[e] + v.f32(e), was.f32(e));
     store_f32<W, N>(to, y);
   };
 
-  const int64_t c0 = (int64_t)blockIdx.y * kJoinCols, c1 = min(m.width, c0 + kJoinCols);
   const uint32_t parts = p - first;
   if (parts < kJoinSplit) {
-    for (int64_t c = c0 + (int64_t)threadIdx.x * N; c < c1; c += (int64_t)kThreads * N) {
-      float acc[N] = {};
-      sum(first, p, c, acc);
-      write(c, acc);
+    for (int c = threadIdx.x * N; c < cols; c += kThreads * N) {
+      float sum[N] = {};
+#pragma unroll 8
+      for (uint32_t q = first; q < p; ++q) {
+        const Vec<float, N> v = load<float, N>(carry + (int64_t)q * m.width + c);
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          sum[e] += v.f32(e);
+      }
+      write(c, sum);
     }
     return;
   }
-  constexpr uint32_t kWarps = kThreads / 32;
   const uint32_t q0 = first + (uint32_t)((uint64_t)parts * warp / kWarps);
   const uint32_t q1 = first + (uint32_t)((uint64_t)parts * (warp + 1) / kWarps);
-  for (int64_t t = c0; t < c1; t += 32 * N) {
-    const int64_t c = t + lane * N;
-    float acc[N] = {};
-    if (c < c1)
-      sum(q0, q1, c, acc);
+  constexpr int kAtOnce = kTiles < 8 ? kTiles : 8;
+  for (int t0 = 0; t0 < kTiles; t0 += kAtOnce) {
+    float sum[kAtOnce][N] = {};
+#pragma unroll 2
+    for (uint32_t q = q0; q < q1; ++q) {
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-      part[warp][lane * N + e] = acc[e];
-    __syncthreads();
-    if (warp == 0 && c < c1) {
-      for (uint32_t w = 1; w < kWarps; ++w)
+      for (int t = 0; t < kAtOnce; ++t) {
+        const int c = ((t0 + t) * 32 + lane) * N;
+        if (c < cols) {
+          const Vec<float, N> v = load<float, N>(carry + (int64_t)q * m.width + c);
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-          acc[e] += part[w][lane * N + e];
-      write(c, acc);
+          for (int e = 0; e < N; ++e)
+            sum[t][e] += v.f32(e);
+        }
+      }
     }
-    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < kAtOnce; ++t)
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        part[warp][((t0 + t) * 32 + lane) * N + e] = sum[t][e];
+  }
+  __syncthreads();
+  for (int c = threadIdx.x * N; c < cols; c += kThreads * N) {
+    float sum[N] = {};
+    for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        sum[e] += part[w][c + e];
+    write(c, sum);
   }
 }
 
@@ -359,18 +420,20 @@ __global__ void __launch_bounds__(kThreads) join_kernel(Merge m, W* out)
 // Host
 // ---------------------------------------------------------------------------
 struct Layout {
-  int passes, digit_bits;
-  Tiling tiles;
-  uint32_t most_shares; // of any call with these sizes
-  size_t pairs, counts, parts, rows, total; // bytes of each piece
+  SortPlan sort;
+  uint32_t most_shares;                         // of any call with these sizes
+  size_t sorted, pairs, counts, parts, rows, total; // bytes of each piece
 };
 
-// Shares of the merge: at most twice as many groups as are resident, of 16
-// steps at least (a share costs a search and up to two parts of rows).
-uint32_t shares_of(int64_t steps, int64_t width)
+// Shares of the merge where a row takes row_threads threads: as many groups as
+// are resident, or a multiple of that where every share then still has 32
+// steps (each costs a search and up to two parts of rows), so that the last
+// wave of blocks is a full one; never less than eight steps a share.
+uint32_t shares_of(int64_t steps, int64_t row_threads)
 {
-  const int64_t most = 2 * (int64_t)kSms * 2048 / std::max<int64_t>(1, std::min<int64_t>((width + 7) / 8, 2048));
-  return (uint32_t)std::max<int64_t>(1, std::min<int64_t>(most, (steps + 15) / 16));
+  const int64_t resident = std::max<int64_t>(1, kSms * 1024 / std::max<int64_t>(1, row_threads));
+  const int64_t waves = std::min<int64_t>(6, std::max<int64_t>(1, steps / (32 * resident)));
+  return (uint32_t)std::max<int64_t>(1, std::min<int64_t>(resident * waves, (steps + 7) / 8));
 }
 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -381,15 +444,15 @@ Layout layout_of(int64_t n, int64_t vocab, int64_t width)
   int bits = 1;
   while ((vocab >> bits) != 0) // keys are 0 .. vocab
     ++bits;
-  l.passes = (bits + kDigitBits - 1) / kDigitBits;
-  l.digit_bits = (bits + l.passes - 1) / l.passes;
-  l.tiles = tiling(n);
-  l.most_shares = shares_of(n + vocab, width);
-  l.pairs = round_up((size_t)n * 4);
-  l.counts = round_up(count_bytes(l.tiles, 1 << l.digit_bits));
+  const int passes = (bits + kDigitBits - 1) / kDigitBits, digit_bits = (bits + passes - 1) / passes;
+  l.sort = sort_plan(n, passes, digit_bits, 1 << digit_bits);
+  l.most_shares = shares_of(n + vocab, (width + 7) / 8); // eight columns a thread: the fewest threads
+  l.sorted = round_up((size_t)n * 4);
+  l.pairs = round_up(l.sort.pairs());
+  l.counts = round_up(l.sort.counts());
   l.parts = round_up((size_t)l.most_shares * (size_t)width * 4);
   l.rows = round_up((size_t)l.most_shares * 4);
-  l.total = 4 * l.pairs + l.counts + 2 * l.parts + 2 * l.rows;
+  l.total = 2 * l.sorted + 2 * l.pairs + l.counts + 2 * l.parts + 2 * l.rows;
   return l;
 }
 
@@ -404,8 +467,8 @@ bool fits(int64_t n, int64_t vocab, int64_t width)
 cudaError_t read_embedding_error(uint32_t* word)
 {
   const uint32_t zero = 0;
-  const cudaError_t e = cudaMemcpyFromSymbol(word, g_error, sizeof(zero));
-  return e != cudaSuccess ? e : cudaMemcpyToSymbol(g_error, &zero, sizeof(zero));
+  const cudaError_t e = cudaMemcpyFromSymbol(word, g_device_error, sizeof(zero));
+  return e != cudaSuccess ? e : cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero));
 }
 
 } // namespace segtopk
@@ -478,7 +541,7 @@ extern "C" int segtopk_embedding_backward(segtopk_dtype dtype, const void* grad_
     return with_float_type(table_dtype, [&](auto zero_out) {
       using G = decltype(zero_in);
       using W = decltype(zero_out);
-      constexpr int N = 16 / (int)sizeof(G);
+      constexpr int N = 16 / (int)std::max(sizeof(G), sizeof(W)); // no access above 16 bytes
       if (width == 0 || (accumulate && num_tokens == 0))
         return (int)SEGTOPK_SUCCESS;
       if ((num_tokens > 0 && (!grad_out || !tokens)) || !grad_table)
@@ -499,53 +562,46 @@ extern "C" int segtopk_embedding_backward(segtopk_dtype dtype, const void* grad_
         w += bytes;
         return at;
       };
-      uint32_t* keys[2] = {(uint32_t*)piece(l.pairs), (uint32_t*)piece(l.pairs)};
-      uint32_t* at[2] = {(uint32_t*)piece(l.pairs), (uint32_t*)piece(l.pairs)};
+      uint32_t* keys = (uint32_t*)piece(l.sorted);
+      uint32_t* at = (uint32_t*)piece(l.sorted);
+      uint32_t* const pairs[2] = {(uint32_t*)piece(l.pairs), (uint32_t*)piece(l.pairs)};
       uint32_t* counts = (uint32_t*)piece(l.counts);
       cudaStream_t st = (cudaStream_t)stream;
       cudaError_t e = cudaSuccess;
-      int launches = 0, to = 0;
       const uint32_t n = (uint32_t)num_tokens;
-      const int bins = 1 << l.digit_bits;
-      for (int pass = 0; pass < l.passes && n > 0; ++pass) {
-        const PairSink sink = {keys[to], at[to]};
-        int made;
-        if (pass > 0)
-          made = rank_pass(PairSource{keys[1 - to], at[1 - to], pass * l.digit_bits, (uint32_t)bins - 1}, sink, n,
-                           l.tiles, bins, counts, st, &e);
-        else if (token_bytes == 4)
-          made = rank_pass(TokenSource<int32_t>{(const int32_t*)tokens, vocab, padding_token, (uint32_t)bins - 1},
-                           sink, n, l.tiles, bins, counts, st, &e);
-        else
-          made = rank_pass(TokenSource<int64_t>{(const int64_t*)tokens, vocab, padding_token, (uint32_t)bins - 1},
-                           sink, n, l.tiles, bins, counts, st, &e);
-        if (made < 0)
+      int launches = 0;
+      if (n > 0) {
+        auto by = [&](auto id) {
+          using I = decltype(id);
+          return sort<false>(l.sort, TokenSource<I>{(const I*)tokens, vocab, padding_token}, PairSink{keys, at}, pairs, counts,
+                      st, &e);
+        };
+        launches = token_bytes == 4 ? by(int32_t{}) : by(int64_t{});
+        if (launches < 0)
           return record_cuda_error(e);
-        launches += made;
-        to = 1 - to;
       }
       auto go = [&](auto nv, auto all) {
         constexpr int V = decltype(nv)::value;
         constexpr bool DENSE = decltype(all)::value;
         Merge m = {};
-        m.keys = keys[1 - to];
-        m.at = at[1 - to];
+        m.keys = keys;
+        m.at = at;
         m.n = n;
         m.vocab = (uint32_t)vocab;
         m.width = width;
         // no share without a step: a row's shares have to be neighbours
-        m.shares = shares_of((int64_t)n + (DENSE ? vocab : 0), width);
         m.lanes = lanes_for(width / V, kThreads);
+        const int64_t cols = (int64_t)m.lanes * V, tiles = (width + cols - 1) / cols;
+        m.shares = std::min(l.most_shares, shares_of((int64_t)n + (DENSE ? vocab : 0), m.lanes * tiles));
         m.scale = scale;
         m.head = (float*)piece(l.parts);
         m.carry = (float*)piece(l.parts);
         m.head_row = (int32_t*)piece(l.rows);
         m.carry_row = (int32_t*)piece(l.rows);
         const uint32_t per_block = (uint32_t)(kThreads / m.lanes);
-        const int64_t cols = (int64_t)m.lanes * V;
-        const dim3 grid((m.shares + per_block - 1) / per_block, (unsigned)((width + cols - 1) / cols));
-        e = launch(merge_kernel<G, W, V, DENSE>, grid, kThreads, 0, st, m, (const G*)grad_out, grad_stride,
-                   (W*)grad_table);
+        const dim3 grid((m.shares + per_block - 1) / per_block, (unsigned)tiles);
+        e = launch(merge_kernel<G, W, V, DENSE>, grid, kThreads, Ring<G, W, V, DENSE>::kBytes, st, m,
+                   (const G*)grad_out, grad_stride, (W*)grad_table);
         constexpr int J = V > 4 ? 4 : V; // columns of a thread: 16 bytes of the parts
         const dim3 joins(m.shares, (unsigned)((width + kJoinCols - 1) / kJoinCols));
         if (e == cudaSuccess)

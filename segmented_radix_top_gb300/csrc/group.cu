@@ -7,23 +7,18 @@ namespace segtopk {
 namespace {
 using namespace rows;
 
-__device__ uint32_t g_error;
-
 template <class I>
 struct SlotSource {
   const I* ids;
   int experts;
-  struct Item {
-    uint32_t digit;
-  };
-  __device__ __forceinline__ uint32_t digit(uint32_t i) const
+  __device__ __forceinline__ uint32_t key(uint32_t i) const
   {
-    const I e = *(ids + i);
+    const I e = ids[i];
     if (e >= (I)experts)
-      atomicOr(&g_error, (uint32_t)SEGTOPK_DEVICE_ERROR_INDEX);
+      raise_error(SEGTOPK_DEVICE_ERROR_INDEX);
     return e >= 0 && e < (I)experts ? (uint32_t)e : (uint32_t)experts;
   }
-  __device__ __forceinline__ Item load(uint32_t i) const { return {digit(i)}; }
+  __device__ __forceinline__ uint32_t at(uint32_t i) const { return i; }
 };
 
 struct SlotSink {
@@ -31,23 +26,24 @@ struct SlotSink {
   int64_t* offsets;
   int32_t* row_of_slot;
   int32_t* slot_of_row;
-  template <class Item>
-  __device__ __forceinline__ void put(uint32_t i, Item item, uint32_t place) const
+  __device__ __forceinline__ void put(uint32_t key, uint32_t at, uint32_t place) const
   {
-    const bool some = item.digit < (uint32_t)experts;
-    row_of_slot[i] = some ? (int32_t)place : -1;
-    slot_of_row[place] = some ? (int32_t)i : -1;
+    const bool some = key < (uint32_t)experts;
+    row_of_slot[at] = some ? (int32_t)place : -1;
+    slot_of_row[place] = some ? (int32_t)at : -1;
   }
   __device__ __forceinline__ void start(int d, uint32_t first) const { offsets[d] = first; }
 };
+
+SortPlan plan_of(int64_t slots, int32_t experts) { return sort_plan(slots, 1, 0, experts + 1); }
 
 } // namespace
 
 cudaError_t read_group_error(uint32_t* word)
 {
   const uint32_t zero = 0;
-  const cudaError_t e = cudaMemcpyFromSymbol(word, g_error, sizeof(zero));
-  return e != cudaSuccess ? e : cudaMemcpyToSymbol(g_error, &zero, sizeof(zero));
+  const cudaError_t e = cudaMemcpyFromSymbol(word, g_device_error, sizeof(zero));
+  return e != cudaSuccess ? e : cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero));
 }
 
 } // namespace segtopk
@@ -58,7 +54,7 @@ extern "C" size_t segtopk_group_workspace_bytes(int64_t slots, int32_t experts)
 {
   if (slots <= 0 || slots > 2147483647LL || experts < 1 || experts > SEGTOPK_MAX_EXPERTS)
     return 0;
-  return count_bytes(tiling(slots), experts + 1);
+  return plan_of(slots, experts).counts();
 }
 
 extern "C" int segtopk_group(const void* expert_ids, int32_t id_bytes, int64_t slots, int32_t experts,
@@ -86,8 +82,8 @@ extern "C" int segtopk_group(const void* expert_ids, int32_t id_bytes, int64_t s
   auto pass = [&](auto zero) {
     using I = decltype(zero);
     cudaError_t e = cudaSuccess;
-    const int launches = rank_pass(SlotSource<I>{(const I*)expert_ids, experts}, sink, (uint32_t)slots, tiling(slots),
-                                   experts + 1, (uint32_t*)workspace, (cudaStream_t)stream, &e);
+    const int launches = sort<true>(plan_of(slots, experts), SlotSource<I>{(const I*)expert_ids, experts}, sink,
+                              {nullptr, nullptr}, (uint32_t*)workspace, (cudaStream_t)stream, &e);
     return finish(e, launches);
   };
   return id_bytes == 4 ? pass(int32_t{}) : pass(int64_t{});

@@ -142,6 +142,19 @@ def test_sort_passes(vocab, passes):
     assert int((got != 0).any(1).sum()) == len(some)
 
 
+@pytest.mark.parametrize("n", [4096, 4097, 8193, 16385, 32769, 70000, 131072, 131073, 300001])
+@pytest.mark.parametrize("vocab", [300, 40000, 300000])
+def test_sort_sizes(n, vocab):
+    # every token's positions in order: a column of ones counts them, one of
+    # whole numbers below 2^24 in all adds them exactly in 32 bits
+    t = tokens_of("frequent", n, vocab, seed=n).int().cuda()
+    g = torch.ones(n, 4, device="cuda")
+    g[:, 1] = torch.arange(n, device="cuda") % 37
+    got = st.embedding_backward(g, t, vocab)
+    want = torch.zeros(vocab, 4, dtype=torch.float64, device="cuda").index_add_(0, t, g.double())
+    assert torch.equal(got.double(), want)
+
+
 def test_padding_token():
     tokens = tokens_of("frequent", 3000, 90)
     for padding in (0, 89, -1, 45):

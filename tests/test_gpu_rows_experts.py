@@ -43,6 +43,24 @@ def test_group(tokens, k, experts, dropped, dtype):
     grouped(ids_of(tokens, k, experts, tokens, dropped, dtype), experts)
 
 
+@pytest.mark.parametrize("slots", [4096, 4097, 8193, 16385, 32768, 32769, 99999, 131072, 131073])
+@pytest.mark.parametrize("experts", [1, 100, 1024])
+def test_group_sizes(slots, experts):
+    # against torch's stable sort
+    ids = torch.randint(-1, experts, (slots, 1), generator=torch.Generator().manual_seed(slots), dtype=torch.int32)
+    groups = st.group_by_expert(ids.cuda(), experts)
+    flat = ids.flatten().long()
+    key = torch.where(flat < 0, experts, flat)
+    order, kept = torch.argsort(key, stable=True), int((flat >= 0).sum())
+    assert torch.equal(groups.slot_of_row.cpu()[:kept].long(), order[:kept])
+    assert (groups.slot_of_row[kept:] == -1).all()
+    rows = torch.full_like(flat, -1)
+    rows[order[:kept]] = torch.arange(kept)
+    assert torch.equal(groups.row_of_slot.cpu().flatten().long(), rows)
+    counts = torch.bincount(key, minlength=experts + 1)[:experts]
+    assert torch.equal(groups.offsets.cpu(), torch.cat([torch.zeros(1, dtype=torch.long), counts.cumsum(0)]))
+
+
 def test_group_with_one_expert_for_all():
     for tokens in (33, 5000):
         grouped(torch.full((tokens, 2), 6, dtype=torch.int32), 7)
