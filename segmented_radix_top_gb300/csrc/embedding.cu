@@ -84,11 +84,75 @@ struct TokenSource {
   __device__ __forceinline__ uint32_t at(uint32_t i) const { return i; }
 };
 
+// Few tokens are placed by counting instead: an item's place is the number of
+// items before it by (key, position). A block places 32 of them, each warp
+// counting over an eighth of all; n^2 comparisons over the whole GPU, about
+// 5 us at kFewTokens, where the cluster sort takes 9. The blocks past those
+// clear the table meanwhile, where most of its rows have no token.
+constexpr int64_t kFewTokens = 8192;
+
+template <class I>
+__global__ void __launch_bounds__(kThreads)
+place_kernel(TokenSource<I> src, uint32_t n, uint32_t place_blocks, uint64_t* items, char* clear, size_t clear_bytes)
+{
+  extern __shared__ uint4 place_keys[];
+  __shared__ uint32_t part[kThreads / 32][32];
+  wait_for_previous();
+  allow_next();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x >= place_blocks) {
+    const size_t first = (size_t)(blockIdx.x - place_blocks) * kThreads + threadIdx.x;
+    const size_t step = (size_t)(gridDim.x - place_blocks) * kThreads;
+    if ((((size_t)clear | clear_bytes) & 15) == 0) {
+#pragma unroll 4
+      for (size_t i = first; i < clear_bytes / 16; i += step)
+        reinterpret_cast<uint4*>(clear)[i] = uint4{};
+    } else {
+#pragma unroll 4
+      for (size_t i = first; i < clear_bytes / 2; i += step)
+        reinterpret_cast<uint16_t*>(clear)[i] = 0;
+    }
+    return;
+  }
+  uint32_t* keys = reinterpret_cast<uint32_t*>(place_keys);
+  const uint32_t groups = (n + 31) / 32;
+#pragma unroll 4
+  for (uint32_t i = threadIdx.x; i < groups * 32; i += kThreads)
+    keys[i] = i < n ? src.key(i) : ~0u; // past every item
+  __syncthreads();
+  const uint32_t i = blockIdx.x * 32 + lane, key = keys[i];
+  uint32_t before = 0;
+  // items of earlier positions count with an equal key, later ones do not
+  auto count = [&](uint32_t g, auto earlier) {
+    const uint4* at = place_keys + g * 8;
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      const uint4 k = at[v];
+      before += earlier(k.x, v * 4) + earlier(k.y, v * 4 + 1) + earlier(k.z, v * 4 + 2) + earlier(k.w, v * 4 + 3);
+    }
+  };
+  const uint32_t g0 = groups * warp / 8, g1 = groups * (warp + 1) / 8, own = blockIdx.x;
+  for (uint32_t g = g0; g < min(g1, own); ++g)
+    count(g, [&](uint32_t k, int) { return k <= key; });
+  if (own >= g0 && own < g1)
+    count(own, [&](uint32_t k, int j) { return k < key || (k == key && j < lane); });
+  for (uint32_t g = max(g0, own + 1); g < g1; ++g)
+    count(g, [&](uint32_t k, int) { return k < key; });
+  part[warp][lane] = before;
+  __syncthreads();
+  if (warp > 0 || i >= n)
+    return;
+#pragma unroll
+  for (int w = 1; w < kThreads / 32; ++w)
+    before += part[w][lane];
+  items[before] = pack(key, i);
+}
+
 // ---------------------------------------------------------------------------
 // Backward: merge of sorted positions and table rows
 // ---------------------------------------------------------------------------
 struct Merge {
-  const uint32_t *keys, *at; // sorted
+  const uint64_t* items; // sorted
   uint32_t n;
   uint32_t vocab;
   int64_t width;
@@ -97,10 +161,19 @@ struct Merge {
   float scale;
   float *head, *carry;          // [shares][width]: parts of rows that several shares hold
   int32_t *head_row, *carry_row; // [shares]: their rows, or -1
+  __device__ __forceinline__ uint32_t key(uint32_t i) const { return (uint32_t)items[i]; }
+  __device__ __forceinline__ int64_t at(uint32_t i) const { return (int64_t)(items[i] >> 32); }
+};
+
+// What becomes of the table:
+enum Mode {
+  kDense, // all rows are written, those without tokens as zeros; a share is a part of the positions and rows together
+  kAdd,   // the tokens' rows are added to; a share is a part of the positions
+  kWrite  // the tokens' rows are written, the others hold zeros already; shares as for kAdd
 };
 
 // The number of positions among the first d[i] steps of the merge, in which
-// position a comes before the end of row r if keys[a] <= r, for both ends of
+// position a comes before the end of row r if its key is at most r, for both ends of
 // a share. The group's lanes (those of a warp at most) try as many places a
 // round, so a search takes two or three dependent loads instead of a dozen.
 __device__ __forceinline__ void positions_before(const Merge& m, const uint64_t (&d)[2], uint32_t (&a)[2])
@@ -121,7 +194,7 @@ __device__ __forceinline__ void positions_before(const Merge& m, const uint64_t 
       const uint32_t span = hi[i] - lo[i];
       // `mine`-th of g places, all different while there are so many
       at[i] = lo[i] + (span <= g ? mine : (uint32_t)((uint64_t)span * (mine + 1) / (g + 1)));
-      less[i] = at[i] < hi[i] && (uint64_t)m.keys[at[i]] + at[i] < d[i];
+      less[i] = at[i] < hi[i] && (uint64_t)m.key(at[i]) + at[i] < d[i];
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -142,10 +215,6 @@ __device__ __forceinline__ void positions_before(const Merge& m, const uint64_t 
   a[1] = lo[1];
 }
 
-// DENSE: every row of the table is written, rows without tokens as zeros, and
-// a share is a part of the positions and rows together. Otherwise only the
-// tokens' rows are added to, and a share is a part of the positions.
-//
 // A row is written by the share that holds its last position; if that share
 // does not hold the row's first one too, its part goes to `head`, and the
 // parts of the shares before it to their `carry`.
@@ -157,10 +226,10 @@ __device__ __forceinline__ void positions_before(const Merge& m, const uint64_t 
 // thread reads another's part, no barrier. Elements too badly aligned for
 // that (N = 1) go in batches of eight through registers.
 constexpr int kRingBytes = 48 << 10; // of a block; four blocks an SM
-template <class G, class W, int N, bool DENSE>
+template <class G, class W, int N, Mode MODE>
 struct Ring {
   static constexpr bool kUsed = N > 1;
-  static constexpr int kGrad = N * (int)sizeof(G), kRow = DENSE ? 0 : N * (int)sizeof(W); // bytes of a position
+  static constexpr int kGrad = N * (int)sizeof(G), kRow = MODE == kAdd ? N * (int)sizeof(W) : 0; // bytes of a position
   static constexpr int kFit = kRingBytes / (kThreads * (kGrad + kRow));
   static constexpr int kAhead = kFit < 16 ? kFit : 16;
   static constexpr int kBytes = kUsed ? kAhead * kThreads * (kGrad + kRow) : 0;
@@ -187,7 +256,7 @@ __device__ __forceinline__ void wait_for_copies() // all but the last N groups
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <class G, class W, int N, bool DENSE>
+template <class G, class W, int N, Mode MODE>
 __global__ void __launch_bounds__(kThreads, 4)
 merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
 {
@@ -198,19 +267,19 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
   const int64_t c = ((int64_t)blockIdx.y * m.lanes + lane) * N;
   if (p >= m.shares)
     return;
-  const uint64_t steps = (uint64_t)m.n + (DENSE ? m.vocab : 0);
+  const uint64_t steps = (uint64_t)m.n + (MODE == kDense ? m.vocab : 0);
   const uint64_t d[2] = {steps * p / m.shares, steps * (p + 1) / m.shares};
   uint32_t a[2] = {(uint32_t)d[0], (uint32_t)d[1]};
-  if (DENSE)
+  if (MODE == kDense)
     positions_before(m, d, a);
   if (c >= m.width)
     return;
   out += c;
   const uint32_t a0 = a[0], a1 = a[1];
-  const uint32_t before = a0 > 0 ? m.keys[a0 - 1] : m.vocab;
-  bool begun = a0 < a1 && m.keys[a0] == before; // the first position's row, by an earlier share
-  uint32_t empty = 0;                           // DENSE: the next row that may have no position
-  if (DENSE) {
+  const uint32_t before = a0 > 0 ? m.key(a0 - 1) : m.vocab;
+  bool begun = a0 < a1 && m.key(a0) == before; // the first position's row, by an earlier share
+  uint32_t empty = 0;                           // kDense: the next row that may have no position
+  if (MODE == kDense) {
     empty = (uint32_t)(d[0] - a0);
     empty += empty == before;
   }
@@ -228,7 +297,7 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
   // one position: its key, the next one's, its gradient, and the row it adds
   // to if the keys differ
   auto take = [&](uint32_t key, uint32_t next, const Vec<G, N>& v, const Vec<W, N>& was) {
-    if (DENSE)
+    if (MODE == kDense)
       clear_to(key);
 #pragma unroll
     for (int e = 0; e < N; ++e)
@@ -242,7 +311,7 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
     } else {
 #pragma unroll
       for (int e = 0; e < N; ++e)
-        acc[e] = DENSE ? m.scale * acc[e] : fmaf(m.scale, acc[e], was.f32(e));
+        acc[e] = MODE == kAdd ? fmaf(m.scale, acc[e], was.f32(e)) : m.scale * acc[e];
       store_f32<W, N>(out + (int64_t)key * m.width, acc);
     }
     begun = false;
@@ -251,10 +320,10 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
     for (int e = 0; e < N; ++e)
       acc[e] = 0;
   };
-  auto key_at = [&](uint32_t i) { return i < m.n ? m.keys[i] : m.vocab; };
+  auto key_at = [&](uint32_t i) { return i < m.n ? m.key(i) : m.vocab; };
   grad += c;
 
-  using R = Ring<G, W, N, DENSE>;
+  using R = Ring<G, W, N, MODE>;
   if constexpr (R::kUsed) {
     extern __shared__ uint4 ring_memory[];
     const R ring = {reinterpret_cast<char*>(ring_memory)};
@@ -265,8 +334,8 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
         const uint32_t key = ahead;
         ahead = key_at(i + 1);
         if (key < m.vocab) {
-          copy_async<R::kGrad>(ring.grad(slot), grad + (int64_t)m.at[i] * stride);
-          if constexpr (!DENSE)
+          copy_async<R::kGrad>(ring.grad(slot), grad + m.at(i) * stride);
+          if constexpr (MODE == kAdd)
             if (ahead != key)
               copy_async<R::kRow>(ring.row(slot), out + (int64_t)key * m.width);
         }
@@ -282,7 +351,7 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
       wait_for_copies<A - 1>();
       if (key < m.vocab) {
         Vec<W, N> was = {};
-        if constexpr (!DENSE)
+        if constexpr (MODE == kAdd)
           was = load<W, N>(reinterpret_cast<const W*>(ring.row(slot)));
         take(key, next, load<G, N>(reinterpret_cast<const G*>(ring.grad(slot))), was);
       }
@@ -302,8 +371,8 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (i + u < a1 && key[u] < m.vocab)
-          v[u] = load<G, N>(grad + (int64_t)m.at[i + u] * stride);
-        if (!DENSE && i + u < a1 && key[u] < m.vocab && key[u + 1] != key[u])
+          v[u] = load<G, N>(grad + m.at(i + u) * stride);
+        if (MODE == kAdd && i + u < a1 && key[u] < m.vocab && key[u + 1] != key[u])
           was[u] = load<W, N>(out + (int64_t)key[u] * m.width);
       }
 #pragma unroll
@@ -312,7 +381,7 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
           take(key[u], key[u + 1], v[u], was[u]);
     }
   }
-  if (DENSE)
+  if (MODE == kDense)
     clear_to((uint32_t)(d[1] - a1));
   if (carry_row >= 0)
     store_f32<float, N>(m.carry + (int64_t)p * m.width + c, acc);
@@ -330,7 +399,7 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
 constexpr int kJoinCols = kThreads * 4;
 constexpr uint32_t kJoinSplit = 48;
 
-template <class W, int N, bool DENSE>
+template <class W, int N, Mode MODE>
 __global__ void __launch_bounds__(kThreads) join_kernel(Merge m, W* out)
 {
   constexpr int kWarps = kThreads / 32;
@@ -357,12 +426,12 @@ __global__ void __launch_bounds__(kThreads) join_kernel(Merge m, W* out)
     const Vec<float, N> v = load<float, N>(m.head + (int64_t)p * m.width + c0 + c);
     W* to = out + (int64_t)row * m.width + c0 + c;
     Vec<W, N> was = {};
-    if constexpr (!DENSE)
+    if constexpr (MODE == kAdd)
       was = load<W, N>(to);
     float y[N];
 #pragma unroll
     for (int e = 0; e < N; ++e)
-      y[e] = DENSE ? m.scale * (sum[e] + v.f32(e)) : fmaf(m.scale, sum[e] + v.f32(e), was.f32(e));
+      y[e] = MODE == kAdd ? fmaf(m.scale, sum[e] + v.f32(e), was.f32(e)) : m.scale * (sum[e] + v.f32(e));
     store_f32<W, N>(to, y);
   };
 
@@ -421,8 +490,9 @@ __global__ void __launch_bounds__(kThreads) join_kernel(Merge m, W* out)
 // ---------------------------------------------------------------------------
 struct Layout {
   SortPlan sort;
+  bool few; // placed by counting, not sorted
   uint32_t most_shares;                         // of any call with these sizes
-  size_t sorted, pairs, counts, parts, rows, total; // bytes of each piece
+  size_t items, copy, counts, parts, rows, total; // bytes of each piece
 };
 
 // Shares of the merge where a row takes row_threads threads: as many groups as
@@ -447,12 +517,13 @@ Layout layout_of(int64_t n, int64_t vocab, int64_t width)
   const int passes = (bits + kDigitBits - 1) / kDigitBits, digit_bits = (bits + passes - 1) / passes;
   l.sort = sort_plan(n, passes, digit_bits, 1 << digit_bits);
   l.most_shares = shares_of(n + vocab, (width + 7) / 8); // eight columns a thread: the fewest threads
-  l.sorted = round_up((size_t)n * 4);
-  l.pairs = round_up(l.sort.pairs());
+  l.few = n <= kFewTokens;
+  l.items = round_up((size_t)n * 8);
+  l.copy = round_up(l.sort.copy());
   l.counts = round_up(l.sort.counts());
   l.parts = round_up((size_t)l.most_shares * (size_t)width * 4);
   l.rows = round_up((size_t)l.most_shares * 4);
-  l.total = 2 * l.sorted + 2 * l.pairs + l.counts + 2 * l.parts + 2 * l.rows;
+  l.total = l.items + 2 * l.copy + l.counts + 2 * l.parts + 2 * l.rows;
   return l;
 }
 
@@ -562,37 +633,48 @@ extern "C" int segtopk_embedding_backward(segtopk_dtype dtype, const void* grad_
         w += bytes;
         return at;
       };
-      uint32_t* keys = (uint32_t*)piece(l.sorted);
-      uint32_t* at = (uint32_t*)piece(l.sorted);
-      uint32_t* const pairs[2] = {(uint32_t*)piece(l.pairs), (uint32_t*)piece(l.pairs)};
+      uint64_t* items = (uint64_t*)piece(l.items);
+      uint64_t* const copies[2] = {(uint64_t*)piece(l.copy), (uint64_t*)piece(l.copy)};
       uint32_t* counts = (uint32_t*)piece(l.counts);
       cudaStream_t st = (cudaStream_t)stream;
       cudaError_t e = cudaSuccess;
       const uint32_t n = (uint32_t)num_tokens;
+      // Clearing the table beside the placing and then writing the tokens'
+      // rows writes those twice: worth it where they are few of all. 2048 of
+      // 32000 rows of 4 KB: 41.7 us the dense way.
+      const bool clear_first = !accumulate && l.few && num_tokens <= vocab / 4;
       int launches = 0;
-      if (n > 0) {
+      if (n > 0 || clear_first) {
         auto by = [&](auto id) {
           using I = decltype(id);
-          return sort<false>(l.sort, TokenSource<I>{(const I*)tokens, vocab, padding_token}, PairSink{keys, at}, pairs, counts,
-                      st, &e);
+          const TokenSource<I> src = {(const I*)tokens, vocab, padding_token};
+          if (!l.few)
+            return sort<false>(l.sort, src, ItemSink{items}, copies, counts, st, &e);
+          const uint32_t places = (n + 31) / 32;
+          const size_t bytes = clear_first ? (size_t)vocab * (size_t)width * sizeof(W) : 0;
+          const uint32_t clears = (uint32_t)std::min<size_t>(4 * kSms, (bytes + (1 << 14) - 1) >> 14);
+          e = launch(place_kernel<I>, dim3(places + clears), kThreads, (size_t)places * 128, st, src, n, places, items,
+                     (char*)grad_table, bytes);
+          return e == cudaSuccess ? 1 : -1;
         };
         launches = token_bytes == 4 ? by(int32_t{}) : by(int64_t{});
         if (launches < 0)
           return record_cuda_error(e);
       }
-      auto go = [&](auto nv, auto all) {
+      if (clear_first && n == 0)
+        return finish(e, launches);
+      auto go = [&](auto nv, auto mode) {
         constexpr int V = decltype(nv)::value;
-        constexpr bool DENSE = decltype(all)::value;
+        constexpr Mode MODE = decltype(mode)::value;
         Merge m = {};
-        m.keys = keys;
-        m.at = at;
+        m.items = items;
         m.n = n;
         m.vocab = (uint32_t)vocab;
         m.width = width;
         // no share without a step: a row's shares have to be neighbours
         m.lanes = lanes_for(width / V, kThreads);
         const int64_t cols = (int64_t)m.lanes * V, tiles = (width + cols - 1) / cols;
-        m.shares = std::min(l.most_shares, shares_of((int64_t)n + (DENSE ? vocab : 0), m.lanes * tiles));
+        m.shares = std::min(l.most_shares, shares_of((int64_t)n + (MODE == kDense ? vocab : 0), m.lanes * tiles));
         m.scale = scale;
         m.head = (float*)piece(l.parts);
         m.carry = (float*)piece(l.parts);
@@ -600,21 +682,22 @@ extern "C" int segtopk_embedding_backward(segtopk_dtype dtype, const void* grad_
         m.carry_row = (int32_t*)piece(l.rows);
         const uint32_t per_block = (uint32_t)(kThreads / m.lanes);
         const dim3 grid((m.shares + per_block - 1) / per_block, (unsigned)tiles);
-        e = launch(merge_kernel<G, W, V, DENSE>, grid, kThreads, Ring<G, W, V, DENSE>::kBytes, st, m,
+        e = launch(merge_kernel<G, W, V, MODE>, grid, kThreads, Ring<G, W, V, MODE>::kBytes, st, m,
                    (const G*)grad_out, grad_stride, (W*)grad_table);
         constexpr int J = V > 4 ? 4 : V; // columns of a thread: 16 bytes of the parts
         const dim3 joins(m.shares, (unsigned)((width + kJoinCols - 1) / kJoinCols));
         if (e == cudaSuccess)
-          e = launch(join_kernel<W, J, DENSE>, joins, kThreads, 0, st, m, (W*)grad_table);
+          e = launch(join_kernel<W, J, MODE>, joins, kThreads, 0, st, m, (W*)grad_table);
         return finish(e, launches + 2);
       };
       const bool vector = rows_fit(grad_out, grad_stride, width, sizeof(G), N) &&
                           rows_fit(grad_table, width, width, sizeof(W), N);
       using One = std::integral_constant<int, 1>;
       using Many = std::integral_constant<int, N>;
+      auto by_mode = [&](auto mode) { return vector ? go(Many{}, mode) : go(One{}, mode); };
       if (accumulate)
-        return vector ? go(Many{}, std::false_type{}) : go(One{}, std::false_type{});
-      return vector ? go(Many{}, std::true_type{}) : go(One{}, std::true_type{});
+        return by_mode(std::integral_constant<Mode, kAdd>{});
+      return clear_first ? by_mode(std::integral_constant<Mode, kWrite>{}) : by_mode(std::integral_constant<Mode, kDense>{});
     });
   });
 }

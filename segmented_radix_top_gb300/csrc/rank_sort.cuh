@@ -15,7 +15,8 @@
 // shared memory and, unless it is the last, sends every item to the shared
 // memory of the block whose tile its place falls into. Bound by the latency
 // of its steps (two cluster barriers and about 30 dependent shared-memory
-// accesses a pass), not by the few hundred kilobytes it moves.
+// accesses a pass) and by the exchange's 8-byte stores, not by the few hundred
+// kilobytes it moves.
 //
 // count_kernel and rank_kernel, any number: two launches a pass over global
 // memory, one tile a block.
@@ -35,6 +36,10 @@ struct Digit {
   uint32_t mask;
   __device__ __forceinline__ uint32_t of(uint32_t key) const { return (key >> shift) & mask; }
 };
+
+// Items in memory: the key in the low word, its place in the input in the
+// high one, so that an item is moved by one access.
+__device__ __forceinline__ uint64_t pack(uint32_t key, uint32_t at) { return (uint64_t)at << 32 | key; }
 
 // Exclusive sum over the digits: x is the caller's value for its digit, one
 // digit a thread; `all` becomes the sum of all. Two block barriers.
@@ -133,16 +138,16 @@ constexpr uint32_t kClusterItems = kMaxCluster * kBlockItems;
 // a sort of one pass, start(d, first place of digit d).
 template <class Src, class Sink>
 __global__ void __launch_bounds__(kSortThreads, 1)
-cluster_sort_kernel(Src src, Sink sink, uint32_t n, uint32_t rounds, int passes, int digit_bits, int bins)
+cluster_sort_kernel(Src src, Sink sink, uint32_t n, int round_bits, int passes, int digit_bits, int bins)
 {
+  const uint32_t rounds = 1u << round_bits;
   extern __shared__ uint32_t sh[];
   const uint32_t blocks = cluster_nctarank(), block = cluster_ctarank();
   uint32_t* seen = sh;                        // [warps][bins]
   uint32_t* who = seen + kSortWarps * bins;   // [warps][bins]
   uint32_t* table = who + kSortWarps * bins;  // [blocks][bins], filled by the blocks of the cluster
-  uint32_t* keys = table + blocks * bins;     // [tile], likewise
+  uint64_t* items = reinterpret_cast<uint64_t*>(table + (blocks * bins + 1) / 2 * 2); // [tile] at:key, likewise
   const uint32_t tile = rounds * kSortThreads;
-  uint32_t* ats = keys + tile;
   __shared__ uint32_t warp_sums[kSortWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t here = warp * rounds * 32 + lane; // in the tile, of round 0
@@ -219,9 +224,8 @@ cluster_sort_kernel(Src src, Sink sink, uint32_t n, uint32_t rounds, int passes,
       if (last) {
         sink.put(key[r], at[r], p);
       } else {
-        const uint32_t to = p / tile, slot = p - to * tile;
-        dsmem_st(dsmem_map(smem_addr(keys + slot), to), key[r]);
-        dsmem_st(dsmem_map(smem_addr(ats + slot), to), at[r]);
+        dsmem_st(dsmem_map(smem_addr(items + (p & (tile - 1))), p / kSortThreads >> round_bits),
+                 pack(key[r], at[r]));
       }
     }
     if (last)
@@ -234,8 +238,9 @@ cluster_sort_kernel(Src src, Sink sink, uint32_t n, uint32_t rounds, int passes,
 #pragma unroll
     for (int r = 0; r < kMaxRounds; ++r)
       if ((uint32_t)r < rounds && r * 32u < left) {
-        key[r] = keys[here + r * 32];
-        at[r] = ats[here + r * 32];
+        const uint64_t item = items[here + r * 32];
+        key[r] = (uint32_t)item;
+        at[r] = (uint32_t)(item >> 32);
       }
     for (int d = threadIdx.x; d < warps * bins; d += kSortThreads)
       seen[d] = who[d] = 0;
@@ -249,9 +254,11 @@ cudaError_t launch_cluster_sort(Src src, Sink sink, uint32_t n, int passes, int 
                                 uint32_t blocks, cudaStream_t stream)
 {
   auto kernel = cluster_sort_kernel<Src, Sink>;
-  const uint32_t rounds = (n + blocks * kSortThreads - 1) / (blocks * kSortThreads);
-  const size_t tile = passes > 1 ? (size_t)rounds * kSortThreads : 0;
-  const size_t smem = ((2 * kSortWarps + blocks) * (size_t)bins + 2 * tile) * 4;
+  int round_bits = 0; // a power of two, so that a place's block and slot are bits of it
+  while (blocks * kSortThreads << round_bits < n)
+    ++round_bits;
+  const size_t tile = passes > 1 ? (size_t)kSortThreads << round_bits : 0;
+  const size_t smem = ((2 * kSortWarps + blocks) * (size_t)bins + 1 + 2 * tile) * 4;
   static DevicePrep prep;
   const cudaError_t e = allow_smem(prep, kernel, smem);
   if (e != cudaSuccess)
@@ -269,7 +276,7 @@ cudaError_t launch_cluster_sort(Src src, Sink sink, uint32_t n, int passes, int 
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, src, sink, n, std::max(rounds, 1u), passes, digit_bits, bins);
+  return cudaLaunchKernelEx(&cfg, kernel, src, sink, n, round_bits, passes, digit_bits, bins);
 }
 
 // ---------------------------------------------------------------------------
@@ -374,18 +381,14 @@ cudaError_t launch_rank(Src src, Digit digit, Sink sink, uint32_t n, Tiling t, i
                                        bins, counts, only);
 }
 
-struct PairSource {
-  const uint32_t *keys, *ats;
-  __device__ __forceinline__ uint32_t key(uint32_t i) const { return keys[i]; }
-  __device__ __forceinline__ uint32_t at(uint32_t i) const { return ats[i]; }
+struct ItemSource {
+  const uint64_t* items;
+  __device__ __forceinline__ uint32_t key(uint32_t i) const { return (uint32_t)items[i]; }
+  __device__ __forceinline__ uint32_t at(uint32_t i) const { return (uint32_t)(items[i] >> 32); }
 };
-struct PairSink {
-  uint32_t *keys, *ats;
-  __device__ __forceinline__ void put(uint32_t key, uint32_t at, uint32_t place) const
-  {
-    keys[place] = key;
-    ats[place] = at;
-  }
+struct ItemSink {
+  uint64_t* items;
+  __device__ __forceinline__ void put(uint32_t key, uint32_t at, uint32_t place) const { items[place] = pack(key, at); }
   __device__ __forceinline__ void start(int, uint32_t) const {}
 };
 
@@ -398,7 +401,7 @@ struct SortPlan {
   uint32_t n;
   int passes, digit_bits, bins;
   Tiling tiles; // items 0: one cluster
-  size_t pairs() const { return tiles.items && passes > 1 ? (size_t)n * 8 : 0; } // bytes of one copy of all items
+  size_t copy() const { return tiles.items && passes > 1 ? (size_t)n * 8 : 0; } // bytes of a copy of all items
   size_t counts() const { return tiles.items ? (size_t)tiles.tiles * (size_t)bins * 4 : 0; }
 };
 inline SortPlan sort_plan(int64_t n, int passes, int digit_bits, int bins)
@@ -406,11 +409,11 @@ inline SortPlan sort_plan(int64_t n, int passes, int digit_bits, int bins)
   return {(uint32_t)n, passes, digit_bits, bins, n > (int64_t)kClusterItems ? tiling(n) : Tiling{0, 0}};
 }
 
-// `pairs`: two copies of the items (plan.pairs() bytes each) for passes that
+// `copies`: two copies of the items (plan.copy() bytes each) for passes that
 // are not the last; counts: plan.counts() bytes. ONE_PASS: plan.passes is 1.
 // Returns the number of launches, or -1 with *e set.
 template <bool ONE_PASS, class Src, class Sink>
-int sort(const SortPlan& p, Src src, Sink sink, uint32_t* const (&pairs)[2], uint32_t* counts, cudaStream_t stream,
+int sort(const SortPlan& p, Src src, Sink sink, uint64_t* const (&copies)[2], uint32_t* counts, cudaStream_t stream,
          cudaError_t* e)
 {
   if (!p.tiles.items) {
@@ -428,8 +431,8 @@ int sort(const SortPlan& p, Src src, Sink sink, uint32_t* const (&pairs)[2], uin
       return;
     *e = launch_rank(from, digit, to, p.n, p.tiles, p.bins, counts, p.passes == 1, stream);
   };
-  auto from = [&](int k) { return PairSource{pairs[k & 1], pairs[k & 1] + p.n}; };
-  auto to = [&](int k) { return PairSink{pairs[k & 1], pairs[k & 1] + p.n}; };
+  auto from = [&](int k) { return ItemSource{copies[k & 1]}; };
+  auto to = [&](int k) { return ItemSink{copies[k & 1]}; };
   *e = cudaSuccess;
   if constexpr (ONE_PASS) {
     pass(src, sink, 0);

@@ -142,7 +142,7 @@ def test_sort_passes(vocab, passes):
     assert int((got != 0).any(1).sum()) == len(some)
 
 
-@pytest.mark.parametrize("n", [4096, 4097, 8193, 16385, 32769, 70000, 131072, 131073, 300001])
+@pytest.mark.parametrize("n", [2017, 4096, 4097, 8192, 8193, 16385, 32769, 70000, 131072, 131073, 300001])
 @pytest.mark.parametrize("vocab", [300, 40000, 300000])
 def test_sort_sizes(n, vocab):
     # every token's positions in order: a column of ones counts them, one of
