@@ -26,9 +26,13 @@ DEVICE_ERROR_INDEX = 4  # SEGTOPK_DEVICE_ERROR_INDEX
 _FLOAT = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 _INT_BYTES = {torch.int32: 4, torch.int64: 8}
 
-# the current stream's handle, without building a Stream object
+# The current stream's handle and the current device, without building a Stream
+# object or entering torch.cuda's lazy initialisation (the tensors are on the
+# GPU already): the calls take about as long as the smallest kernels.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_empty = torch.empty
 
 
 class ExpertGroups(NamedTuple):
@@ -69,24 +73,24 @@ def _on_stream(call):
     return wrapped
 
 
-def _device(first, *others) -> int:
-    index = first.get_device()
-    if index < 0:
+def _run(fn, device, *args):
+    """Calls a C entry point on the current stream of a tensor's device (its
+    index, as Tensor.get_device gives it)."""
+    if device < 0:
         raise ValueError("tensors must be on a CUDA device")
-    for t in others:
-        if t is not None and t.get_device() != index:
-            raise ValueError("tensors must be on one CUDA device")
-    return index
-
-
-def _run(fn, index, *args):
-    if torch.cuda.current_device() == index:
-        rc = fn(*args, _raw_stream(index))
+    if device == _current_device():
+        rc = fn(*args, _raw_stream(device))
     else:
-        with torch.cuda.device(index):
-            rc = fn(*args, _raw_stream(index))
+        with torch.cuda.device(device):
+            rc = fn(*args, _raw_stream(device))
     if rc:
         B._check(rc)
+
+
+def _same_device(device, *tensors):
+    for t in tensors:
+        if t.get_device() != device:
+            raise ValueError("tensors must be on one CUDA device")
 
 
 def _float(t, name) -> int:
@@ -103,28 +107,26 @@ def _matrix(t, name):
     return t if t.stride(1) == 1 else t.contiguous()
 
 
-def _like(t, name, shape, dtype):
-    """Checks a tensor that is read densely, or written."""
+def _dense(t, name, shape, dtype):
+    """A contiguous tensor of this shape and type (t, or a copy)."""
     if t.shape != shape or t.dtype != dtype:
         raise ValueError("%s must be %s of %s" % (name, dtype, tuple(shape)))
-    return t
+    return t if t.is_contiguous() else t.contiguous()
 
 
-def _output(out, name, shape, dtype, near):
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=near.device)
-    _like(out, name, torch.Size(shape), dtype)
-    if not out.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    if out.get_device() != near.get_device():
-        raise ValueError("tensors must be on one CUDA device")
+def _given(out, name, shape, dtype, device):
+    """Checks a tensor to write to."""
+    if out.shape != shape or out.dtype != dtype or not out.is_contiguous():
+        raise ValueError("%s must be contiguous, %s of %s" % (name, dtype, tuple(shape)))
+    _same_device(device, out)
     return out
 
 
 def _score(score) -> int:
-    if score not in SCORE:
+    code = SCORE.get(score)
+    if code is None:
         raise ValueError("score must be one of %s" % ", ".join(SCORE))
-    return SCORE[score]
+    return code
 
 
 @_on_stream
@@ -141,15 +143,16 @@ def route(logits: torch.Tensor, k: int, *, score: str = "softmax", renormalize: 
     L = B.load()
     how, kind = _score(score), _float(logits, "logits")
     logits = _matrix(logits, "logits")
-    index = _device(logits, bias)
-    tokens, experts = logits.shape
+    device, tokens, experts = logits.get_device(), *logits.shape
     at = None
     if bias is not None:
-        bias = _like(bias, "bias", (experts,), torch.float32).contiguous()
+        bias = _dense(bias, "bias", (experts,), torch.float32)
+        _same_device(device, bias)
         at = bias.data_ptr()
-    ids = torch.empty((tokens, max(k, 0)), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((tokens, max(k, 0)), dtype=torch.float32, device=logits.device)
-    _run(L.segtopk_route, index, kind, logits.data_ptr(), tokens, experts, logits.stride(0), k, how, bool(renormalize),
+    shape, place = (tokens, max(k, 0)), logits.device
+    ids = _empty(shape, dtype=torch.int32, device=place)
+    weights = _empty(shape, dtype=torch.float32, device=place)
+    _run(L.segtopk_route, device, kind, logits.data_ptr(), tokens, experts, logits.stride(0), k, how, bool(renormalize),
          scale, at, ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
@@ -162,13 +165,13 @@ def route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, expert_ids:
     L = B.load()
     how, kind = _score(score), _float(logits, "logits")
     logits = _matrix(logits, "logits")
-    tokens, experts = logits.shape
+    device, tokens, experts = logits.get_device(), *logits.shape
     k = expert_ids.shape[-1]
-    ids = _like(expert_ids, "expert_ids", (tokens, k), torch.int32).contiguous()
-    grad = _like(grad_weights, "grad_weights", (tokens, k), torch.float32).contiguous()
-    index = _device(logits, ids, grad)
-    out = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
-    _run(L.segtopk_route_backward, index, kind, grad.data_ptr(), logits.data_ptr(), tokens, experts, logits.stride(0),
+    ids = _dense(expert_ids, "expert_ids", (tokens, k), torch.int32)
+    grad = _dense(grad_weights, "grad_weights", (tokens, k), torch.float32)
+    _same_device(device, ids, grad)
+    out = _empty((tokens, experts), dtype=logits.dtype, device=logits.device)
+    _run(L.segtopk_route_backward, device, kind, grad.data_ptr(), logits.data_ptr(), tokens, experts, logits.stride(0),
          k, ids.data_ptr(), how, bool(renormalize), scale, out.data_ptr())
     return out
 
@@ -181,25 +184,26 @@ def group_by_expert(expert_ids: torch.Tensor, num_experts: int) -> ExpertGroups:
     id_bytes = _INT_BYTES.get(expert_ids.dtype)
     if id_bytes is None or expert_ids.dim() != 2:
         raise ValueError("expert_ids must be int32 or int64 of two dimensions")
-    index = _device(expert_ids)
-    ids = expert_ids.contiguous()
-    device, slots = ids.device, ids.numel()
-    offsets = torch.empty(max(num_experts, 0) + 1, dtype=torch.int64, device=device)
-    rows = torch.empty(ids.shape, dtype=torch.int32, device=device)
-    slot_of_row = torch.empty(slots, dtype=torch.int32, device=device)
+    ids = expert_ids if expert_ids.is_contiguous() else expert_ids.contiguous()
+    place, slots = ids.device, ids.numel()
+    offsets = _empty(max(num_experts, 0) + 1, dtype=torch.int64, device=place)
+    rows = _empty(ids.shape, dtype=torch.int32, device=place)
+    slot_of_row = _empty(slots, dtype=torch.int32, device=place)
     need = L.segtopk_group_workspace_bytes(slots, num_experts)
-    space = torch.empty(need, dtype=torch.uint8, device=device).data_ptr() if need else None
-    _run(L.segtopk_group, index, ids.data_ptr(), id_bytes, slots, num_experts, offsets.data_ptr(), rows.data_ptr(),
-         slot_of_row.data_ptr(), space, need)
+    space = _empty(need, dtype=torch.uint8, device=place) if need else None
+    _run(L.segtopk_group, ids.get_device(), ids.data_ptr(), id_bytes, slots, num_experts, offsets.data_ptr(),
+         rows.data_ptr(), slot_of_row.data_ptr(), space.data_ptr() if need else None, need)
     return ExpertGroups(offsets, rows, slot_of_row)
 
 
-def _groups(groups):
-    offsets, rows = groups.offsets, groups.row_of_slot
-    if offsets.dtype != torch.int64 or rows.dtype != torch.int32 or rows.dim() != 2 or not rows.is_contiguous() \
-            or offsets.dim() != 1 or not offsets.is_contiguous() or offsets.shape[0] < 1:
+def _groups(groups, device):
+    """The rows of the slots, and the address of the number of kept ones."""
+    offsets, rows, _ = groups
+    if offsets.dtype != torch.int64 or rows.dtype != torch.int32 or rows.dim() != 2 or offsets.dim() != 1 \
+            or not (rows.is_contiguous() and offsets.is_contiguous()) or offsets.numel() < 1:
         raise ValueError("groups must come from group_by_expert")
-    return rows, offsets.data_ptr() + 8 * (offsets.shape[0] - 1)
+    _same_device(device, rows, offsets)
+    return rows, offsets.data_ptr() + 8 * (offsets.numel() - 1)
 
 
 @_on_stream
@@ -209,14 +213,18 @@ def dispatch(x: torch.Tensor, groups: ExpertGroups, *, out=None):
     k, width], zeros from row groups.offsets[-1] on."""
     L = B.load()
     x = _matrix(x, "x")
-    rows, kept = _groups(groups)
+    device = x.get_device()
+    rows, kept = _groups(groups, device)
     tokens, k = rows.shape
-    if x.shape[0] != tokens:
+    count, width = x.shape
+    if count != tokens:
         raise ValueError("x must have a row for each token of the groups")
-    index = _device(x, rows, groups.offsets)
-    width = x.shape[1]
-    out = _output(out, "out", (tokens * k, width), x.dtype, x)
-    _run(L.segtopk_dispatch, index, x.data_ptr(), x.element_size(), tokens, k, width, x.stride(0), rows.data_ptr(),
+    shape = (tokens * k, width)
+    if out is None:
+        out = _empty(shape, dtype=x.dtype, device=x.device)
+    else:
+        _given(out, "out", shape, x.dtype, device)
+    _run(L.segtopk_dispatch, device, x.data_ptr(), x.element_size(), tokens, k, width, x.stride(0), rows.data_ptr(),
          kept, out.data_ptr())
     return out
 
@@ -225,18 +233,22 @@ def _combine(values, groups, weights, out):
     L = B.load()
     kind = _float(values, "rows")
     values = _matrix(values, "rows")
-    rows, _ = _groups(groups)
+    device = values.get_device()
+    rows, _ = _groups(groups, device)
     tokens, k = rows.shape
-    if values.shape[0] != tokens * k:
+    count, width = values.shape
+    if count != tokens * k:
         raise ValueError("rows must have a row for each slot of the groups")
-    index = _device(values, rows, weights)
     at = None
     if weights is not None:
-        weights = _like(weights, "weights", (tokens, k), torch.float32).contiguous()
+        weights = _dense(weights, "weights", rows.shape, torch.float32)
+        _same_device(device, weights)
         at = weights.data_ptr()
-    width = values.shape[1]
-    out = _output(out, "out", (tokens, width), values.dtype, values)
-    _run(L.segtopk_combine, index, kind, values.data_ptr(), tokens, k, width, values.stride(0), rows.data_ptr(), at,
+    if out is None:
+        out = _empty((tokens, width), dtype=values.dtype, device=values.device)
+    else:
+        _given(out, "out", (tokens, width), values.dtype, device)
+    _run(L.segtopk_combine, device, kind, values.data_ptr(), tokens, k, width, values.stride(0), rows.data_ptr(), at,
          out.data_ptr())
     return out
 
@@ -266,17 +278,19 @@ def combine_backward(grad_out: torch.Tensor, rows: torch.Tensor, groups: ExpertG
     L = B.load()
     kind = _float(rows, "rows")
     values, grad = _matrix(rows, "rows"), _matrix(grad_out, "grad_out")
-    at, kept = _groups(groups)
+    device, place = values.get_device(), values.device
+    at, kept = _groups(groups, device)
     tokens, k = at.shape
-    width = values.shape[1]
-    if values.shape[0] != tokens * k:
+    count, width = values.shape
+    if count != tokens * k:
         raise ValueError("rows must have a row for each slot of the groups")
-    _like(grad, "grad_out", (tokens, width), values.dtype)
-    weights = _like(weights, "weights", (tokens, k), torch.float32).contiguous()
-    index = _device(values, grad, at, weights, groups.offsets)
-    grad_rows = torch.empty((tokens * k, width), dtype=values.dtype, device=values.device)
-    grad_weights = torch.empty((tokens, k), dtype=torch.float32, device=values.device)
-    _run(L.segtopk_combine_backward, index, kind, grad.data_ptr(), grad.stride(0), values.data_ptr(), values.stride(0),
+    if grad.shape != (tokens, width) or grad.dtype != values.dtype:
+        raise ValueError("grad_out must be %s of %s" % (values.dtype, (tokens, width)))
+    weights = _dense(weights, "weights", at.shape, torch.float32)
+    _same_device(device, grad, weights)
+    grad_rows = _empty((count, width), dtype=values.dtype, device=place)
+    grad_weights = _empty((tokens, k), dtype=torch.float32, device=place)
+    _run(L.segtopk_combine_backward, device, kind, grad.data_ptr(), grad.stride(0), values.data_ptr(), values.stride(0),
          tokens, k, width, at.data_ptr(), kept, weights.data_ptr(), grad_rows.data_ptr(), grad_weights.data_ptr())
     return grad_rows, grad_weights
 
@@ -285,7 +299,7 @@ def _token_ids(tokens):
     size = _INT_BYTES.get(tokens.dtype)
     if size is None:
         raise ValueError("tokens must be int32 or int64")
-    return tokens.contiguous(), size
+    return tokens if tokens.is_contiguous() else tokens.contiguous(), size
 
 
 @_on_stream
@@ -297,12 +311,14 @@ def embedding(table: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0, 
     kind = _float(table, "table")
     table = _matrix(table, "table")
     tokens, size = _token_ids(tokens)
-    index = _device(table, tokens)
-    vocab, width = table.shape
-    if out_dtype is None:
-        out_dtype = table.dtype if out is None else out.dtype
-    out = _output(out, "out", (*tokens.shape, width), out_dtype, table)
-    _run(L.segtopk_embedding, index, kind, table.data_ptr(), vocab, width, table.stride(0), tokens.data_ptr(), size,
+    device, vocab, width = table.get_device(), *table.shape
+    _same_device(device, tokens)
+    shape = (*tokens.shape, width)
+    if out is None:
+        out = _empty(shape, dtype=out_dtype or table.dtype, device=table.device)
+    else:
+        _given(out, "out", shape, out_dtype or out.dtype, device)
+    _run(L.segtopk_embedding, device, kind, table.data_ptr(), vocab, width, table.stride(0), tokens.data_ptr(), size,
          tokens.numel(), scale, _float(out, "out"), out.data_ptr())
     return out
 
@@ -322,21 +338,26 @@ def embedding_backward(grad_out: torch.Tensor, tokens: torch.Tensor, num_rows: i
     tokens, size = _token_ids(tokens)
     if grad_out.dim() < 1 or grad_out.shape[:-1] != tokens.shape:
         raise ValueError("grad_out must have a row for each token")
-    width = grad_out.shape[-1]
-    grad = _matrix(grad_out if grad_out.dim() == 2 else grad_out.reshape(tokens.numel(), width), "grad_out")
-    index = _device(grad, tokens)
-    if padding_idx is not None:
-        if not -num_rows <= padding_idx < num_rows:
-            raise ValueError("padding_idx must be a row of the table")
-        padding_idx %= num_rows
-    if accumulate and grad_table is None:
+    count, width = tokens.numel(), grad_out.shape[-1]
+    grad = _matrix(grad_out if grad_out.dim() == 2 else grad_out.reshape(count, width), "grad_out")
+    device, place = grad.get_device(), grad.device
+    _same_device(device, tokens)
+    if padding_idx is None:
+        padding = -1
+    elif -num_rows <= padding_idx < num_rows:
+        padding = padding_idx % num_rows
+    else:
+        raise ValueError("padding_idx must be a row of the table")
+    shape = (max(num_rows, 0), width)
+    if grad_table is not None:
+        out = _given(grad_table, "grad_table", shape, dtype or grad_table.dtype, device)
+    elif accumulate:
         raise ValueError("accumulate needs grad_table")
-    if dtype is None:
-        dtype = grad.dtype if grad_table is None else grad_table.dtype
-    out = _output(grad_table, "grad_table", (max(num_rows, 0), width), dtype, grad)
-    need = L.segtopk_embedding_backward_workspace_bytes(tokens.numel(), num_rows, width)
-    space = torch.empty(need, dtype=torch.uint8, device=grad.device)
-    _run(L.segtopk_embedding_backward, index, kind, grad.data_ptr(), grad.stride(0), tokens.data_ptr(), size,
-         tokens.numel(), num_rows, width, -1 if padding_idx is None else padding_idx, scale, _float(out, "grad_table"),
-         out.data_ptr(), bool(accumulate), space.data_ptr(), need)
+    else:
+        out = _empty(shape, dtype=dtype or grad.dtype, device=place)
+    need = L.segtopk_embedding_backward_workspace_bytes(count, num_rows, width)
+    space = _empty(need, dtype=torch.uint8, device=place)
+    _run(L.segtopk_embedding_backward, device, kind, grad.data_ptr(), grad.stride(0), tokens.data_ptr(), size, count,
+         num_rows, width, padding, scale, _float(out, "grad_table"), out.data_ptr(), bool(accumulate), space.data_ptr(),
+         need)
     return out
