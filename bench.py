@@ -118,7 +118,8 @@ def measured_peak():
 
 
 # sources that no top-k workload runs
-ROW_OPERATOR_SOURCES = {"rows.cuh", "rank_sort.cuh", "route.cu", "group.cu", "experts.cu", "embedding.cu"}
+ROW_OPERATOR_SOURCES = {"rows.cuh", "rank_sort.cuh", "route.cu", "group.cu", "experts.cu", "embedding.cu",
+                        "rows_binding.cpp"}
 
 
 def kernel_source_hash() -> str:

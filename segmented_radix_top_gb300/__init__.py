@@ -11,12 +11,13 @@ from ._binding import (DETERMINISM, DIRECTION, DTYPE, KEY_BYTES, MAX_K, NOALLOC_
                        batched_topk_host_noalloc, host_workspace_bytes,
                        last_launch_count, library_path, load, load_instrumented, read_device_error,
                        read_stats, set_test_hooks, topk)
-from ._rows import (DEVICE_ERROR_INDEX, MAX_EXPERTS, ROUTE_MAX_K, SCORE, ExpertGroups, combine,  # noqa: F401
+from ._rows import (DEVICE_ERROR_INDEX, MAX_EXPERTS, ROUTE_MAX_K, ExpertGroups, combine,  # noqa: F401
                     combine_backward, dispatch, dispatch_backward, embedding, embedding_backward,
                     group_by_expert, route, route_backward)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libsegtopk.so for sm_103a in-tree (nvcc; no GPU needed)."""
+    """Compile libsegtopk.so for sm_103a and the row operators' binding
+    in-tree (nvcc, g++; no GPU needed)."""
     from . import _build
     return _build.build(force=force, verbose=verbose)

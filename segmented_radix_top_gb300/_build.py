@@ -9,6 +9,10 @@ sources compiled with SEGTOPK_STATS and SEGTOPK_TEST_HOOKS: per-CTA counters
 (segtopk_read_stats) and the test hooks of the bounded copy wait
 (segtopk_set_test_hooks). build_all() compiles both in one pool of
 compiler processes.
+
+Beside the library, csrc/rows_binding.cpp becomes _rows_native.so (g++ and
+PyTorch's headers): the Python binding of the row operators. It does not link
+the library; _rows.py hands it the entry points of the loaded one.
 """
 from __future__ import annotations
 
@@ -24,6 +28,8 @@ ROOT = os.path.dirname(HERE)
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libsegtopk.so")
+BINDING_SRC = os.path.join(CSRC, "rows_binding.cpp")
+BINDING_PATH = os.path.join(HERE, "_rows_native.so")
 VARIANTS = {
     "": (BUILD_DIR, LIB_PATH, []),
     "instr": (os.path.join(HERE, "_build_instr"), os.path.join(HERE, "libsegtopk_instr.so"),
@@ -77,6 +83,35 @@ def _compile(variant: str, src: str, extra_flags, verbose: bool) -> str:
     return obj
 
 
+def binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING_PATH):
+        return False
+    t = os.path.getmtime(BINDING_PATH)
+    return all(os.path.getmtime(d) <= t for d in [BINDING_SRC, os.path.join(INCLUDE, "segtopk.h")])
+
+
+def _compile_binding(verbose: bool) -> str:
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    tmp = BINDING_PATH + ".tmp.%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I", os.path.join(base, "include"), "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", cuda, BINDING_SRC, "-o", tmp, "-L", os.path.join(base, "lib"),
+           "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+           "-Wl,-rpath," + os.path.join(base, "lib")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (BINDING_SRC, r.stdout, r.stderr))
+    if verbose and (r.stdout or r.stderr):
+        sys.stderr.write(r.stdout + r.stderr)
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
+
+
 def _link(variant: str, objs) -> str:
     out_path = VARIANTS[variant][1]
     tmp = out_path + ".tmp.%d" % os.getpid()
@@ -89,16 +124,21 @@ def _link(variant: str, objs) -> str:
 
 
 def build_variants(variants, force: bool = False, verbose: bool = False, extra_flags=None):
-    """Builds the given variants, every translation unit of all of them in
-    one pool of compiler processes; returns the library paths."""
+    """Builds the given variants and the row operators' binding, every
+    translation unit of all of them in one pool of compiler processes;
+    returns the library paths."""
     todo = [v for v in variants if force or not up_to_date(v)]
     for v in todo:
         os.makedirs(VARIANTS[v][0], exist_ok=True)
     srcs = _sources()
     jobs = [(v, s) for v in todo for s in srcs]
-    if jobs:
-        with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
+    binding = force or not binding_up_to_date()
+    if jobs or binding:
+        with ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
+            bound = ex.submit(_compile_binding, verbose) if binding else None
             objs = list(ex.map(lambda j: _compile(j[0], j[1], extra_flags, verbose), jobs))
+            if bound:
+                bound.result()
         for v in todo:
             _link(v, [o for (vv, _), o in zip(jobs, objs) if vv == v])
     return [lib_path(v) for v in variants]
