@@ -225,7 +225,6 @@ __device__ __forceinline__ void positions_before(const Merge& m, const uint64_t 
 // its own with asynchronous copies, which takes no registers and, as no
 // thread reads another's part, no barrier. Elements too badly aligned for
 // that (N = 1) go in batches of eight through registers.
-constexpr int kRingBytes = 48 << 10; // of a block; four blocks an SM
 template <class G, class W, int N, Mode MODE>
 struct Ring {
   static constexpr bool kUsed = N > 1;
@@ -240,21 +239,6 @@ struct Ring {
     return memory + kAhead * kThreads * kGrad + (slot * kThreads + threadIdx.x) * kRow;
   }
 };
-
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void* to, const void* from)
-{
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(to)), "l"(from), "n"(BYTES) : "memory");
-}
-__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void wait_for_copies() // all but the last N groups
-{
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 template <class G, class W, int N, Mode MODE>
 __global__ void __launch_bounds__(kThreads, 4)

@@ -7,7 +7,8 @@
 //
 // r(t, j) is the row of token t's j-th slot, or none. Every kernel goes by
 // token, so a token's row is read or written once and only the k sorted rows
-// are scattered; all are bound by memory bandwidth.
+// are scattered; all are bound by memory bandwidth, if the gathered rows are
+// asked for early enough.
 #include "rows.cuh"
 
 namespace segtopk {
@@ -75,6 +76,9 @@ dispatch_kernel(const T* x, int64_t stride, Shape s, const int32_t* row_of_slot,
   clear_tail(s, kept, t, lane, s.width, rows);
 }
 
+// A group of threads per token, eight rows in flight in registers: for few
+// tokens, and for rows that cannot be copied asynchronously (N = 1: their
+// parts do not start on 16-byte boundaries).
 template <class T, int N, bool WEIGHTED>
 __global__ void __launch_bounds__(kThreads, 3)
 combine_kernel(const T* rows, int64_t stride, Shape s, const int32_t* row_of_slot, const float* weights, T* out)
@@ -114,12 +118,15 @@ combine_kernel(const T* rows, int64_t stride, Shape s, const int32_t* row_of_slo
   }
 }
 
-template <class T, int N>
+// The backward pass for rows that cannot be copied asynchronously: a group of
+// threads per token, element by element.
+template <class T>
 __global__ void __launch_bounds__(kThreads, 3)
 combine_backward_kernel(const T* grad, int64_t grad_stride, const T* rows, int64_t stride, Shape s,
                         const int32_t* row_of_slot, const float* weights, const int64_t* kept, T* grad_rows,
                         float* grad_weights)
 {
+  constexpr int N = 1;
   __shared__ float part[kThreads / 32][8];
   wait_for_previous();
   allow_next();
@@ -192,7 +199,243 @@ combine_backward_kernel(const T* grad, int64_t grad_stride, const T* rows, int64
     }
   }
   if (some)
-    clear_tail(s, kept, t, lane, s.width / N, reinterpret_cast<Vec<T, N>*>(grad_rows));
+    clear_tail(s, kept, t, lane, s.width, grad_rows);
+}
+
+// Many tokens: a group of threads takes a run of them and copies the next
+// kAhead rows into shared memory meanwhile, across tokens. Four blocks of 48
+// KB an SM keep 192 KB under way; eight rows a thread in registers, 96 KB
+// while a block lasts and nothing while the next one starts.
+constexpr int kAhead = kRingBytes / (kThreads * 16);
+constexpr int kAheadBack = kAhead - 1; // leaves room for the products' parts
+
+struct Run {
+  Shape s;
+  uint32_t groups;
+  uint32_t at, end; // tokens of this thread's group, as set by start()
+  int lane;
+  __device__ __forceinline__ uint32_t start()
+  {
+    lane = threadIdx.x & (s.lanes - 1);
+    const uint32_t g = blockIdx.x * (kThreads / s.lanes) + threadIdx.x / s.lanes;
+    at = g < groups ? (uint32_t)((uint64_t)s.tokens * g / groups) : 0;
+    end = g < groups ? (uint32_t)((uint64_t)s.tokens * (g + 1) / groups) : 0;
+    return g;
+  }
+};
+
+template <class T, int N, bool WEIGHTED>
+__global__ void __launch_bounds__(kThreads, 4)
+combine_run_kernel(const T* rows, int64_t stride, Run run, const int32_t* row_of_slot, const float* weights, T* out)
+{
+  extern __shared__ uint4 ring[];
+  wait_for_previous();
+  allow_next();
+  run.start();
+  const int64_t c = ((int64_t)blockIdx.y * run.s.lanes + run.lane) * N;
+  if (c >= run.s.width || run.at == run.end)
+    return;
+  rows += c;
+  out += c;
+  const int k = run.s.k;
+  const uint32_t slots = run.s.tokens * (uint32_t)k, last = run.end * (uint32_t)k;
+  uint32_t ahead = run.at * (uint32_t)k; // the next slot to copy
+  auto copy = [&](int at) {
+    if (ahead < last) {
+      const int32_t r = row_at(row_of_slot + ahead, slots);
+      if (r >= 0)
+        copy_async<16>(&ring[at * kThreads + threadIdx.x], rows + r * stride);
+      ++ahead;
+    }
+    commit_copies();
+  };
+  for (int u = 0; u < kAhead; ++u)
+    copy(u);
+  float acc[N] = {};
+  uint32_t t = run.at;
+  int at = 0, j = 0;
+  for (uint32_t i = run.at * (uint32_t)k; i < last; ++i) {
+    const int32_t r = row_at(row_of_slot + i, slots);
+    const float w = WEIGHTED ? weights[i] : 1.0f;
+    wait_for_copies<kAhead - 1>();
+    if (r >= 0) {
+      const Vec<T, N> v = load<T, N>(reinterpret_cast<const T*>(&ring[at * kThreads + threadIdx.x]));
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        acc[e] = fmaf(w, v.f32(e), acc[e]);
+    }
+    copy(at);
+    at = at + 1 == kAhead ? 0 : at + 1;
+    if (++j == k) {
+      store_f32<T, N>(out + (int64_t)t * run.s.width, acc);
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        acc[e] = 0;
+      ++t;
+      j = 0;
+    }
+  }
+}
+
+// Sums over a warp of eight values of each lane, in nine exchanges instead of
+// forty: at each of the first three a lane passes on half of the values that
+// it still has. The result in lane l is the sum of value l / 4.
+__device__ __forceinline__ float warp_sum8(float (&v)[8])
+{
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 4, o = 16; n > 0; n /= 2, o /= 2) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float pass = upper ? v[i] : v[i + n];
+      v[i] = (upper ? v[i + n] : v[i]) + __shfl_xor_sync(kAll, pass, o);
+    }
+  }
+  v[0] += __shfl_xor_sync(kAll, v[0], 2);
+  return v[0] + __shfl_xor_sync(kAll, v[0], 1);
+}
+
+template <class T, int N>
+__global__ void __launch_bounds__(kThreads, 4)
+combine_backward_run_kernel(const T* grad, int64_t grad_stride, const T* rows, int64_t stride, Run run,
+                            const int32_t* row_of_slot, const float* weights, const int64_t* kept, T* grad_rows,
+                            float* grad_weights)
+{
+  extern __shared__ uint4 ring[];
+  __shared__ float part[2][kThreads / 32][8];
+  wait_for_previous();
+  allow_next();
+  const uint32_t group = run.start();
+  const int lanes = run.s.lanes, lane = run.lane, k = run.s.k;
+  const int64_t width = run.s.width, step = (int64_t)lanes * N, c0 = (int64_t)lane * N;
+  const uint32_t slots = run.s.tokens * (uint32_t)k;
+  // Copies, for each token, eight of its slots at a time and each of the
+  // thread's columns: the gradient's part, then the rows'. The order is that
+  // of the loops below.
+  struct {
+    uint32_t t;
+    int j0, u; // u 0: the gradient, else slot j0 + u - 1
+    int64_t c;
+  } ahead = {run.at, 0, 0, c0};
+  auto copy = [&](int at) {
+    if (ahead.t < run.end) {
+      const T* from = nullptr;
+      if (ahead.u == 0) {
+        from = grad + (int64_t)ahead.t * grad_stride;
+      } else {
+        const int32_t r = row_at(row_of_slot + (ahead.t * (uint32_t)k + ahead.j0 + ahead.u - 1), slots);
+        if (r >= 0)
+          from = rows + r * stride;
+      }
+      if (from && ahead.c < width)
+        copy_async<16>(&ring[at * kThreads + threadIdx.x], from + ahead.c);
+      if (++ahead.u > min(8, k - ahead.j0)) {
+        ahead.u = 0;
+        ahead.c += step;
+        if (ahead.c - c0 >= width) {
+          ahead.c = c0;
+          ahead.j0 += 8;
+          if (ahead.j0 >= k) {
+            ahead.j0 = 0;
+            ++ahead.t;
+          }
+        }
+      }
+    }
+    commit_copies();
+  };
+  for (int u = 0; u < kAheadBack; ++u)
+    copy(u);
+  int at = 0, turn = 0;
+  auto take = [&]() { // the next copied part; its place is copied to again
+    wait_for_copies<kAheadBack - 1>();
+    const Vec<T, N> v = load<T, N>(reinterpret_cast<const T*>(&ring[at * kThreads + threadIdx.x]));
+    copy(at);
+    at = at + 1 == kAheadBack ? 0 : at + 1;
+    return v;
+  };
+  for (uint32_t t = run.at; t < run.end; ++t) {
+    for (int j0 = 0; j0 < k; j0 += 8) {
+      const uint32_t i0 = t * (uint32_t)k + j0;
+      float dot[8] = {};
+      for (int64_t c = c0; c - c0 < width; c += step) {
+        const Vec<T, N> g = take();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j0 + j >= k)
+            break;
+          const Vec<T, N> v = take();
+          const int32_t r = row_at(row_of_slot + i0 + j, slots);
+          if (r < 0 || c >= width)
+            continue;
+          const float w = weights[i0 + j];
+          float y[N];
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            dot[j] = fmaf(v.f32(e), g.f32(e), dot[j]);
+            y[e] = w * g.f32(e);
+          }
+          store_f32<T, N>(grad_rows + r * width + c, y);
+        }
+      }
+      // the lanes' parts of each product, always added in the same order
+      if (lanes < 32) {
+        const unsigned mask = ((1u << lanes) - 1) << ((threadIdx.x & 31) - lane);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          for (int o = lanes / 2; o > 0; o >>= 1)
+            dot[j] += __shfl_xor_sync(mask, dot[j], o);
+          if (lane == 0 && j0 + j < k)
+            grad_weights[i0 + j] = dot[j];
+        }
+        continue;
+      }
+      const float sum = warp_sum8(dot);
+      const int j = (threadIdx.x & 31) / 4;
+      if (lanes == 32) {
+        if (lane % 4 == 0 && j0 + j < k)
+          grad_weights[i0 + j] = sum;
+        continue;
+      }
+      const int warp = threadIdx.x >> 5;
+      if (lane % 4 == 0)
+        part[turn][warp][j] = sum;
+      // the group's warps only; the two turns' memory makes one barrier do
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / lanes), "r"(lanes) : "memory");
+      if (lane < 8 && j0 + lane < k) {
+        float all = 0;
+        for (int v = 0; v < lanes / 32; ++v)
+          all += part[turn][warp + v][lane];
+        grad_weights[i0 + lane] = all;
+      }
+      turn ^= 1;
+    }
+  }
+  if (group < run.groups)
+    for (int64_t r = max(*kept, (int64_t)0) + group; r < slots; r += run.groups)
+      for (int64_t c = c0; c < width; c += step)
+        store<T, N>(grad_rows + r * width + c, Vec<T, N>{});
+}
+
+// Groups resident at four blocks an SM where a token's columns take `tiles`
+// groups.
+int64_t resident(const Shape& s, int64_t tiles, int sms)
+{
+  return std::max<int64_t>(1, (int64_t)sms * 4 * kThreads / (s.lanes * tiles));
+}
+// Whole waves of resident groups, of as many as leave runs of eight tokens or
+// more. 8192 tokens of 2048 in bf16, k = 8, in runs of 1, 3, 8, 13 (one
+// wave): 62, 53, 53, 50 us; 32768 of 4096 in runs of 7, 27, 108: 353, 364, 369.
+Run run_of(const Shape& s, int64_t tiles, int sms)
+{
+  const int64_t groups = resident(s, tiles, sms);
+  return {s, (uint32_t)std::min<int64_t>(s.tokens, groups * std::max<int64_t>(1, s.tokens / (8 * groups))), 0, 0, 0};
+}
+dim3 grid_of(const Run& run, int64_t tiles)
+{
+  const uint32_t per_block = (uint32_t)(kThreads / run.s.lanes);
+  return dim3((run.groups + per_block - 1) / per_block, (unsigned)tiles);
 }
 
 dim3 grid_of(const Shape& s)
@@ -280,6 +523,18 @@ extern "C" int segtopk_combine(segtopk_dtype dtype, const void* rows, int64_t to
     auto go = [&](auto n) {
       constexpr int V = decltype(n)::value;
       const Shape s = {(uint32_t)tokens, k, width, lanes_for(width / V, kThreads)};
+      if constexpr (V > 1) {
+        const int64_t cols = (int64_t)s.lanes * V, tiles = (width + cols - 1) / cols;
+        // runs pay once they are long: 1237 tokens of 1000 in f32, k = 6, take
+        // 6.1 us a token per group and 7.1 in runs of two; 8192 of 2048 in
+        // bf16 58 and 50
+        if (tokens >= 8 * resident(s, tiles, sms)) {
+          const Run run = run_of(s, tiles, sms);
+          auto kernel = weights ? combine_run_kernel<T, V, true> : combine_run_kernel<T, V, false>;
+          return finish(launch(kernel, grid_of(run, tiles), kThreads, kRingBytes, (cudaStream_t)stream, (const T*)rows,
+                               row_stride, run, row_of_slot, weights, (T*)out), 1);
+        }
+      }
       auto kernel = weights ? combine_kernel<T, V, true> : combine_kernel<T, V, false>;
       return finish(launch(kernel, grid_of(s), kThreads, 0, (cudaStream_t)stream, (const T*)rows, row_stride, s,
                            row_of_slot, weights, (T*)out), 1);
@@ -319,7 +574,13 @@ extern "C" int segtopk_combine_backward(segtopk_dtype dtype, const void* grad_ou
     auto go = [&](auto n) {
       constexpr int V = decltype(n)::value;
       const Shape s = {(uint32_t)tokens, k, width, lanes_for(width / V, kThreads)};
-      return finish(launch(combine_backward_kernel<T, V>, grid_of(s), kThreads, 0, (cudaStream_t)stream,
+      if constexpr (V > 1) {
+        const Run run = run_of(s, 1, sms);
+        return finish(launch(combine_backward_run_kernel<T, V>, grid_of(run, 1), kThreads, kAheadBack * kThreads * 16,
+                             (cudaStream_t)stream, (const T*)grad_out, grad_stride, (const T*)rows, row_stride, run,
+                             row_of_slot, weights, kept, (T*)grad_rows, grad_weights), 1);
+      }
+      return finish(launch(combine_backward_kernel<T>, grid_of(s), kThreads, 0, (cudaStream_t)stream,
                            (const T*)grad_out, grad_stride, (const T*)rows, row_stride, s, row_of_slot, weights, kept,
                            (T*)grad_rows, grad_weights), 1);
     };

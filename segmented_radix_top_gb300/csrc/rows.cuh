@@ -133,6 +133,31 @@ __device__ __forceinline__ void store_f32(T* p, const float (&x)[N])
 }
 
 // ---------------------------------------------------------------------------
+// Asynchronous copies of a thread's own
+// ---------------------------------------------------------------------------
+// A kernel that gathers rows is bound by their latency unless enough of them
+// are under way. Copied into shared memory ahead of their use they take no
+// registers, and where a thread reads only what it copied itself, no barrier.
+constexpr int kRingBytes = 48 << 10; // of a block: no opt-in, four blocks an SM
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from)
+{
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(BYTES) : "memory");
+}
+// Copies since the last call become a group (an empty one without any).
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_for_copies() // all but the last N groups
+{
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ---------------------------------------------------------------------------
 // Host helpers
 // ---------------------------------------------------------------------------
 // Calls f with a value of the element type of `dtype`; NOT_SUPPORTED for a

@@ -127,6 +127,46 @@ def test_there_and_back(tokens, k, experts, width, dropped, dtype):
     ref.within(grad_w, exact_w, (width + 1) * ref.U32 * size)
 
 
+@pytest.mark.parametrize("tokens,k,experts,width,dropped,dtype", [
+    (2500, 3, 40, 2048, 0.2, torch.float32), (2433, 9, 16, 4104, 0.1, torch.bfloat16),
+    (9900, 2, 8, 1000, 0, torch.float16), (40000, 1, 4, 256, 0.5, torch.bfloat16), (80000, 2, 6, 64, 0.1, torch.float32)])
+def test_runs_of_many_tokens(tokens, k, experts, width, dropped, dtype):
+    # enough tokens for groups of threads to take several each; the
+    # definitions in 64 bits on the GPU
+    groups = st.group_by_expert(ids_of(tokens, k, experts, 1, dropped).cuda(), experts)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, y = (torch.randn(n, width, generator=g, device="cuda", dtype=dtype) for n in (tokens, tokens * k))
+    w = torch.rand(tokens, k, generator=g, device="cuda")
+    rows, kept = groups.row_of_slot.long(), int(groups.offsets[-1])
+    y[kept:] = float("nan")
+    some = (rows >= 0).double()[..., None]
+    at, wide = rows.clamp(min=0), w.double()[..., None] * some
+    out, back = st.combine(y, groups, w), st.dispatch_backward(y, groups)
+    exact, size = torch.zeros(2, tokens, width, dtype=torch.float64, device="cuda")
+    exact_back, size_back = torch.zeros(2, tokens, width, dtype=torch.float64, device="cuda")
+    grad_w, size_w = torch.zeros(2, tokens, k, dtype=torch.float64, device="cuda")
+    for j in range(k):
+        part = torch.where(some[:, j] > 0, y[at[:, j]].double(), 0)
+        exact += wide[:, j] * part
+        size += wide[:, j] * part.abs()
+        exact_back += part
+        size_back += part.abs()
+        grad_w[:, j] = (part * x.double()).sum(1)
+        size_w[:, j] = (part * x.double()).abs().sum(1)
+
+    def near(got, want, bound):
+        assert bool(((got.double() - want).abs() <= bound).all())
+
+    near(out, exact, (k + 1) * ref.U32 * size + ref.rounded(dtype, exact.abs()))
+    near(back, exact_back, (k + 1) * ref.U32 * size_back + ref.rounded(dtype, exact_back.abs()))
+    got_y, got_w = st.combine_backward(x, y, groups, w)
+    near(got_w, grad_w, (width + 1) * ref.U32 * size_w)
+    want = torch.zeros(tokens * k, width, dtype=torch.float64, device="cuda")
+    slot = groups.slot_of_row[:kept].long()
+    want[:kept] = w.double().reshape(-1)[slot, None] * x.double()[slot // k]
+    near(got_y, want, 1.01 * ref.U32 * want.abs() + ref.rounded(dtype, want.abs()))
+
+
 @pytest.mark.parametrize("dtype", [torch.uint8, torch.int16, torch.int32, torch.float64, torch.float8_e4m3fn])
 @pytest.mark.parametrize("width", [1, 5, 48, 260])
 def test_dispatch_moves_any_element(dtype, width):
