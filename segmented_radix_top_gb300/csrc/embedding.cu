@@ -48,21 +48,23 @@ lookup_kernel(const T* table, int64_t stride, int64_t vocab, const I* tokens, ui
     return;
   const int64_t v = row_of_token(tokens, i, vocab);
   constexpr int U = kInFlight;
-  const int64_t step = (int64_t)lanes * N;
-  for (int64_t c0 = (int64_t)lane * N; c0 < width; c0 += U * step) {
-    Vec<T, N> got[U] = {};
+  const int64_t step = (int64_t)lanes * kPart<N>;
+  table += v * stride;
+  out += (int64_t)i * width;
+  for (int64_t c0 = part_start<N>(lane); c0 < width; c0 += U * step) {
+    Part<T, N> got[U] = {};
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (v >= 0 && c0 + u * step < width)
-        got[u] = load<T, N>(table + v * stride + c0 + u * step);
+        got[u] = load_part<T, N>(table + c0 + u * step, lanes, width - c0 - u * step);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float y[N];
+      float y[kPart<N>];
 #pragma unroll
-      for (int e = 0; e < N; ++e)
+      for (int e = 0; e < kPart<N>; ++e)
         y[e] = v >= 0 ? scale * got[u].f32(e) : 0.0f;
       if (c0 + u * step < width)
-        store_f32<O, N>(out + (int64_t)i * width + c0 + u * step, y);
+        store_part<O, N>(out + c0 + u * step, y, lanes, width - c0 - u * step);
     }
   }
 }
@@ -224,7 +226,7 @@ __device__ __forceinline__ void positions_before(const Merge& m, const uint64_t 
 // when adding, of the table rows that they complete) into shared memory of
 // its own with asynchronous copies, which takes no registers and, as no
 // thread reads another's part, no barrier. Elements too badly aligned for
-// that (N = 1) go in batches of eight through registers.
+// that (N = 1) go in batches through registers.
 template <class G, class W, int N, Mode MODE>
 struct Ring {
   static constexpr bool kUsed = N > 1;
@@ -241,14 +243,15 @@ struct Ring {
 };
 
 template <class G, class W, int N, Mode MODE>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, N > 1 ? 4 : 3)
 merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
 {
   wait_for_previous();
   allow_next();
   const int lane = threadIdx.x & (m.lanes - 1);
   const uint32_t p = blockIdx.x * (kThreads / m.lanes) + threadIdx.x / m.lanes;
-  const int64_t c = ((int64_t)blockIdx.y * m.lanes + lane) * N;
+  constexpr int P = kPart<N>;
+  const int64_t c = (int64_t)blockIdx.y * m.lanes * P + part_start<N>(lane), left = m.width - c;
   if (p >= m.shares)
     return;
   const uint64_t steps = (uint64_t)m.n + (MODE == kDense ? m.vocab : 0);
@@ -269,39 +272,39 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
   }
   auto clear_to = [&](uint32_t row) {
     W* to = out + (int64_t)empty * m.width;
-    const Vec<W, N> zero = {};
+    const float zero[P] = {};
 #pragma unroll 4
     for (; empty < row; ++empty, to += m.width)
-      store<W, N>(to, zero);
+      store_part<W, N>(to, zero, m.lanes, left);
     empty = row + 1;
   };
 
-  float acc[N] = {};
+  float acc[P] = {};
   int32_t head_row = -1, carry_row = -1;
   // one position: its key, the next one's, its gradient, and the row it adds
   // to if the keys differ
-  auto take = [&](uint32_t key, uint32_t next, const Vec<G, N>& v, const Vec<W, N>& was) {
+  auto take = [&](uint32_t key, uint32_t next, const Part<G, N>& v, const Part<W, N>& was) {
     if (MODE == kDense)
       clear_to(key);
 #pragma unroll
-    for (int e = 0; e < N; ++e)
+    for (int e = 0; e < P; ++e)
       acc[e] += v.f32(e);
     carry_row = (int32_t)key;
     if (next == key)
       return;
     if (begun) {
-      store_f32<float, N>(m.head + (int64_t)p * m.width + c, acc);
+      store_part<float, N>(m.head + (int64_t)p * m.width + c, acc, m.lanes, left);
       head_row = carry_row;
     } else {
 #pragma unroll
-      for (int e = 0; e < N; ++e)
+      for (int e = 0; e < P; ++e)
         acc[e] = MODE == kAdd ? fmaf(m.scale, acc[e], was.f32(e)) : m.scale * acc[e];
-      store_f32<W, N>(out + (int64_t)key * m.width, acc);
+      store_part<W, N>(out + (int64_t)key * m.width, acc, m.lanes, left);
     }
     begun = false;
     carry_row = -1;
 #pragma unroll
-    for (int e = 0; e < N; ++e)
+    for (int e = 0; e < P; ++e)
       acc[e] = 0;
   };
   auto key_at = [&](uint32_t i) { return i < m.n ? m.key(i) : m.vocab; };
@@ -344,20 +347,20 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
       key = next;
     }
   } else {
-    constexpr int U = 8;
+    constexpr int U = MODE == kAdd ? 4 : 8;
     for (uint32_t i = a0; i < a1; i += U) {
       uint32_t key[U + 1]; // vocab: none
-      Vec<G, N> v[U];
-      Vec<W, N> was[U];
+      Part<G, N> v[U];
+      Part<W, N> was[U];
 #pragma unroll
       for (int u = 0; u <= U; ++u)
         key[u] = key_at(i + u);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (i + u < a1 && key[u] < m.vocab)
-          v[u] = load<G, N>(grad + m.at(i + u) * stride);
+          v[u] = load_part<G, N>(grad + m.at(i + u) * stride, m.lanes, left);
         if (MODE == kAdd && i + u < a1 && key[u] < m.vocab && key[u + 1] != key[u])
-          was[u] = load<W, N>(out + (int64_t)key[u] * m.width);
+          was[u] = load_part<W, N>(out + (int64_t)key[u] * m.width, m.lanes, left);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -368,7 +371,7 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
   if (MODE == kDense)
     clear_to((uint32_t)(d[1] - a1));
   if (carry_row >= 0)
-    store_f32<float, N>(m.carry + (int64_t)p * m.width + c, acc);
+    store_part<float, N>(m.carry + (int64_t)p * m.width + c, acc, m.lanes, left);
   if (c == 0) {
     m.head_row[p] = head_row;
     m.carry_row[p] = carry_row;
@@ -559,7 +562,7 @@ extern "C" int segtopk_embedding(segtopk_dtype dtype, const void* table, int64_t
       auto go = [&](auto n, auto id) {
         constexpr int V = decltype(n)::value;
         using I = decltype(id);
-        const int lanes = lanes_for((width / V + kInFlight - 1) / kInFlight, kThreads);
+        const int lanes = lanes_for((parts_of(width, V) + kInFlight - 1) / kInFlight, kThreads);
         const int64_t per_block = kThreads / lanes;
         return finish(launch(lookup_kernel<T, O, V, I>, dim3((unsigned)((num_tokens + per_block - 1) / per_block)),
                              kThreads, 0, (cudaStream_t)stream, (const T*)table, row_stride, vocab, (const I*)tokens,
@@ -656,8 +659,8 @@ extern "C" int segtopk_embedding_backward(segtopk_dtype dtype, const void* grad_
         m.vocab = (uint32_t)vocab;
         m.width = width;
         // no share without a step: a row's shares have to be neighbours
-        m.lanes = lanes_for(width / V, kThreads);
-        const int64_t cols = (int64_t)m.lanes * V, tiles = (width + cols - 1) / cols;
+        m.lanes = lanes_for(parts_of(width, V), kThreads);
+        const int64_t cols = (int64_t)m.lanes * (V > 1 ? V : kLoose), tiles = (width + cols - 1) / cols;
         m.shares = std::min(l.most_shares, shares_of((int64_t)n + (MODE == kDense ? vocab : 0), m.lanes * tiles));
         m.scale = scale;
         m.head = (float*)piece(l.parts);

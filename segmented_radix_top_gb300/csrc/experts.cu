@@ -65,12 +65,23 @@ dispatch_kernel(const T* x, int64_t stride, Shape s, const int32_t* row_of_slot,
     return;
   const int32_t* at = row_of_slot + (int64_t)t * s.k;
   const uint32_t slots = s.tokens * (uint32_t)s.k;
-  for (int64_t c = lane; c < s.width; c += s.lanes) {
-    const T v = x[(int64_t)t * stride + c];
+  x += (int64_t)t * stride;
+  constexpr int U = 4; // units in flight
+  for (int64_t c0 = lane; c0 < s.width; c0 += U * s.lanes) {
+    T v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + u * s.lanes < s.width)
+        v[u] = x[c0 + u * s.lanes];
     for (int j = 0; j < s.k; ++j) {
       const int32_t r = row_at(at + j, slots);
-      if (r >= 0)
-        rows[(int64_t)r * s.width + c] = v;
+      if (r >= 0) {
+        T* to = rows + (int64_t)r * s.width;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (c0 + u * s.lanes < s.width)
+            to[c0 + u * s.lanes] = v[u];
+      }
     }
   }
   clear_tail(s, kept, t, lane, s.width, rows);
@@ -92,17 +103,18 @@ combine_kernel(const T* rows, int64_t stride, Shape s, const int32_t* row_of_slo
   const int32_t* at = row_of_slot + (int64_t)t * s.k;
   const uint32_t slots = s.tokens * (uint32_t)s.k;
   const float* w = weights + (int64_t)t * s.k;
-  for (int64_t c = (int64_t)lane * N; c < s.width; c += (int64_t)s.lanes * N) {
-    float acc[N] = {};
+  constexpr int P = kPart<N>;
+  for (int64_t c = part_start<N>(lane); c < s.width; c += (int64_t)s.lanes * P) {
+    float acc[P] = {};
     // eight rows in flight; summed in the order of the slots
     for (int j0 = 0; j0 < s.k; j0 += 8) {
-      Vec<T, N> v[8];
+      Part<T, N> v[8];
       int32_t r[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         r[j] = j0 + j < s.k ? row_at(at + j0 + j, slots) : -1;
         if (r[j] >= 0)
-          v[j] = load<T, N>(rows + r[j] * stride + c);
+          v[j] = load_part<T, N>(rows + r[j] * stride + c, s.lanes, s.width - c);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -110,11 +122,11 @@ combine_kernel(const T* rows, int64_t stride, Shape s, const int32_t* row_of_slo
           continue;
         const float wj = WEIGHTED ? *(w + j0 + j) : 1.0f;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+        for (int i = 0; i < P; ++i)
           acc[i] = fmaf(wj, v[j].f32(i), acc[i]);
       }
     }
-    store_f32<T, N>(out + (int64_t)t * s.width + c, acc);
+    store_part<T, N>(out + (int64_t)t * s.width + c, acc, s.lanes, s.width - c);
   }
 }
 
@@ -126,7 +138,7 @@ combine_backward_kernel(const T* grad, int64_t grad_stride, const T* rows, int64
                         const int32_t* row_of_slot, const float* weights, const int64_t* kept, T* grad_rows,
                         float* grad_weights)
 {
-  constexpr int N = 1;
+  constexpr int P = kPart<1>;
   __shared__ float part[kThreads / 32][8];
   wait_for_previous();
   allow_next();
@@ -147,28 +159,25 @@ combine_backward_kernel(const T* grad, int64_t grad_stride, const T* rows, int64
       wj[j] = r[j] >= 0 ? *(w + j0 + j) : 0.0f;
     }
     if (some)
-      for (int64_t c = (int64_t)lane * N; c < s.width; c += (int64_t)s.lanes * N) {
-        float g[N];
-        const Vec<T, N> got = load<T, N>(grad + (int64_t)t * grad_stride + c);
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          g[i] = got.f32(i);
-        Vec<T, N> v[8];
+      for (int64_t c = part_start<1>(lane); c < s.width; c += (int64_t)s.lanes * P) {
+        const int64_t left = s.width - c;
+        const Part<T, 1> g = load_part<T, 1>(grad + (int64_t)t * grad_stride + c, s.lanes, left);
+        Part<T, 1> v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           if (r[j] >= 0)
-            v[j] = load<T, N>(rows + r[j] * stride + c);
+            v[j] = load_part<T, 1>(rows + r[j] * stride + c, s.lanes, left);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (r[j] < 0)
             continue;
-          float y[N];
+          float y[P];
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            dot[j] = fmaf(v[j].f32(i), g[i], dot[j]);
-            y[i] = wj[j] * g[i];
+          for (int i = 0; i < P; ++i) {
+            dot[j] = fmaf(v[j].f32(i), g.f32(i), dot[j]); // zeros past the row's end
+            y[i] = wj[j] * g.f32(i);
           }
-          store_f32<T, N>(grad_rows + r[j] * s.width + c, y);
+          store_part<T, 1>(grad_rows + r[j] * s.width + c, y, s.lanes, left);
         }
       }
     // the lanes' parts of each product, always added in the same order
@@ -484,7 +493,11 @@ extern "C" int segtopk_dispatch(const void* x, int32_t element_bytes, int64_t to
   const uint64_t bits = (uint64_t)(uintptr_t)x | (uint64_t)(uintptr_t)rows | row | step;
   auto move = [&](auto unit) {
     using T = decltype(unit);
-    const Shape s = {(uint32_t)tokens, k, (int64_t)(row / sizeof(T)), lanes_for((int64_t)(row / sizeof(T)), kThreads)};
+    const int64_t units = (int64_t)(row / sizeof(T));
+    // a thread for every 16 bytes, so that few tokens are soon done (1237
+    // rows of 4000 bytes, k = 6: 5.4 us, with four units a thread 6.4); of
+    // smaller units each takes four
+    const Shape s = {(uint32_t)tokens, k, units, lanes_for(sizeof(T) == 16 ? units : (units + 3) / 4, kThreads)};
     return finish(launch(dispatch_kernel<T>, grid_of(s), kThreads, 0, (cudaStream_t)stream, (const T*)x,
                          (int64_t)(step / sizeof(T)), s, row_of_slot, kept, (T*)rows), 1);
   };
@@ -522,7 +535,7 @@ extern "C" int segtopk_combine(segtopk_dtype dtype, const void* rows, int64_t to
       return bad;
     auto go = [&](auto n) {
       constexpr int V = decltype(n)::value;
-      const Shape s = {(uint32_t)tokens, k, width, lanes_for(width / V, kThreads)};
+      const Shape s = {(uint32_t)tokens, k, width, lanes_for(parts_of(width, V), kThreads)};
       if constexpr (V > 1) {
         const int64_t cols = (int64_t)s.lanes * V, tiles = (width + cols - 1) / cols;
         // runs pay once they are long: 1237 tokens of 1000 in f32, k = 6, take
@@ -573,7 +586,7 @@ extern "C" int segtopk_combine_backward(segtopk_dtype dtype, const void* grad_ou
       return bad;
     auto go = [&](auto n) {
       constexpr int V = decltype(n)::value;
-      const Shape s = {(uint32_t)tokens, k, width, lanes_for(width / V, kThreads)};
+      const Shape s = {(uint32_t)tokens, k, width, lanes_for(parts_of(width, V), kThreads)};
       if constexpr (V > 1) {
         const Run run = run_of(s, 1, sms);
         return finish(launch(combine_backward_run_kernel<T, V>, grid_of(run, 1), kThreads, kAheadBack * kThreads * 16,
