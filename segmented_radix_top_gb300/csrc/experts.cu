@@ -51,22 +51,11 @@ __device__ __forceinline__ void clear_tail(const Shape& s, const int64_t* kept, 
       rows[r * units + c] = U{};
 }
 
-// Elements are moved as they are: T is an unsigned integer of their size or
-// of several of them.
-template <class T>
-__global__ void __launch_bounds__(kThreads)
-dispatch_kernel(const T* x, int64_t stride, Shape s, const int32_t* row_of_slot, const int64_t* kept, T* rows)
+// U units of a token's row at a time, from the lane's first on.
+template <int U, class T>
+__device__ __forceinline__ void copy_units(const T* x, const Shape& s, const int32_t* at, int lane, T* rows)
 {
-  wait_for_previous();
-  allow_next();
-  int lane;
-  const uint32_t t = group_token(s, &lane);
-  if (t >= s.tokens)
-    return;
-  const int32_t* at = row_of_slot + (int64_t)t * s.k;
   const uint32_t slots = s.tokens * (uint32_t)s.k;
-  x += (int64_t)t * stride;
-  constexpr int U = 4; // units in flight
   for (int64_t c0 = lane; c0 < s.width; c0 += U * s.lanes) {
     T v[U];
 #pragma unroll
@@ -84,6 +73,26 @@ dispatch_kernel(const T* x, int64_t stride, Shape s, const int32_t* row_of_slot,
       }
     }
   }
+}
+
+// Elements are moved as they are: T is an unsigned integer of their size or
+// of several of them. Bound by the k rows written for each one read.
+template <class T>
+__global__ void __launch_bounds__(kThreads)
+dispatch_kernel(const T* x, int64_t stride, Shape s, const int32_t* row_of_slot, const int64_t* kept, T* rows)
+{
+  wait_for_previous();
+  allow_next();
+  int lane;
+  const uint32_t t = group_token(s, &lane);
+  if (t >= s.tokens)
+    return;
+  x += (int64_t)t * stride;
+  const int32_t* at = row_of_slot + (int64_t)t * s.k;
+  if (s.width <= s.lanes)
+    copy_units<1>(x, s, at, lane, rows);
+  else
+    copy_units<4>(x, s, at, lane, rows);
   clear_tail(s, kept, t, lane, s.width, rows);
 }
 
