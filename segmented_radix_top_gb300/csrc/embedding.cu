@@ -92,6 +92,7 @@ struct TokenSource {
 // 5 us at kFewTokens, where the cluster sort takes 9. The blocks past those
 // clear the table meanwhile, where most of its rows have no token.
 constexpr int64_t kFewTokens = 8192;
+constexpr size_t kClearBlocks = 64 * kSms;
 
 template <class I>
 __global__ void __launch_bounds__(kThreads)
@@ -159,6 +160,7 @@ struct Merge {
   uint32_t vocab;
   int64_t width;
   uint32_t shares;
+  uint32_t reach; // see row_end()
   int lanes;
   float scale;
   float *head, *carry;          // [shares][width]: parts of rows that several shares hold
@@ -166,6 +168,23 @@ struct Merge {
   __device__ __forceinline__ uint32_t key(uint32_t i) const { return (uint32_t)items[i]; }
   __device__ __forceinline__ int64_t at(uint32_t i) const { return (int64_t)(items[i] >> 32); }
 };
+
+// A share's end (a position) moved past the end of the row it falls into, if
+// that is among the next m.reach positions (or as many as the group has lanes
+// in a warp). Only the rows of frequent tokens are then held by several
+// shares. Short shares have a reach of 0: their sizes would differ too much
+// (27 positions a share: 33 us as they are, 38 moved by up to 32).
+__device__ __forceinline__ uint32_t row_end(const Merge& m, uint32_t a)
+{
+  if (m.reach == 0)
+    return a;
+  const uint32_t g = min(m.lanes, 32), lane = threadIdx.x & 31, mine = lane & (g - 1);
+  const unsigned mask = (g == 32 ? kAll : ((1u << g) - 1)) << (lane - mine);
+  const uint32_t row = a > 0 ? m.key(a - 1) : 0;
+  const bool other = mine <= m.reach && (a + mine >= m.n || m.key(a + mine) != row);
+  const unsigned found = __ballot_sync(mask, other) >> (lane - mine);
+  return a > 0 && found != 0 ? a + __ffs(found) - 1 : a;
+}
 
 // What becomes of the table:
 enum Mode {
@@ -259,23 +278,43 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
   uint32_t a[2] = {(uint32_t)d[0], (uint32_t)d[1]};
   if (MODE == kDense)
     positions_before(m, d, a);
-  if (c >= m.width)
-    return;
+  const uint32_t starts = row_end(m, a[0]), ends = row_end(m, a[1]);
+  if (N > 1 && c >= m.width)
+    return; // loose elements are guarded one by one
+  W* const table = out;
   out += c;
-  const uint32_t a0 = a[0], a1 = a[1];
+  const uint32_t a0 = starts, a1 = ends;
   const uint32_t before = a0 > 0 ? m.key(a0 - 1) : m.vocab;
   bool begun = a0 < a1 && m.key(a0) == before; // the first position's row, by an earlier share
   uint32_t empty = 0;                           // kDense: the next row that may have no position
   if (MODE == kDense) {
-    empty = (uint32_t)(d[0] - a0);
+    empty = (uint32_t)(d[0] - a[0]);
     empty += empty == before;
   }
   auto clear_to = [&](uint32_t row) {
-    W* to = out + (int64_t)empty * m.width;
-    const float zero[P] = {};
+    if constexpr (N > 1) {
+      W* to = out + (int64_t)empty * m.width;
+      const Vec<W, N> zero = {};
 #pragma unroll 4
-    for (; empty < row; ++empty, to += m.width)
-      store_part<W, N>(to, zero, m.lanes, left);
+      for (; empty < row; ++empty, to += m.width)
+        store<W, N>(to, zero);
+    } else if (empty < row) {
+      // the rows are one run of memory: whole 16 bytes of it, whatever the
+      // width, a part for each of the blocks that share its columns
+      const int64_t all = (int64_t)(row - empty) * m.width;
+      W* from = table + (int64_t)empty * m.width + all * blockIdx.y / gridDim.y;
+      W* const to = table + (int64_t)empty * m.width + all * (blockIdx.y + 1) / gridDim.y;
+      const int64_t edge = min((int64_t)((16 - ((uintptr_t)from & 15)) & 15) / (int64_t)sizeof(W), to - from);
+      for (int64_t e = lane; e < edge; e += m.lanes)
+        from[e] = from_f32<W>(0.0f);
+      from += edge;
+      const int64_t whole = (to - from) * (int64_t)sizeof(W) / 16;
+#pragma unroll 4
+      for (int64_t v = lane; v < whole; v += m.lanes)
+        reinterpret_cast<uint4*>(from)[v] = uint4{};
+      for (W* e = from + whole * 16 / (int64_t)sizeof(W) + lane; e < to; e += m.lanes)
+        *e = from_f32<W>(0.0f);
+    }
     empty = row + 1;
   };
 
@@ -369,7 +408,7 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
     }
   }
   if (MODE == kDense)
-    clear_to((uint32_t)(d[1] - a1));
+    clear_to((uint32_t)(d[1] - a[1]));
   if (carry_row >= 0)
     store_part<float, N>(m.carry + (int64_t)p * m.width + c, acc, m.lanes, left);
   if (c == 0) {
@@ -379,25 +418,20 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
 }
 
 // A row that began in shares before p and ended in p: the parts that those
-// left, in their order, and p's own. A block serves one share and kJoinCols
-// columns, a thread four of them. The row of a frequent token has parts in
+// left, in their order, and p's own. A block looks at one share or several
+// and serves kJoinCols columns, a thread four of them. The row of a frequent token has parts in
 // many shares: from kJoinSplit on, each warp sums a run of them over all the
 // block's columns, and the runs' sums are added in order.
+constexpr uint32_t kJoinShares = 8; // where most have no such row, else one
 constexpr int kJoinCols = kThreads * 4;
 constexpr uint32_t kJoinSplit = 48;
 
 template <class W, int N, Mode MODE>
-__global__ void __launch_bounds__(kThreads) join_kernel(Merge m, W* out)
+__device__ __forceinline__ void join_row(const Merge& m, uint32_t p, int32_t row, W* out,
+                                         float (*part)[kJoinCols])
 {
   constexpr int kWarps = kThreads / 32;
   constexpr int kTiles = kJoinCols / (32 * N); // a warp's accesses for the block's columns
-  __shared__ float part[kWarps][kJoinCols];
-  wait_for_previous();
-  allow_next();
-  const uint32_t p = blockIdx.x;
-  const int32_t row = m.head_row[p];
-  if (row < 0)
-    return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t first = p; // of the shares that hold a part
   for (bool more = true; more;) {
@@ -472,6 +506,23 @@ __global__ void __launch_bounds__(kThreads) join_kernel(Merge m, W* out)
   }
 }
 
+template <class W, int N, Mode MODE>
+__global__ void __launch_bounds__(kThreads) join_kernel(Merge m, W* out)
+{
+  __shared__ float part[kThreads / 32][kJoinCols];
+  wait_for_previous();
+  allow_next();
+  const uint32_t count = m.reach > 0 ? kJoinShares : 1;
+  const uint32_t first = blockIdx.x * count, lane = threadIdx.x & 31;
+  const bool mine = lane < count && first + lane < m.shares;
+  const int32_t row = mine ? m.head_row[first + lane] : -1; // every warp the same ones
+  for (unsigned left = __ballot_sync(kAll, row >= 0); left != 0; left &= left - 1) {
+    const int i = __ffs(left) - 1;
+    join_row<W, N, MODE>(m, first + i, __shfl_sync(kAll, row, i), out, part);
+    __syncthreads(); // part is written again
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
@@ -489,7 +540,7 @@ struct Layout {
 uint32_t shares_of(int64_t steps, int64_t row_threads)
 {
   const int64_t resident = std::max<int64_t>(1, kSms * 1024 / std::max<int64_t>(1, row_threads));
-  const int64_t waves = std::min<int64_t>(6, std::max<int64_t>(1, steps / (32 * resident)));
+  const int64_t waves = std::min<int64_t>(9, std::max<int64_t>(1, steps / (32 * resident)));
   return (uint32_t)std::max<int64_t>(1, std::min<int64_t>(resident * waves, (steps + 7) / 8));
 }
 
@@ -639,7 +690,7 @@ extern "C" int segtopk_embedding_backward(segtopk_dtype dtype, const void* grad_
             return sort<false>(l.sort, src, ItemSink{items}, copies, counts, st, &e);
           const uint32_t places = (n + 31) / 32;
           const size_t bytes = clear_first ? (size_t)vocab * (size_t)width * sizeof(W) : 0;
-          const uint32_t clears = (uint32_t)std::min<size_t>(4 * kSms, (bytes + (1 << 14) - 1) >> 14);
+          const uint32_t clears = (uint32_t)std::min<size_t>(kClearBlocks, (bytes + (1 << 14) - 1) >> 14);
           e = launch(place_kernel<I>, dim3(places + clears), kThreads, (size_t)places * 128, st, src, n, places, items,
                      (char*)grad_table, bytes);
           return e == cudaSuccess ? 1 : -1;
@@ -662,6 +713,8 @@ extern "C" int segtopk_embedding_backward(segtopk_dtype dtype, const void* grad_
         m.lanes = lanes_for(parts_of(width, V), kThreads);
         const int64_t cols = (int64_t)m.lanes * (V > 1 ? V : kLoose), tiles = (width + cols - 1) / cols;
         m.shares = std::min(l.most_shares, shares_of((int64_t)n + (MODE == kDense ? vocab : 0), m.lanes * tiles));
+        const uint32_t a_share = (uint32_t)(((int64_t)n + (MODE == kDense ? vocab : 0)) / m.shares);
+        m.reach = a_share >= 64 ? std::min(32u, a_share / 4) : 0;
         m.scale = scale;
         m.head = (float*)piece(l.parts);
         m.carry = (float*)piece(l.parts);
@@ -672,7 +725,8 @@ extern "C" int segtopk_embedding_backward(segtopk_dtype dtype, const void* grad_
         e = launch(merge_kernel<G, W, V, MODE>, grid, kThreads, Ring<G, W, V, MODE>::kBytes, st, m,
                    (const G*)grad_out, grad_stride, (W*)grad_table);
         constexpr int J = V > 4 ? 4 : V; // columns of a thread: 16 bytes of the parts
-        const dim3 joins(m.shares, (unsigned)((width + kJoinCols - 1) / kJoinCols));
+        const uint32_t looks = m.reach > 0 ? kJoinShares : 1; // of a block: see join_kernel
+        const dim3 joins((m.shares + looks - 1) / looks, (unsigned)((width + kJoinCols - 1) / kJoinCols));
         if (e == cudaSuccess)
           e = launch(join_kernel<W, J, MODE>, joins, kThreads, 0, st, m, (W*)grad_table);
         return finish(e, launches + 2);

@@ -155,8 +155,8 @@ __device__ __forceinline__ int part_start(int lane)
 {
   return N > 1 ? lane * N : lane;
 }
-// p: the part's first element, which is inside the row; `left`: columns of
-// the row from there on.
+// p: the part's first element; left: columns of the row from there on (none
+// are read or written past them).
 template <class T, int N>
 __device__ __forceinline__ Part<T, N> load_part(const T* p, int lanes, int64_t left)
 {
