@@ -86,69 +86,36 @@ struct TokenSource {
   __device__ __forceinline__ uint32_t at(uint32_t i) const { return i; }
 };
 
-// Few tokens are placed by counting instead: an item's place is the number of
-// items before it by (key, position). A block places 32 of them, each warp
-// counting over an eighth of all; n^2 comparisons over the whole GPU, about
-// 5 us at kFewTokens, where the cluster sort takes 9. The blocks past those
-// clear the table meanwhile, where most of its rows have no token.
-constexpr int64_t kFewTokens = 8192;
-constexpr size_t kClearBlocks = 64 * kSms;
-
-template <class I>
-__global__ void __launch_bounds__(kThreads)
-place_kernel(TokenSource<I> src, uint32_t n, uint32_t place_blocks, uint64_t* items, char* clear, size_t clear_bytes)
+// Clears the table while the sort, launched before it, still runs: the sort's
+// cluster lets the next kernel start once all its blocks have seen the work
+// before them complete, and this one waits for the sort only at its end, so
+// that the kernel after it finds both done. (The other order would not do: a
+// sort launched second would wait for the clearing first.) Bound by the
+// writes. 2048 tokens of 32000 rows of 4 KB: 30 us in all, 40 where the merge
+// writes every row after the sort; 34 with a block for every 16 KB, whose
+// first wave then holds the SMs until the sort ends.
+constexpr size_t kClearRun = 32 << 10;
+__global__ void __launch_bounds__(kThreads) clear_kernel(char* at, size_t bytes)
 {
-  extern __shared__ uint4 place_keys[];
-  __shared__ uint32_t part[kThreads / 32][32];
-  wait_for_previous();
   allow_next();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x >= place_blocks) {
-    const size_t first = (size_t)(blockIdx.x - place_blocks) * kThreads + threadIdx.x;
-    const size_t step = (size_t)(gridDim.x - place_blocks) * kThreads;
-    if ((((size_t)clear | clear_bytes) & 15) == 0) {
-#pragma unroll 4
-      for (size_t i = first; i < clear_bytes / 16; i += step)
-        reinterpret_cast<uint4*>(clear)[i] = uint4{};
+  // a block clears runs of consecutive memory
+  constexpr int U = kClearRun / (kThreads * 16);
+  const bool whole = (((size_t)at | bytes) & 15) == 0;
+  for (size_t run = (size_t)blockIdx.x * kClearRun; run < bytes; run += (size_t)gridDim.x * kClearRun) {
+    if (whole) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const size_t i = run + (size_t)(u * kThreads + threadIdx.x) * 16;
+        if (i < bytes)
+          *reinterpret_cast<uint4*>(at + i) = uint4{};
+      }
     } else {
-#pragma unroll 4
-      for (size_t i = first; i < clear_bytes / 2; i += step)
-        reinterpret_cast<uint16_t*>(clear)[i] = 0;
+      const size_t end = min(bytes, run + kClearRun);
+      for (size_t i = run + threadIdx.x * 2; i < end; i += kThreads * 2)
+        *reinterpret_cast<uint16_t*>(at + i) = 0;
     }
-    return;
   }
-  uint32_t* keys = reinterpret_cast<uint32_t*>(place_keys);
-  const uint32_t groups = (n + 31) / 32;
-#pragma unroll 4
-  for (uint32_t i = threadIdx.x; i < groups * 32; i += kThreads)
-    keys[i] = i < n ? src.key(i) : ~0u; // past every item
-  __syncthreads();
-  const uint32_t i = blockIdx.x * 32 + lane, key = keys[i];
-  uint32_t before = 0;
-  // items of earlier positions count with an equal key, later ones do not
-  auto count = [&](uint32_t g, auto earlier) {
-    const uint4* at = place_keys + g * 8;
-#pragma unroll
-    for (int v = 0; v < 8; ++v) {
-      const uint4 k = at[v];
-      before += earlier(k.x, v * 4) + earlier(k.y, v * 4 + 1) + earlier(k.z, v * 4 + 2) + earlier(k.w, v * 4 + 3);
-    }
-  };
-  const uint32_t g0 = groups * warp / 8, g1 = groups * (warp + 1) / 8, own = blockIdx.x;
-  for (uint32_t g = g0; g < min(g1, own); ++g)
-    count(g, [&](uint32_t k, int) { return k <= key; });
-  if (own >= g0 && own < g1)
-    count(own, [&](uint32_t k, int j) { return k < key || (k == key && j < lane); });
-  for (uint32_t g = max(g0, own + 1); g < g1; ++g)
-    count(g, [&](uint32_t k, int) { return k < key; });
-  part[warp][lane] = before;
-  __syncthreads();
-  if (warp > 0 || i >= n)
-    return;
-#pragma unroll
-  for (int w = 1; w < kThreads / 32; ++w)
-    before += part[w][lane];
-  items[before] = pack(key, i);
+  wait_for_previous();
 }
 
 // ---------------------------------------------------------------------------
@@ -528,7 +495,6 @@ __global__ void __launch_bounds__(kThreads) join_kernel(Merge m, W* out)
 // ---------------------------------------------------------------------------
 struct Layout {
   SortPlan sort;
-  bool few; // placed by counting, not sorted
   uint32_t most_shares;                         // of any call with these sizes
   size_t items, copy, counts, parts, rows, total; // bytes of each piece
 };
@@ -555,7 +521,6 @@ Layout layout_of(int64_t n, int64_t vocab, int64_t width)
   const int passes = (bits + kDigitBits - 1) / kDigitBits, digit_bits = (bits + passes - 1) / passes;
   l.sort = sort_plan(n, passes, digit_bits, 1 << digit_bits);
   l.most_shares = shares_of(n + vocab, (width + 7) / 8); // eight columns a thread: the fewest threads
-  l.few = n <= kFewTokens;
   l.items = round_up((size_t)n * 8);
   l.copy = round_up(l.sort.copy());
   l.counts = round_up(l.sort.counts());
@@ -565,6 +530,8 @@ Layout layout_of(int64_t n, int64_t vocab, int64_t width)
   return l;
 }
 
+constexpr size_t kClearBlocks = 7 * kSms;
+constexpr int64_t kFewOf = 4; // tokens are few of a table's rows if not more than one in as many
 constexpr int64_t kMaxVocab = 2147483646LL;
 bool fits(int64_t n, int64_t vocab, int64_t width)
 {
@@ -677,27 +644,31 @@ extern "C" int segtopk_embedding_backward(segtopk_dtype dtype, const void* grad_
       cudaStream_t st = (cudaStream_t)stream;
       cudaError_t e = cudaSuccess;
       const uint32_t n = (uint32_t)num_tokens;
-      // Clearing the table beside the placing and then writing the tokens'
-      // rows writes those twice: worth it where they are few of all. 2048 of
-      // 32000 rows of 4 KB: 41.7 us the dense way.
-      const bool clear_first = !accumulate && l.few && num_tokens <= vocab / 4;
+      // Clearing the table beside the sort, on the SMs that a cluster leaves,
+      // and then writing the tokens' rows writes those twice: worth it where
+      // they are few of all (32000 rows of 4 KB: 2048 tokens 28 against 38 us,
+      // 4096 31 against 41, 8192 44 against 45).
+      const bool clear_first = !accumulate && l.sort.tiles.items == 0 && num_tokens <= vocab / kFewOf;
       int launches = 0;
-      if (n > 0 || clear_first) {
+      if (n > 0 || clear_first) { // the clearing follows a sort, of no tokens too
         auto by = [&](auto id) {
           using I = decltype(id);
-          const TokenSource<I> src = {(const I*)tokens, vocab, padding_token};
-          if (!l.few)
-            return sort<false>(l.sort, src, ItemSink{items}, copies, counts, st, &e);
-          const uint32_t places = (n + 31) / 32;
-          const size_t bytes = clear_first ? (size_t)vocab * (size_t)width * sizeof(W) : 0;
-          const uint32_t clears = (uint32_t)std::min<size_t>(kClearBlocks, (bytes + (1 << 14) - 1) >> 14);
-          e = launch(place_kernel<I>, dim3(places + clears), kThreads, (size_t)places * 128, st, src, n, places, items,
-                     (char*)grad_table, bytes);
-          return e == cudaSuccess ? 1 : -1;
+          return sort<false>(l.sort, TokenSource<I>{(const I*)tokens, vocab, padding_token}, ItemSink{items}, copies,
+                             counts, st, &e);
         };
         launches = token_bytes == 4 ? by(int32_t{}) : by(int64_t{});
         if (launches < 0)
           return record_cuda_error(e);
+      }
+      if (clear_first) {
+        const size_t bytes = (size_t)vocab * (size_t)width * sizeof(W);
+        // fewer blocks than fill the SMs: one that has cleared its runs stays
+        // until the sort is done, and the merge's blocks come in beside them
+        const unsigned blocks = (unsigned)std::min<size_t>(kClearBlocks, (bytes + kClearRun - 1) / kClearRun);
+        e = launch(clear_kernel, dim3(blocks), kThreads, 0, st, (char*)grad_table, bytes);
+        if (e != cudaSuccess)
+          return record_cuda_error(e);
+        ++launches;
       }
       if (clear_first && n == 0)
         return finish(e, launches);

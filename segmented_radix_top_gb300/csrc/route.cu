@@ -9,10 +9,14 @@
 // new ties. Weights: c s_i, or c s_i / (sum of the chosen scores).
 //
 // One warp serves a token: its lanes hold the row in registers (NV
-// consecutive logits each), so the row is read once. What bounds the kernels
-// is the instructions a row takes, about twice its bytes' time at 256
-// experts, so the k best are not searched for one after the other: see
-// choose() below.
+// consecutive logits each), so the row is read once. 65536 rows of 256 in
+// f32, k = 8, weights from the full softmax: 25 us, 10.5 at the copy rate;
+// bound by issue (385 instructions a row, 83 % of the issue slots), which is
+// why the k best are not searched for one after the other, see choose(). A
+// warp that fetches its next row ahead, or blocks that stay, were slower (28
+// to 30 us): the registers cost more warps than the loads cost time. The
+// backward pass reads the row again and writes it: 24 us, 20.4 at the copy
+// rate, bound by memory.
 #include "rows.cuh"
 
 namespace segtopk {
@@ -143,8 +147,8 @@ __device__ __forceinline__ float chosen_weight(float l, bool on, bool renormaliz
 // counts the entries ahead of its own. The rounds (k times: find the best,
 // take it out) are left for k above 16, where the list overflows, for rows
 // that overflow it by ties at the bound or hold NaN, and for the shares
-// where they are as fast. 65536 rows of 256, k = 8, on GB300: 51 us by rounds,
-// 29 with the list.
+// where they are as fast. 65536 rows of 256, k = 8, on GB300: 50 us by rounds,
+// 24 with the list; k = 2: 22 and 19; rows of 64, k = 6: 17.3 and 18.7.
 constexpr int kListCap = 32;
 struct Choice {
   uint64_t ranked[kListCap]; // code, and ~expert: larger is ahead, ties go to the lower expert

@@ -22,11 +22,12 @@ constexpr uint32_t kAll = 0xffffffffu;
 // ---------------------------------------------------------------------------
 // Every row kernel is launched as a programmatic dependent of the kernel
 // before it on its stream: its blocks may be scheduled while that kernel
-// drains, and wait_for_previous() (the first thing each of them does, before
-// any access to global memory) holds them until that kernel has completed
-// and its writes are visible. A chain of such kernels stays in order, since
-// none completes before its own wait has ended. allow_next() lets the next
-// kernel's blocks be scheduled; it promises nothing about memory.
+// drains, and wait_for_previous() (before any access to global memory, but
+// for the one kernel that says otherwise) holds them until that kernel has
+// completed and its writes are visible. A chain of such kernels stays in
+// order, since none completes before its own wait has ended. allow_next()
+// lets the next kernel's blocks be scheduled once all blocks have called it
+// or ended; it promises nothing about memory.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;"); }
 
