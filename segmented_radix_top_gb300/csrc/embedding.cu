@@ -35,6 +35,8 @@ __device__ __forceinline__ int64_t row_of_token(const I* tokens, uint32_t i, int
 // ---------------------------------------------------------------------------
 // Forward: a group of `lanes` threads copies a row
 // ---------------------------------------------------------------------------
+// Bound by memory with kInFlight vectors a thread under way: 65536 rows of
+// 4096 in bf16 114 us, 103 at the copy rate (142 with one vector).
 template <class T, class O, int N, class I>
 __global__ void __launch_bounds__(kThreads)
 lookup_kernel(const T* table, int64_t stride, int64_t vocab, const I* tokens, uint32_t n, int64_t width, int lanes,
@@ -211,7 +213,9 @@ __device__ __forceinline__ void positions_before(const Merge& m, const uint64_t 
 // way: every thread copies its part of the next kAhead positions' rows (and,
 // when adding, of the table rows that they complete) into shared memory of
 // its own with asynchronous copies, which takes no registers and, as no
-// thread reads another's part, no barrier. Elements too badly aligned for
+// thread reads another's part, no barrier. 65536 tokens of a table of 152064
+// rows of 4096 in bf16: about 270 us for 1.8 GB (262 at the copy rate), 312
+// with four rows under way in registers. Elements too badly aligned for
 // that (N = 1) go in batches through registers.
 template <class G, class W, int N, Mode MODE>
 struct Ring {

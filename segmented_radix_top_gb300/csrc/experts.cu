@@ -8,7 +8,9 @@
 // r(t, j) is the row of token t's j-th slot, or none. Every kernel goes by
 // token, so a token's row is read or written once and only the k sorted rows
 // are scattered; all are bound by memory bandwidth, if the gathered rows are
-// asked for early enough.
+// asked for early enough. 8192 tokens of 2048 in bf16, k = 8: copy 46 us, sum
+// 50, unweighted 51, backward 97 (44, 44, 44 and 84 at the copy rate); 32768
+// of 4096: copy and sum 355 each (356).
 #include "rows.cuh"
 
 namespace segtopk {
@@ -223,7 +225,8 @@ combine_backward_kernel(const T* grad, int64_t grad_stride, const T* rows, int64
 // Many tokens: a group of threads takes a run of them and copies the next
 // kAhead rows into shared memory meanwhile, across tokens. Four blocks of 48
 // KB an SM keep 192 KB under way; eight rows a thread in registers, 96 KB
-// while a block lasts and nothing while the next one starts.
+// while a block lasts and nothing while the next one starts (58 us and 102
+// for the sum and its backward above, 392 for the larger sum).
 constexpr int kAhead = kRingBytes / (kThreads * 16);
 constexpr int kAheadBack = kAhead - 1; // leaves room for the products' parts
 

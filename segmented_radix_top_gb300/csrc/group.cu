@@ -1,6 +1,7 @@
 // Token slots sorted by expert (segtopk_group in include/segtopk.h): a stable
 // counting sort with one digit, the expert; slots without an expert come
-// last and get no row.
+// last and get no row. 64 slots take 2.1 us, 7422 4.4, 65536 6.7, 262144 9.8:
+// the latency of one or two launches, not their traffic.
 #include "rank_sort.cuh"
 
 namespace segtopk {
