@@ -85,13 +85,21 @@ def _load():
 
 def _on_stream(call):
     """Gives an operator its `stream` argument: the call, its results and its
-    workspace belong to that stream."""
+    workspace belong to that stream. The tensors that it is given are held
+    for the stream, so that the memory of one dropped after the call is not
+    handed out before the stream has got there. The caller orders the stream
+    after what writes them."""
     @functools.wraps(call)
     def wrapped(*args, stream=None, **kw):
         if stream is None:
             return call(*args, **kw)
         with torch.cuda.stream(stream):
-            return call(*args, **kw)
+            result = call(*args, **kw)
+        for value in (*args, *kw.values()):
+            for t in value if isinstance(value, tuple) else (value,):
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(stream)
+        return result
     return wrapped
 
 

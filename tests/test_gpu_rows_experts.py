@@ -288,6 +288,25 @@ def test_on_another_stream_and_in_a_graph():
     ids.copy_(keep)
 
 
+def test_inputs_dropped_after_a_call_on_another_stream():
+    # the input's memory is not given to another tensor before the call has
+    # read it; a long fill keeps the stream busy meanwhile
+    side = torch.cuda.Stream()
+    groups = st.group_by_expert(ids_of(4000, 4, 16, 1).cuda(), 16)
+    busy = torch.empty(1 << 30, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        x = torch.ones(4000, 2048, device="cuda")
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                busy.fill_(1)
+        rows = st.dispatch(x, groups, stream=side)
+        del x
+        torch.full((4000, 2048), 7.0, device="cuda")
+        side.synchronize()
+        assert (rows == 1).all()
+
+
 def test_given_outputs():
     groups, rows, slots = grouped(ids_of(10, 2, 4, 1), 4)
     x, w = randn(10, 16, seed=1).cuda(), randn(10, 2, seed=2).cuda()
