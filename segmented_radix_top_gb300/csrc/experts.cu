@@ -131,7 +131,7 @@ combine_kernel(const T* rows, int64_t stride, Shape s, const int32_t* row_of_slo
       for (int j = 0; j < 8; ++j) {
         if (r[j] < 0)
           continue;
-        const float wj = WEIGHTED ? *(w + j0 + j) : 1.0f;
+        const float wj = WEIGHTED ? w[j0 + j] : 1.0f;
 #pragma unroll
         for (int i = 0; i < P; ++i)
           acc[i] = fmaf(wj, v[j].f32(i), acc[i]);
@@ -167,7 +167,7 @@ combine_backward_kernel(const T* grad, int64_t grad_stride, const T* rows, int64
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       r[j] = some && j0 + j < s.k ? row_at(at + j0 + j, slots) : -1;
-      wj[j] = r[j] >= 0 ? *(w + j0 + j) : 0.0f;
+      wj[j] = r[j] >= 0 ? w[j0 + j] : 0.0f;
     }
     if (some)
       for (int64_t c = part_start<1>(lane); c < s.width; c += (int64_t)s.lanes * P) {
