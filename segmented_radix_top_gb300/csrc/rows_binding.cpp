@@ -115,17 +115,23 @@ void want_args(Py_ssize_t n, Py_ssize_t wanted)
   TORCH_CHECK_TYPE(n == wanted, "expected ", wanted, " arguments, got ", n);
 }
 
+// Whether t's memory holds other values than t has: a view whose conjugation
+// or negation torch has put off.
+bool put_off(const at::Tensor& t) { return t.is_conj() || t.is_neg(); }
+// The values of t in memory: t, or a copy.
+at::Tensor values(const at::Tensor& t) { return put_off(t) ? t.resolve_conj().resolve_neg() : t; }
+
 // Rows of contiguous elements: t, or a copy.
 at::Tensor matrix(const at::Tensor& t, const char* name)
 {
   TORCH_CHECK_VALUE(t.dim() == 2, name, " must have two dimensions");
-  return t.stride(1) == 1 ? t : t.contiguous();
+  return values(t.stride(1) == 1 ? t : t.contiguous());
 }
 // A contiguous tensor of this shape and type: t, or a copy.
 at::Tensor dense(const at::Tensor& t, const char* name, at::IntArrayRef shape, at::ScalarType type)
 {
   TORCH_CHECK_VALUE(t.sizes() == shape && t.scalar_type() == type, name, " must be ", type, " of ", shape);
-  return t.contiguous();
+  return values(t).contiguous();
 }
 
 // The device of a call: that of its first tensor, made current if it is not.
@@ -153,8 +159,8 @@ struct Place {
     if (given == Py_None)
       return empty(shape, type);
     const at::Tensor& t = tensor(given, name);
-    TORCH_CHECK_VALUE(t.sizes() == shape && t.scalar_type() == type && t.is_contiguous(), name,
-                      " must be contiguous, ", type, " of ", shape);
+    TORCH_CHECK_VALUE(t.sizes() == shape && t.scalar_type() == type && t.is_contiguous() && !put_off(t), name,
+                      " must be contiguous, ", type, " of ", shape, " and no conjugated or negated view");
     same(t);
     return t;
   }
@@ -173,7 +179,7 @@ Groups groups_of(PyObject* o, const Place& place)
   const at::Tensor& rows = tensor(PyTuple_GET_ITEM(o, 1), "groups.row_of_slot");
   TORCH_CHECK_VALUE(offsets.scalar_type() == at::kLong && offsets.dim() == 1 && offsets.is_contiguous() &&
                       offsets.numel() > 0 && rows.scalar_type() == at::kInt && rows.dim() == 2 &&
-                      rows.is_contiguous() && rows.size(1) <= INT32_MAX,
+                      rows.is_contiguous() && rows.size(1) <= INT32_MAX && !put_off(offsets) && !put_off(rows),
                     "groups must come from group_by_expert");
   place.same(offsets);
   place.same(rows);
@@ -266,7 +272,7 @@ PyObject* group(PyObject*, PyObject* const* a, Py_ssize_t n)
   const at::Tensor& given = tensor(a[0], "expert_ids");
   const int bytes = id_bytes(given, "expert_ids");
   TORCH_CHECK_VALUE(given.dim() == 2, "expert_ids must have two dimensions");
-  const at::Tensor ids = given.contiguous();
+  const at::Tensor ids = values(given).contiguous();
   const int32_t experts = integer32(a[1], "num_experts");
   const Place place(ids);
   const int64_t slots = ids.numel();
@@ -357,7 +363,7 @@ PyObject* embedding(PyObject*, PyObject* const* a, Py_ssize_t n)
   const segtopk_dtype type = float_type(table.scalar_type(), "table");
   const at::Tensor& given = tensor(a[1], "tokens");
   const int bytes = id_bytes(given, "tokens");
-  const at::Tensor tokens = given.contiguous();
+  const at::Tensor tokens = values(given).contiguous();
   const float scale = real(a[2]);
   const Place place(table);
   place.same(tokens);
@@ -387,7 +393,7 @@ PyObject* embedding_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
   const int bytes = id_bytes(given_tokens, "tokens");
   TORCH_CHECK_VALUE(given.dim() >= 1 && given.sizes().slice(0, given.dim() - 1) == given_tokens.sizes(),
                     "grad_out must have a row for each token");
-  const at::Tensor tokens = given_tokens.contiguous();
+  const at::Tensor tokens = values(given_tokens).contiguous();
   const int64_t count = tokens.numel(), width = given.size(-1), num_rows = integer(a[2]);
   const at::Tensor grad = matrix(given.dim() == 2 ? given : given.reshape({count, width}), "grad_out");
   const float scale = real(a[3]);
