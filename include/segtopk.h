@@ -431,8 +431,10 @@ typedef enum {
  * The k best experts of each token, best first, and their weights.
  *
  * Chosen by score + bias (bias: `experts` float values, or NULL: none), ties
- * to the lower expert. Without a bias the logits are compared, which order
- * as the scores do; +0.0 and -0.0 are equal, and NaN ranks above +inf.
+ * to the lower expert. The scores and sums are those of 32 bits, so two that
+ * are less than their roundings apart may tie or change places; equal logits
+ * with equal biases always tie. Without a bias the logits are compared, which
+ * order as the scores do; +0.0 and -0.0 are equal, and NaN ranks above +inf.
  * Weights: scale * score, or with renormalize (0 or 1) scale * score / (sum
  * of the k chosen scores). The bias chooses only and is in no weight.
  *
