@@ -123,3 +123,23 @@ def test_scores_below_the_normal_numbers_are_compared(score, dtype):
     l = torch.tensor([[0.0, -90.0, -88.5], [-89.5, 0.0, -89.0], [-100.0, -101.0, -99.0]], dtype=dtype).cuda()
     ids, _ = st.route(l, 2, score=score, bias=torch.zeros(3, device="cuda"))
     assert ids.tolist() == [[0, 2], [1, 2], [2, 0]]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("k", [1, 3, 6])
+@pytest.mark.parametrize("experts", [8, 200])
+def test_a_bias_of_minus_infinity_wins_over_nan(experts, k):
+    bias = torch.zeros(experts)
+    bias[1] = bias[7] = -np.inf
+    l = 0.01 * torch.arange(experts).float().expand(4, experts).clone()
+    l[0, 5] = float("nan")
+    l[1, 7] = float("nan")
+    l[2, 4] = float("inf")
+    l[3, 1] = float("inf")
+    left = [e for e in range(experts) if e not in (1, 7)]
+    ids, _ = st.route(l.cuda(), k, score="softmax", bias=bias.cuda())
+    assert ids.tolist() == [left[:k]] * 4  # every score of such a row is NaN
+    ids, _ = st.route(l.cuda(), k, score="sigmoid", bias=bias.cuda())
+    down = left[::-1]
+    assert ids.tolist() == [([5] + [e for e in down if e != 5])[:k], down[:k],
+                            ([4] + [e for e in down if e != 4])[:k], down[:k]]
