@@ -5,10 +5,14 @@ operator's contract).
 Inputs are CUDA tensors on one device. Rows may lie any distance apart (a
 part of a wider tensor's columns, one row expanded to many); tensors whose
 rows are not contiguous, and views whose conjugation or negation torch has put
-off (x.conj() of a complex tensor), are copied first. Everything runs on the
-current stream, or on `stream`, from whose memory pool results and workspaces then
-come. Nothing here synchronises, so all of it can be captured in a graph.
-Gradients are functions of their own; autograd does not see these calls.
+off (x.conj() of a complex tensor), are copied first, whole and on every call.
+Everything runs on the current stream, or on `stream`, from whose memory pool
+results and workspaces then come. Nothing here synchronises, so all of it can
+be captured in a graph.
+
+Gradients are functions of their own; autograd does not see these calls
+(examples/sparse_layer.py wraps them for it). A given output counts as changed
+for autograd; outside torch.no_grad() one that requires a gradient is refused.
 
 The calls go through a compiled binding (csrc/rows_binding.cpp), which checks
 the tensors and makes the results. Like the rest of the package it raises if

@@ -15,6 +15,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -161,10 +162,21 @@ struct Place {
     const at::Tensor& t = tensor(given, name);
     TORCH_CHECK_VALUE(t.sizes() == shape && t.scalar_type() == type && t.is_contiguous() && !put_off(t), name,
                       " must be contiguous, ", type, " of ", shape, " and no conjugated or negated view");
+    // as torch does with outputs: autograd would not see the write
+    TORCH_CHECK_VALUE(!t.requires_grad() || !c10::GradMode::is_enabled(), name, " must not require a gradient");
     same(t);
     return t;
   }
 };
+
+// After a call that wrote to `given` (None: to a new tensor): whoever saved it
+// for a backward pass learns that it changed. Tensors of inference mode keep
+// no count and are saved by nobody.
+void written(PyObject* given, const at::Tensor& t)
+{
+  if (given != Py_None && !t.is_inference())
+    t.unsafeGetTensorImpl()->bump_version();
+}
 
 struct Groups {
   at::Tensor rows; // [tokens, k]
@@ -301,6 +313,7 @@ PyObject* dispatch(PyObject*, PyObject* const* a, Py_ssize_t n)
   at::Tensor out = place.result(a[2], "out", {g.slots, width}, x.scalar_type());
   check(lib.segtopk_dispatch(x.const_data_ptr(), (int32_t)x.element_size(), g.tokens, g.k, width, x.stride(0),
                              g.rows.const_data_ptr<int32_t>(), g.kept, out.mutable_data_ptr(), place.stream()));
+  written(a[2], out);
   return wrap(std::move(out));
   END_HANDLE_TH_ERRORS
 }
@@ -325,6 +338,7 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n)
                             g.rows.const_data_ptr<int32_t>(),
                             weights.defined() ? weights.const_data_ptr<float>() : nullptr, out.mutable_data_ptr(),
                             place.stream()));
+  written(a[3], out);
   return wrap(std::move(out));
   END_HANDLE_TH_ERRORS
 }
@@ -379,6 +393,7 @@ PyObject* embedding(PyObject*, PyObject* const* a, Py_ssize_t n)
   check(lib.segtopk_embedding(type, table.const_data_ptr(), table.size(0), table.size(1), table.stride(0),
                               tokens.const_data_ptr(), bytes, tokens.numel(), scale, out_code,
                               out.mutable_data_ptr(), place.stream()));
+  written(a[4], out);
   return wrap(std::move(out));
   END_HANDLE_TH_ERRORS
 }
@@ -420,6 +435,7 @@ PyObject* embedding_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
   check(lib.segtopk_embedding_backward(type, grad.const_data_ptr(), grad.stride(0), tokens.const_data_ptr(), bytes,
                                        count, num_rows, width, padding, scale, table_code, out.mutable_data_ptr(),
                                        accumulate, space.mutable_data_ptr(), need, place.stream()));
+  written(a[6], out);
   return wrap(std::move(out));
   END_HANDLE_TH_ERRORS
 }
