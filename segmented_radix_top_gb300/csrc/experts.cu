@@ -453,6 +453,7 @@ Run run_of(const Shape& s, int64_t tiles, int sms)
   const int64_t groups = resident(s, tiles, sms);
   return {s, (uint32_t)std::min<int64_t>(s.tokens, groups * std::max<int64_t>(1, s.tokens / (8 * groups))), 0, 0, 0};
 }
+constexpr int64_t kMaxTilesOfGrid = 65535; // they are grid.y
 dim3 grid_of(const Run& run, int64_t tiles)
 {
   const uint32_t per_block = (uint32_t)(kThreads / run.s.lanes);
@@ -552,8 +553,9 @@ extern "C" int segtopk_combine(segtopk_dtype dtype, const void* rows, int64_t to
         const int64_t cols = (int64_t)s.lanes * V, tiles = (width + cols - 1) / cols;
         // runs pay once they are long: 1237 tokens of 1000 in f32, k = 6, take
         // 6.1 us a token per group and 7.1 in runs of two; 8192 of 2048 in
-        // bf16 58 and 50
-        if (tokens >= 8 * resident(s, tiles, sms)) {
+        // bf16 58 and 50. Rows of more tiles than a grid has (67 million
+        // columns in f32) go by the other kernel, which loops over columns.
+        if (tokens >= 8 * resident(s, tiles, sms) && tiles <= kMaxTilesOfGrid) {
           const Run run = run_of(s, tiles, sms);
           auto kernel = weights ? combine_run_kernel<T, V, true> : combine_run_kernel<T, V, false>;
           return finish(launch(kernel, grid_of(run, tiles), kThreads, kRingBytes, (cudaStream_t)stream, (const T*)rows,
