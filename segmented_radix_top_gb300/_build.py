@@ -10,16 +10,20 @@ sources compiled with SEGTOPK_STATS and SEGTOPK_TEST_HOOKS: per-CTA counters
 (segtopk_set_test_hooks). build_all() compiles both in one pool of
 compiler processes.
 
-Beside the library, csrc/rows_binding.cpp becomes _rows_native.so (g++ and
-PyTorch's headers): the Python binding of the row operators. It does not link
-the library; _rows.py hands it the entry points of the loaded one.
+Beside the library, csrc/rows_binding.cpp becomes _rows_native.so (g++,
+Python's and PyTorch's headers): the Python binding of the row operators. It
+does not link the library; _rows.py hands it the entry points of the loaded
+one. The library needs none of that: it is built first, and alone where those
+headers are not installed.
 """
 from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -29,7 +33,6 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libsegtopk.so")
 BINDING_SRC = os.path.join(CSRC, "rows_binding.cpp")
-BINDING_PATH = os.path.join(HERE, "_rows_native.so")
 VARIANTS = {
     "": (BUILD_DIR, LIB_PATH, []),
     "instr": (os.path.join(HERE, "_build_instr"), os.path.join(HERE, "libsegtopk_instr.so"),
@@ -83,33 +86,50 @@ def _compile(variant: str, src: str, extra_flags, verbose: bool) -> str:
     return obj
 
 
+def binding_path() -> str:
+    return os.path.join(HERE, "_rows_native.so")
+
+
+def _binding_includes():
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    return [base, os.path.join(base, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], cuda]
+
+
+def binding_lacks():
+    """What the binding cannot be compiled without and this machine does not have."""
+    lacks = [] if shutil.which("g++") else ["g++"]
+    for header in ("Python.h", os.path.join("torch", "csrc", "autograd", "python_variable.h")):
+        if not any(os.path.exists(os.path.join(d, header)) for d in _binding_includes()):
+            lacks.append(header)
+    return lacks
+
+
 def binding_up_to_date() -> bool:
-    if not os.path.exists(BINDING_PATH):
+    path = binding_path()
+    if not os.path.exists(path):
         return False
-    t = os.path.getmtime(BINDING_PATH)
+    t = os.path.getmtime(path)
     return all(os.path.getmtime(d) <= t for d in [BINDING_SRC, os.path.join(INCLUDE, "segtopk.h")])
 
 
 def _compile_binding(verbose: bool) -> str:
-    import sysconfig
-
     import torch
-    base = os.path.dirname(torch.__file__)
-    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
-    tmp = BINDING_PATH + ".tmp.%d" % os.getpid()
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    path = binding_path()
+    tmp = path + ".tmp.%d" % os.getpid()
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
-           "-I", os.path.join(base, "include"), "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
-           "-I", sysconfig.get_paths()["include"], "-I", cuda, BINDING_SRC, "-o", tmp, "-L", os.path.join(base, "lib"),
-           "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10",
-           "-Wl,-rpath," + os.path.join(base, "lib")]
+           *("-I" + d for d in _binding_includes()), BINDING_SRC, "-o", tmp, "-L", lib,
+           "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath," + lib]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("g++ failed for %s:\n%s\n%s" % (BINDING_SRC, r.stdout, r.stderr))
     if verbose and (r.stdout or r.stderr):
         sys.stderr.write(r.stdout + r.stderr)
-    os.replace(tmp, BINDING_PATH)
-    return BINDING_PATH
+    os.replace(tmp, path)
+    return path
 
 
 def _link(variant: str, objs) -> str:
@@ -126,21 +146,28 @@ def _link(variant: str, objs) -> str:
 def build_variants(variants, force: bool = False, verbose: bool = False, extra_flags=None):
     """Builds the given variants and the row operators' binding, every
     translation unit of all of them in one pool of compiler processes;
-    returns the library paths."""
+    returns the library paths. The libraries do not wait for the binding: an
+    error of its compilation is raised once they are linked, and where this
+    machine cannot compile it that is said on stderr (and again by the first
+    call of a row operator)."""
     todo = [v for v in variants if force or not up_to_date(v)]
     for v in todo:
         os.makedirs(VARIANTS[v][0], exist_ok=True)
     srcs = _sources()
     jobs = [(v, s) for v in todo for s in srcs]
     binding = force or not binding_up_to_date()
+    lacks = binding_lacks() if binding else []
+    if lacks:
+        binding = False
+        sys.stderr.write("the binding of the row operators is not built: %s not installed\n" % ", ".join(lacks))
     if jobs or binding:
         with ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
             bound = ex.submit(_compile_binding, verbose) if binding else None
             objs = list(ex.map(lambda j: _compile(j[0], j[1], extra_flags, verbose), jobs))
-            if bound:
-                bound.result()
         for v in todo:
             _link(v, [o for (vv, _), o in zip(jobs, objs) if vv == v])
+        if bound:
+            bound.result()
     return [lib_path(v) for v in variants]
 
 

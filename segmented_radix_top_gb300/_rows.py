@@ -76,10 +76,12 @@ def _load():
     global _native
     if _native is None:
         L = B.load()
-        path = _build.BINDING_PATH
+        path = _build.binding_path()
         if not os.path.exists(path):
-            raise RuntimeError("%s is not built (run __graft_entry__.build()); there is no fallback implementation"
-                               % os.path.basename(path))
+            lacks = _build.binding_lacks()
+            raise RuntimeError("%s is not built (%s); there is no fallback implementation"
+                               % (os.path.basename(path), "not installed: " + ", ".join(lacks) if lacks else
+                                  "run __graft_entry__.build()"))
         spec = importlib.util.spec_from_file_location("segmented_radix_top_gb300._rows_native", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
