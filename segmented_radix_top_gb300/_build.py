@@ -10,7 +10,7 @@ sources compiled with SEGTOPK_STATS and SEGTOPK_TEST_HOOKS: per-CTA counters
 (segtopk_set_test_hooks). build_all() compiles both in one pool of
 compiler processes.
 
-Beside the library, csrc/rows_binding.cpp becomes _rows_native.so (g++,
+Beside the library, csrc/rows_binding.cpp becomes _rows_native.*.so (g++,
 Python's and PyTorch's headers): the Python binding of the row operators. It
 does not link the library; _rows.py hands it the entry points of the loaded
 one. The library needs none of that: it is built first, and alone where those
@@ -87,7 +87,11 @@ def _compile(variant: str, src: str, extra_flags, verbose: bool) -> str:
 
 
 def binding_path() -> str:
-    return os.path.join(HERE, "_rows_native.so")
+    """The binding's file. Its name holds the interpreter's and PyTorch's
+    versions: it is compiled against their classes, which differ from one to
+    the next, so that after a change of either it is built anew."""
+    import torch
+    return os.path.join(HERE, "_rows_native.%s.torch-%s.so" % (sysconfig.get_config_var("SOABI"), torch.__version__))
 
 
 def _binding_includes():
@@ -111,7 +115,8 @@ def binding_up_to_date() -> bool:
     if not os.path.exists(path):
         return False
     t = os.path.getmtime(path)
-    return all(os.path.getmtime(d) <= t for d in [BINDING_SRC, os.path.join(INCLUDE, "segtopk.h")])
+    return all(os.path.getmtime(d) <= t for d in [BINDING_SRC, os.path.join(INCLUDE, "segtopk.h"),
+                                                  os.path.abspath(__file__)])
 
 
 def _compile_binding(verbose: bool) -> str:

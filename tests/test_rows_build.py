@@ -1,5 +1,6 @@
 """The build of the library does not depend on the row operators' Python
-binding. Host only; the compilers are stood in for."""
+binding, and a binding made for another PyTorch is not used. Host only; the
+compilers are stood in for."""
 import os
 
 import pytest
@@ -44,3 +45,23 @@ def test_both_are_built_where_both_can_be(made):
     assert _build.binding_lacks() == []
     _build.build(force=True)
     assert sorted(made, key=str) == sorted([("library", len(_build._sources())), "binding"], key=str)
+
+
+def test_a_binding_for_another_torch_does_not_count(monkeypatch):
+    _build.build()
+    assert _build.binding_up_to_date()
+    here = _build.binding_path()
+    monkeypatch.setattr(torch, "__version__", "1.0.0+other")
+    assert _build.binding_path() != here and not _build.binding_up_to_date()
+
+
+def test_a_binding_made_before_its_flags_changed_does_not_count(monkeypatch, tmp_path):
+    path = tmp_path / "binding.so"
+    path.write_bytes(b"")
+    monkeypatch.setattr(_build, "binding_path", lambda: str(path))
+    newest = max(os.path.getmtime(f) for f in (_build.__file__, _build.BINDING_SRC))
+    os.utime(path, (newest + 1, newest + 1))
+    assert _build.binding_up_to_date()
+    before = os.path.getmtime(_build.__file__) - 1
+    os.utime(path, (before, before))
+    assert not _build.binding_up_to_date()
