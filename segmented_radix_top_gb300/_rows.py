@@ -13,6 +13,7 @@ be captured in a graph.
 Gradients are functions of their own; autograd does not see these calls
 (examples/sparse_layer.py wraps them for it). A given output counts as changed
 for autograd; outside torch.no_grad() one that requires a gradient is refused.
+Outputs must not overlap inputs.
 
 The calls go through a compiled binding (csrc/rows_binding.cpp), which checks
 the tensors and makes the results. Like the rest of the package it raises if
@@ -118,7 +119,7 @@ def route(logits: torch.Tensor, k: int, *, score: str = "softmax", renormalize: 
     logits: [tokens, experts]. score: "softmax" (over all experts) or
     "sigmoid"; renormalize divides by the sum of the k chosen scores; scale
     multiplies. bias: optional float32 [experts], added to the scores for the
-    choice only. Experts with a logit of -inf are never chosen. Returns
+    choice only. Experts with a logit or a bias of -inf are never chosen. Returns
     (expert_ids int32 [tokens, k], best first and -1 where none is left,
     weights float32 [tokens, k])."""
     return (_native or _load()).route(logits, k, score, renormalize, scale, bias)
@@ -176,7 +177,8 @@ def combine_backward(grad_out: torch.Tensor, rows: torch.Tensor, groups: ExpertG
 def embedding(table: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0, out_dtype=None, out=None):
     """scale * table[tokens] (segtopk_embedding): table [vocab, width], tokens
     int32 or int64 of any shape; returns [*tokens.shape, width] of out_dtype
-    (the table's unless given). Tokens outside the table give zeros."""
+    (the table's unless given). Tokens outside the table give zeros. A table
+    whose rows are not contiguous (weight.t()) is copied whole by every call."""
     return (_native or _load()).embedding(table, tokens, scale, out_dtype, out)
 
 

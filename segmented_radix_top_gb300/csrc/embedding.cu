@@ -19,6 +19,9 @@ namespace {
 using namespace rows;
 
 constexpr int kThreads = 256;
+// Of a GB300. Shares and clearing blocks are planned for this number, as the
+// workspace's size is, which is asked for without a device; another number of
+// SMs would only leave the last wave of blocks less full.
 constexpr int kSms = 152;
 constexpr int kInFlight = 4; // vectors of a row that a thread has in flight
 constexpr int kDigitBits = 9; // of a radix pass: 512 counters a warp in shared memory
@@ -94,7 +97,7 @@ struct TokenSource {
 // that the kernel after it finds both done. (The other order would not do: a
 // sort launched second would wait for the clearing first.) Bound by the
 // writes. 2048 tokens of 32000 rows of 4 KB: 30 us in all, 40 where the merge
-// writes every row after the sort; 34 with a block for every 16 KB, whose
+// writes every row after the sort (other sizes at its call); 34 with a block for every 16 KB, whose
 // first wave then holds the SMs until the sort ends.
 constexpr size_t kClearRun = 32 << 10;
 __global__ void __launch_bounds__(kThreads) clear_kernel(char* at, size_t bytes)
@@ -650,8 +653,10 @@ extern "C" int segtopk_embedding_backward(segtopk_dtype dtype, const void* grad_
       const uint32_t n = (uint32_t)num_tokens;
       // Clearing the table beside the sort, on the SMs that a cluster leaves,
       // and then writing the tokens' rows writes those twice: worth it where
-      // they are few of all (32000 rows of 4 KB: 2048 tokens 28 against 38 us,
-      // 4096 31 against 41, 8192 44 against 45).
+      // they are few of all. 32000 rows of 4 KB, ids with a text's frequencies:
+      // 2048 tokens 30 against 40 us, 4096 33 against 44, 8000 37 against 48;
+      // uniform ids 29 against 38, 32 against 42, 36 against 44. The two meet
+      // above a quarter (at 8192 the step is still 36 to 44).
       const bool clear_first = !accumulate && l.sort.tiles.items == 0 && num_tokens <= vocab / kFewOf;
       int launches = 0;
       if (n > 0 || clear_first) { // the clearing follows a sort, of no tokens too

@@ -10,7 +10,7 @@
 //
 // One warp serves a token: its lanes hold the row in registers (NV
 // consecutive logits each), so the row is read once. 65536 rows of 256 in
-// f32, k = 8, weights from the full softmax: 25 us, 10.5 at the copy rate;
+// f32, k = 8, weights from the full softmax: 25.5 us, 10.5 at the copy rate;
 // bound by issue (385 instructions a row, 83 % of the issue slots), which is
 // why the k best are not searched for one after the other, see choose(). A
 // warp that fetches its next row ahead, or blocks that stay, were slower (28
