@@ -540,6 +540,67 @@ SEGTOPK_API int segtopk_embedding_backward(segtopk_dtype dtype, const void* grad
                                            segtopk_dtype table_dtype, void* grad_table, int accumulate,
                                            void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The experts' products
+ * ---------------------------------------------------------------------------
+ * Between segtopk_dispatch and segtopk_combine: expert e's matrix product of
+ * its rows [offsets[e], offsets[e + 1]), as segtopk_group sorted them
+ * (offsets: experts + 1 int64 on the device, which the host does not read).
+ * Rows of `rows` from offsets[experts] on belong to no expert: they are not
+ * read into any result, and their rows of `out` are zeros.
+ *
+ * On the tensor cores: sums are held in 32 bits there, in an order that
+ * depends on the sizes alone, and rounded once, to out_dtype (F16, BF16 or
+ * F32). What TMA reads has 16-byte addresses and strides of a multiple of 16
+ * bytes (else SEGTOPK_ERROR_MISALIGNED); strides of `rows` are at least their
+ * width. Widths of up to 2^20, fewer than 2^31 - 256 rows, experts <=
+ * SEGTOPK_MAX_EXPERTS; one launch a call, no workspace.
+ */
+
+/*
+ * out[r, n] = sum_k rows[r, k] * weights[e, n, k], rows and weights of dtype
+ * F16 or BF16, width (the number of k) a multiple of 8. weights: experts
+ * matrices expert_stride apart; one of out_stride (between values of n) and
+ * in_stride (of k) is 1 and the other at least the number of values of the
+ * first, so that weights can be read transposed, as the rows' gradient does:
+ * it is this product of out's gradient with n and k exchanged. With in_stride
+ * other than 1 out_width is a multiple of 8. out: num_rows x out_width, dense.
+ */
+SEGTOPK_API int segtopk_expert_matmul(segtopk_dtype dtype, const void* rows, int64_t num_rows, int64_t width,
+                                      int64_t row_stride, const void* weights, int32_t experts, int64_t out_width,
+                                      int64_t expert_stride, int64_t out_stride, int64_t in_stride,
+                                      const int64_t* offsets, segtopk_dtype out_dtype, void* out, void* stream);
+
+/*
+ * The same of rows and weights in 8 bits (e4m3: 1 sign, 4 exponent and 3
+ * fraction bits, no infinities), each with a float scale for a block:
+ *   out[r, n] = sum_b row_scales[r, b] * weight_scales[e, n / 128, b]
+ *               * sum_{k of block b} rows[r, k] * weights[e, n, k]
+ * with blocks b of 128 values of k, the last one in part where width is no
+ * multiple of 128. width is a multiple of 16. row_scales: num_rows rows of
+ * ceil(width / 128), scale_stride apart (segtopk_quantize_rows makes them);
+ * weight_scales: experts x ceil(out_width / 128) x ceil(width / 128), dense.
+ */
+SEGTOPK_API int segtopk_expert_matmul_f8(const void* rows, int64_t num_rows, int64_t width, int64_t row_stride,
+                                         const float* row_scales, int64_t scale_stride, const void* weights,
+                                         int32_t experts, int64_t out_width, int64_t expert_stride,
+                                         int64_t out_stride, const float* weight_scales, const int64_t* offsets,
+                                         segtopk_dtype out_dtype, void* out, void* stream);
+
+/*
+ * The weights' gradient of segtopk_expert_matmul:
+ *   out[e, a, b] = sum over expert e's rows r of a_rows[r, a] * b_rows[r, b],
+ * experts x a_width x b_width, dense; zeros for an expert without rows. With
+ * out's gradient as a and the rows as b it has the layout of weights whose k
+ * is dense, and the other way round that of weights whose n is. Both widths
+ * are multiples of 8.
+ */
+SEGTOPK_API int segtopk_expert_matmul_weights(segtopk_dtype dtype, const void* a_rows, int64_t a_width,
+                                              int64_t a_stride, const void* b_rows, int64_t b_width,
+                                              int64_t b_stride, int64_t num_rows, int32_t experts,
+                                              const int64_t* offsets, segtopk_dtype out_dtype, void* out,
+                                              void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,7 +13,7 @@ from ._binding import (DETERMINISM, DIRECTION, DTYPE, KEY_BYTES, MAX_K, NOALLOC_
                        read_stats, set_test_hooks, topk)
 from ._rows import (DEVICE_ERROR_INDEX, MAX_EXPERTS, ROUTE_MAX_K, ExpertGroups, combine,  # noqa: F401
                     combine_backward, dispatch, dispatch_backward, embedding, embedding_backward,
-                    group_by_expert, route, route_backward)
+                    expert_matmul, expert_matmul_backward, group_by_expert, route, route_backward)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

@@ -59,6 +59,9 @@ def _entries():
         "segtopk_embedding": (i, [i, vp, i64, i64, i64, vp, i32, i64, f, i, vp, vp]),
         "segtopk_embedding_backward_workspace_bytes": (sz, [i64, i64, i64]),
         "segtopk_embedding_backward": (i, [i, vp, i64, vp, i32, i64, i64, i64, i64, f, i, vp, i, vp, sz, vp]),
+        "segtopk_expert_matmul": (i, [i, vp, i64, i64, i64, vp, i32, i64, i64, i64, i64, vp, i, vp, vp]),
+        "segtopk_expert_matmul_f8": (i, [vp, i64, i64, i64, vp, i64, vp, i32, i64, i64, i64, vp, vp, i, vp, vp]),
+        "segtopk_expert_matmul_weights": (i, [i, vp, i64, i64, vp, i64, i64, i64, i32, vp, i, vp, vp]),
     }
 
 
@@ -194,3 +197,41 @@ def embedding_backward(grad_out: torch.Tensor, tokens: torch.Tensor, num_rows: i
     gets no gradient."""
     return (_native or _load()).embedding_backward(grad_out, tokens, num_rows, scale, padding_idx, dtype, grad_table,
                                                    accumulate)
+
+
+@_on_stream
+def expert_matmul(rows: torch.Tensor, weights: torch.Tensor, groups: ExpertGroups, *, row_scales=None,
+                  weight_scales=None, out_dtype=None, out=None):
+    """Each expert's matrix product of its rows (segtopk_expert_matmul):
+    out[r] = weights[e] @ rows[r] for the rows r of expert e; zeros from row
+    groups.offsets[-1] on. The offsets stay on the device.
+
+    rows: [tokens * k, width], in the order of dispatch(); weights: [experts,
+    out, width] of the same type, float16 or bfloat16, either of the last two
+    dimensions contiguous (weights.transpose(1, 2) of [experts, width, out]
+    is read as it is). width, and in a transposed layout out, is a multiple
+    of 8. out_dtype: that of rows unless given.
+
+    float8_e4m3fn rows and weights (segtopk_expert_matmul_f8) have a float32
+    scale for each block of 128 values: row_scales [tokens * k, blocks of
+    width], as quantize_rows() gives them, and weight_scales [experts, blocks
+    of out, blocks of width], one for 128 by 128 values; blocks at the end may
+    be smaller. width is a multiple of 16, out is any, and the result bfloat16
+    unless out_dtype is given. A frozen layer's gradient of its rows is this
+    product too, with the transposed weights and scales laid out beside them.
+
+    Tensors whose rows do not start on 16-byte boundaries are copied first, as
+    are weights in another layout, by every call."""
+    return (_native or _load()).expert_matmul(rows, weights, groups, row_scales, weight_scales, out_dtype, out)
+
+
+@_on_stream
+def expert_matmul_backward(grad_out: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor, groups: ExpertGroups, *,
+                           dtype=None):
+    """Gradients of expert_matmul()'s rows and weights in 16 bits
+    (segtopk_expert_matmul with the weights transposed, and
+    segtopk_expert_matmul_weights): ([tokens * k, width] with zeros from row
+    groups.offsets[-1] on, [experts, out, width] of dtype (the weights' unless
+    given) in the weights' layout, zeros for an expert without rows). width
+    and out are multiples of 8."""
+    return (_native or _load()).expert_matmul_backward(grad_out, rows, weights, groups, dtype)

@@ -665,7 +665,7 @@ extern "C" int segtopk_read_device_error(uint32_t* error_word)
       return cuda_fail(e);
     all |= w;
   }
-  for (auto read : {&read_group_error, &read_embedding_error}) {
+  for (auto read : {&read_group_error, &read_embedding_error, &read_matmul_error}) {
     uint32_t w = 0;
     e = read(&w);
     if (e != cudaSuccess)

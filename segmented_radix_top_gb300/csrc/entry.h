@@ -21,5 +21,6 @@ int check_device(int* sms);
 // (synchronous).
 cudaError_t read_group_error(uint32_t* word);
 cudaError_t read_embedding_error(uint32_t* word);
+cudaError_t read_matmul_error(uint32_t* word);
 
 } // namespace segtopk

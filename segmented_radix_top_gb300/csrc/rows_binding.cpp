@@ -37,7 +37,10 @@ namespace {
   X(segtopk_combine_backward)                                                                                    \
   X(segtopk_embedding)                                                                                           \
   X(segtopk_embedding_backward)                                                                                  \
-  X(segtopk_embedding_backward_workspace_bytes)
+  X(segtopk_embedding_backward_workspace_bytes)                                                                  \
+  X(segtopk_expert_matmul)                                                                                       \
+  X(segtopk_expert_matmul_f8)                                                                                    \
+  X(segtopk_expert_matmul_weights)
 
 struct Library {
 #define X(NAME) decltype(&::NAME) NAME = nullptr;
@@ -180,8 +183,9 @@ void written(PyObject* given, const at::Tensor& t)
 
 struct Groups {
   at::Tensor rows; // [tokens, k]
-  const int64_t* kept;
-  int64_t tokens, slots;
+  const int64_t* kept;    // the last of the offsets
+  const int64_t* offsets;
+  int64_t tokens, slots, experts;
   int32_t k;
 };
 Groups groups_of(PyObject* o, const Place& place)
@@ -195,8 +199,9 @@ Groups groups_of(PyObject* o, const Place& place)
                     "groups must come from group_by_expert");
   place.same(offsets);
   place.same(rows);
-  return {rows, offsets.const_data_ptr<int64_t>() + (offsets.numel() - 1), rows.size(0), rows.numel(),
-          (int32_t)rows.size(1)};
+  const int64_t* first = offsets.const_data_ptr<int64_t>();
+  const int64_t experts = offsets.numel() - 1;
+  return {rows, first + experts, first, rows.size(0), rows.numel(), experts, (int32_t)rows.size(1)};
 }
 
 void check(int status)
@@ -440,6 +445,144 @@ PyObject* embedding_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
   END_HANDLE_TH_ERRORS
 }
 
+// Rows as the tensor cores' operands are read, at least 16 bytes apart in
+// steps of 16 from a 16-byte address: t, or a copy.
+at::Tensor operand_rows(const at::Tensor& t, const char* name)
+{
+  const at::Tensor m = matrix(t, name);
+  const int64_t size = m.element_size();
+  const bool fits = reinterpret_cast<uintptr_t>(m.const_data_ptr()) % 16 == 0 &&
+                    (m.size(0) <= 1 || (m.stride(0) >= m.size(1) && m.stride(0) * size % 16 == 0));
+  return fits ? m : m.clone(at::MemoryFormat::Contiguous);
+}
+int64_t row_stride(const at::Tensor& m) { return m.size(0) <= 1 ? m.size(1) : m.stride(0); }
+
+// The experts' matrices [experts, out, in], one of the last two dimensions
+// contiguous: t, or a copy.
+struct Matrices {
+  at::Tensor t;
+  int64_t expert_stride, out_stride, in_stride;
+  bool turned() const { return in_stride != 1; }
+};
+Matrices matrices(const at::Tensor& given)
+{
+  TORCH_CHECK_VALUE(given.dim() == 3, "weights must have three dimensions");
+  const at::Tensor t = values(given);
+  auto view = [](const at::Tensor& w) {
+    const int64_t n = w.size(1), k = w.size(2);
+    // strides along dimensions of one element say nothing
+    Matrices m{w, w.stride(0), n == 1 ? k : w.stride(1), k == 1 ? 1 : w.stride(2)};
+    if (m.in_stride != 1 && k > 1 && n > 1 && w.stride(1) == 1)
+      m.out_stride = 1;
+    if (w.size(0) <= 1)
+      m.expert_stride = n * k;
+    return m;
+  };
+  Matrices m = view(t);
+  const int64_t size = t.element_size(), n = t.size(1), k = t.size(2);
+  const int64_t line = m.turned() ? m.in_stride : m.out_stride;
+  const bool fits = (m.in_stride == 1 ? m.out_stride >= k : m.out_stride == 1 && m.in_stride >= n) &&
+                    reinterpret_cast<uintptr_t>(t.const_data_ptr()) % 16 == 0 && line * size % 16 == 0 &&
+                    m.expert_stride * size % 16 == 0;
+  return fits ? m : view(t.clone(at::MemoryFormat::Contiguous));
+}
+
+PyObject* expert_matmul(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+  HANDLE_TH_ERRORS
+  want_args(n, 7); // rows, weights, groups, row_scales or None, weight_scales or None, out_dtype or None, out
+  const at::Tensor rows = operand_rows(tensor(a[0], "rows"), "rows");
+  const at::ScalarType type = rows.scalar_type();
+  const bool eight = type == at::kFloat8_e4m3fn;
+  TORCH_CHECK_VALUE(eight || type == at::kHalf || type == at::kBFloat16,
+                    "rows must be float16, bfloat16 or float8_e4m3fn");
+  const at::Tensor& given = tensor(a[1], "weights");
+  TORCH_CHECK_VALUE(given.scalar_type() == type && given.dim() == 3 && given.size(2) == rows.size(1), "weights must be ",
+                    type, " of [experts, out, ", rows.size(1), "]");
+  TORCH_CHECK_VALUE(eight == (a[3] != Py_None) && eight == (a[4] != Py_None),
+                    "float8_e4m3fn rows and weights have row_scales and weight_scales, others have none");
+  const Place place(rows);
+  place.same(given);
+  Matrices w = matrices(given);
+  if (eight && w.turned())
+    w = matrices(given.contiguous());
+  const Groups g = groups_of(a[2], place);
+  const int64_t experts = given.size(0), out_width = given.size(1), width = given.size(2);
+  TORCH_CHECK_VALUE(rows.size(0) == g.slots, "rows must have a row for each slot of the groups");
+  TORCH_CHECK_VALUE(experts == g.experts && experts <= INT32_MAX, "weights must have a matrix for each expert of the groups");
+  at::ScalarType out_type = eight ? at::kBFloat16 : type;
+  if (a[5] != Py_None)
+    out_type = dtype_of(a[5]);
+  else if (a[6] != Py_None)
+    out_type = tensor(a[6], "out").scalar_type();
+  const segtopk_dtype out_code = float_type(out_type, "out");
+  at::Tensor row_scales, weight_scales;
+  if (eight) {
+    const int64_t blocks = (width + 127) / 128;
+    row_scales = matrix(tensor(a[3], "row_scales"), "row_scales");
+    TORCH_CHECK_VALUE(row_scales.scalar_type() == at::kFloat && row_scales.size(0) == g.slots &&
+                        row_scales.size(1) == blocks,
+                      "row_scales must be float32 of [", g.slots, ", ", blocks, "]");
+    weight_scales = dense(tensor(a[4], "weight_scales"), "weight_scales", {experts, (out_width + 127) / 128, blocks},
+                          at::kFloat);
+    place.same(row_scales);
+    place.same(weight_scales);
+  }
+  at::Tensor out = place.result(a[6], "out", {g.slots, out_width}, out_type);
+  if (eight)
+    check(lib.segtopk_expert_matmul_f8(rows.const_data_ptr(), g.slots, width, row_stride(rows),
+                                       row_scales.const_data_ptr<float>(), row_scales.stride(0), w.t.const_data_ptr(),
+                                       (int32_t)experts, out_width, w.expert_stride, w.out_stride,
+                                       weight_scales.const_data_ptr<float>(), g.offsets, out_code,
+                                       out.mutable_data_ptr(), place.stream()));
+  else
+    check(lib.segtopk_expert_matmul(float_type(type, "rows"), rows.const_data_ptr(), g.slots, width, row_stride(rows),
+                                    w.t.const_data_ptr(), (int32_t)experts, out_width, w.expert_stride, w.out_stride,
+                                    w.in_stride, g.offsets, out_code, out.mutable_data_ptr(), place.stream()));
+  written(a[6], out);
+  return wrap(std::move(out));
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* expert_matmul_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+  HANDLE_TH_ERRORS
+  want_args(n, 5); // grad_out, rows, weights, groups, dtype or None
+  const at::Tensor grad = operand_rows(tensor(a[0], "grad_out"), "grad_out");
+  const at::Tensor rows = operand_rows(tensor(a[1], "rows"), "rows");
+  const at::Tensor& given = tensor(a[2], "weights");
+  const at::ScalarType type = rows.scalar_type();
+  TORCH_CHECK_VALUE(type == at::kHalf || type == at::kBFloat16, "rows must be float16 or bfloat16");
+  TORCH_CHECK_VALUE(given.scalar_type() == type && given.dim() == 3 && given.size(2) == rows.size(1), "weights must be ",
+                    type, " of [experts, out, ", rows.size(1), "]");
+  const Place place(rows);
+  place.same(given);
+  place.same(grad);
+  const Matrices w = matrices(given);
+  const Groups g = groups_of(a[3], place);
+  const int64_t experts = given.size(0), out_width = given.size(1), width = given.size(2);
+  TORCH_CHECK_VALUE(rows.size(0) == g.slots, "rows must have a row for each slot of the groups");
+  TORCH_CHECK_VALUE(experts == g.experts && experts <= INT32_MAX, "weights must have a matrix for each expert of the groups");
+  TORCH_CHECK_VALUE(grad.scalar_type() == type && grad.size(0) == g.slots && grad.size(1) == out_width,
+                    "grad_out must be ", type, " of [", g.slots, ", ", out_width, "]");
+  const at::ScalarType weight_type = a[4] != Py_None ? dtype_of(a[4]) : type;
+  const segtopk_dtype weight_code = float_type(weight_type, "grad_weights"), code = float_type(type, "rows");
+  at::Tensor grad_rows = place.empty({g.slots, width}, type);
+  check(lib.segtopk_expert_matmul(code, grad.const_data_ptr(), g.slots, out_width, row_stride(grad),
+                                  w.t.const_data_ptr(), (int32_t)experts, width, w.expert_stride, w.in_stride,
+                                  w.out_stride, g.offsets, code, grad_rows.mutable_data_ptr(), place.stream()));
+  // in the layout of the weights
+  at::Tensor grad_weights = w.turned() ? place.empty({experts, width, out_width}, weight_type)
+                                       : place.empty({experts, out_width, width}, weight_type);
+  const at::Tensor &outer = w.turned() ? rows : grad, &inner = w.turned() ? grad : rows;
+  check(lib.segtopk_expert_matmul_weights(code, outer.const_data_ptr(), outer.size(1), row_stride(outer),
+                                          inner.const_data_ptr(), inner.size(1), row_stride(inner), g.slots,
+                                          (int32_t)experts, g.offsets, weight_code, grad_weights.mutable_data_ptr(),
+                                          place.stream()));
+  return tuple(std::move(grad_rows), w.turned() ? grad_weights.transpose(1, 2) : std::move(grad_weights));
+  END_HANDLE_TH_ERRORS
+}
+
 // bind(addresses of the entry points by name, function that raises for a status)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
@@ -469,6 +612,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 PyMethodDef methods[] = {FUNCTION(bind),      FUNCTION(route),    FUNCTION(route_backward),
                          FUNCTION(group),     FUNCTION(dispatch), FUNCTION(combine),
                          FUNCTION(combine_backward), FUNCTION(embedding), FUNCTION(embedding_backward),
+                         FUNCTION(expert_matmul),    FUNCTION(expert_matmul_backward),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_rows_native", nullptr, -1, methods};
 
