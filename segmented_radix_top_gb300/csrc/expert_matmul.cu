@@ -41,10 +41,8 @@ constexpr int kTileQ = 256;      // half of its columns
 constexpr int kStages = 4;
 constexpr int kBytesP = kTileP * 128, kBytesQ = kTileQ * 128;
 constexpr int kStageBytes = kBytesP + kBytesQ;
-constexpr int kBoxQ = 32;        // rows of one copy of Q
+constexpr int kBox = 32;         // rows of one copy of an expert's rows
 constexpr int kDepth = 64;       // rows of one copy where c runs over rows
-constexpr int kScaleSlots = 8;   // blocks of scales under way
-constexpr int kScaleRun = 4;     // blocks whose scales a warp fetches at a time
 constexpr int kMaxExperts = SEGTOPK_MAX_EXPERTS;
 
 enum Kind { kForward8, kForward, kForwardTurned, kWeights };
@@ -52,7 +50,6 @@ enum Kind { kForward8, kForward, kForwardTurned, kWeights };
 struct Control {
   uint64_t full[kStages], empty[kStages];       // copies have landed; products have read them
   uint64_t sums_full[2], sums_empty[2];         // TMEM's halves
-  uint64_t scales_full[kScaleSlots], scales_empty[kScaleSlots];
   uint64_t drained;                             // products behind a wait that ran out
   uint32_t tmem;
   int failed;                                   // a wait ran out: everybody leaves
@@ -60,19 +57,19 @@ struct Control {
   int tile_start[kMaxExperts + 1];              // experts' first tiles
   int row_start[kMaxExperts + 1];               // and rows
 };
-constexpr int kScaleBytes = kScaleSlots * kTileQ * 4;
-constexpr size_t kShared = 1024 + (size_t)kStages * kStageBytes + kScaleBytes + sizeof(Control);
+constexpr size_t kShared = 1024 + (size_t)kStages * kStageBytes + sizeof(Control);
 static_assert(kShared <= 227 * 1024, "shared memory of a block");
 
 struct Sizes {
   int64_t num_rows;     // slots; those from the last offset on have no expert
   int experts;
-  int p, q, c;          // sizes (q: kWeights only, c: not there)
+  int p, q, c;          // sizes; an expert's rows take the place of one
+  int step;             // kForward8: the tiles' q
   uint32_t instruction; // types and majors of the operands
-  int64_t out_stride;   // from one q to the next; the weights' gradient is dense
+  int64_t out_stride;   // between rows of the result, which are dense
+  bool out_vectors;     // kForward8: they can be written 16 bytes at a time
   const float* row_scales;
   int64_t scale_stride;
-  bool scale_vectors;   // rows of scales can be read four at a time
   const float* weight_scales;
 };
 
@@ -125,12 +122,12 @@ __device__ __forceinline__ void arrive(uint64_t* bar)
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// 16 columns of this warp's 32 lanes; the values are there after sums_wait()
+// Columns of this warp's 32 lanes; the values are there after sums_wait()
 // has been given them.
 __device__ __forceinline__ void sums_load(uint32_t (&v)[16], uint32_t at)
 {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-               "%13, %14, %15}, [%16];"
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
                  "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
                : "r"(at));
@@ -143,17 +140,26 @@ __device__ __forceinline__ void sums_wait(uint32_t (&v)[16])
                :
                : "memory");
 }
-
-__device__ __forceinline__ void sums_load(uint32_t (&v)[8], uint32_t at)
+__device__ __forceinline__ void sums_load(uint32_t (&v)[32], uint32_t at)
 {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+               "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+                 "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
+                 "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]),
+                 "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]),
+                 "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
                : "r"(at));
 }
-__device__ __forceinline__ void sums_wait(uint32_t (&v)[8])
+__device__ __forceinline__ void sums_wait(uint32_t (&v)[32])
 {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                 "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+                 "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
+                 "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
                :
                : "memory");
 }
@@ -199,13 +205,22 @@ __host__ __device__ __forceinline__ int pieces(int n, int size) { return (n + si
 struct Tile {
   int expert;
   int p;          // first
-  int q, width;   // first of the expert's, and how many; rounded up to 16 there are
+  int q, width;   // first and how many; rounded up to 16 there are
   int row, rows;  // the expert's rows
   int blocks;     // of c
 };
 
-// An expert's q goes to as few tiles as hold it, of even widths in steps of
+// Tiles of an expert with this many rows. Where q are its rows, or its inputs
+// or outputs, it goes to as few tiles as hold it, of even widths in steps of
 // 16; none is empty, since all but the last are no wider than kTileQ.
+template <Kind K>
+__device__ __forceinline__ int parts_p(int rows, const Sizes& z) { return pieces(K == kForward8 ? rows : z.p, kTileP); }
+template <Kind K>
+__device__ __forceinline__ int parts_q(int rows, const Sizes& z)
+{
+  return K == kForward8 ? pieces(z.q, z.step) : pieces(K == kWeights ? z.q : rows, kTileQ);
+}
+
 template <Kind K>
 __device__ __forceinline__ Tile tile_at(int t, const Sizes& z, const Control& sh)
 {
@@ -221,14 +236,22 @@ __device__ __forceinline__ Tile tile_at(int t, const Sizes& z, const Control& sh
   r.expert = low;
   r.row = sh.row_start[low];
   r.rows = sh.row_start[low + 1] - r.row;
-  const int q = K == kWeights ? z.q : r.rows;
-  const int parts = pieces(q, kTileQ);
-  const int step = (pieces(q, parts) + 15) / 16 * 16;
   const int i = t - sh.tile_start[low];
-  r.q = i % parts * step;
-  r.width = min(step, q - r.q);
-  r.p = i / parts * kTileP;
-  r.blocks = K == kWeights ? pieces(r.rows, kDepth) : pieces(z.c, K == kForward8 ? 128 : 64);
+  if constexpr (K == kForward8) {
+    const int parts = parts_p<K>(r.rows, z);
+    r.p = i % parts * kTileP;
+    r.q = i / parts * z.step;
+    r.width = min(z.step, z.q - r.q);
+    r.blocks = pieces(z.c, 128);
+  } else {
+    const int q = K == kWeights ? z.q : r.rows;
+    const int parts = parts_q<K>(r.rows, z);
+    const int step = (pieces(q, parts) + 15) / 16 * 16;
+    r.q = i % parts * step;
+    r.width = min(step, q - r.q);
+    r.p = i / parts * kTileP;
+    r.blocks = K == kWeights ? pieces(r.rows, kDepth) : pieces(z.c, 64);
+  }
   return r;
 }
 
@@ -264,7 +287,6 @@ __device__ void find_tiles(const int64_t* offsets, const Sizes& z, Control& sh)
   constexpr int kMost = kMaxExperts / kThreads + 1; // offsets of a thread
   static_assert(kMost * kThreads > kMaxExperts);
   const int first = threadIdx.x * kMost;
-  const int tiles_p = pieces(z.p, kTileP);
   int row[kMost], most = 0;
 #pragma unroll
   for (int i = 0; i < kMost; ++i) {
@@ -283,8 +305,10 @@ __device__ void find_tiles(const int64_t* offsets, const Sizes& z, Control& sh)
   for (int i = 0; i < kMost; ++i) {
     const int e = first + i;
     tile[i] = sum;
-    if (e < z.experts)
-      sum += pieces(K == kWeights ? z.q : sh.row_start[e + 1] - sh.row_start[e], kTileQ) * tiles_p;
+    if (e < z.experts) {
+      const int rows = sh.row_start[e + 1] - sh.row_start[e];
+      sum += parts_p<K>(rows, z) * parts_q<K>(rows, z);
+    }
   }
   const int start = before_this_thread(sum, sh, [](int a, int b) { return a + b; });
 #pragma unroll
@@ -297,18 +321,253 @@ __device__ void find_tiles(const int64_t* offsets, const Sizes& z, Control& sh)
 // ---------------------------------------------------------------------------
 // Kernel
 // ---------------------------------------------------------------------------
+constexpr bool eight(Kind k) { return k == kForward8; }
+constexpr bool p_by_rows(Kind k) { return k == kForward8 || k == kForward; } // rows of c in shared memory
+constexpr bool q_by_rows(Kind k) { return k != kWeights; }
+
+// One thread: copies of the tiles' operands, as stages get free.
+template <Kind K>
+__device__ void copy_operands(const CUtensorMap& p_map, const CUtensorMap& q_map, const Sizes& z, char* stages, Control& sh)
+{
+  const int tiles = sh.tile_start[z.experts];
+  Ring<kStages> s;
+  int used = 0; // stages whose copies are under way or have landed
+  bool ok = true;
+  for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+    const Tile tile = tile_at<K>(t, z, sh);
+    // boxes are copied whole, whatever of them there is
+    const int boxes_p = K == kForward8 ? pieces(min(kTileP, tile.rows - tile.p), kBox) : 0;
+    const int boxes_q = pieces(tile.width, K == kForward8 ? kTileP : q_by_rows(K) ? kBox : 64);
+    const int bytes = K == kForward8 ? (boxes_p * kBox + boxes_q * kTileP) * 128
+                                     : (kTileP + boxes_q * (q_by_rows(K) ? kBox : 64)) * 128;
+    for (int b = 0; b < tile.blocks; ++b) {
+      ok = wait(&sh.empty[s.at], s.parity ^ 1, sh);
+      if (!ok)
+        break;
+      char *const to_p = stages + s.at * kStageBytes, *const to_q = to_p + kBytesP;
+      uint64_t* const bar = &sh.full[s.at];
+      mbar_arrive_expect_tx(bar, bytes);
+      if constexpr (K == kForward8) {
+        for (int i = 0; i < boxes_p; ++i)
+          tile_load(to_p + i * kBox * 128, &p_map, b * 128, tile.row + tile.p + i * kBox, 0, bar);
+        for (int i = 0; i < boxes_q; ++i)
+          tile_load(to_q + i * kTileP * 128, &q_map, b * 128, tile.q + i * kTileP, tile.expert, bar);
+      } else if constexpr (K == kWeights) {
+        const int y = tile.row + b * kDepth;
+        for (int i = 0; i < 2; ++i)
+          tile_load(to_p + i * kDepth * 128, &p_map, tile.p + i * 64, y, 0, bar);
+        for (int i = 0; i < boxes_q; ++i)
+          tile_load(to_q + i * kDepth * 128, &q_map, tile.q + i * 64, y, 0, bar);
+      } else {
+        if constexpr (K == kForward)
+          tile_load(to_p, &p_map, b * 64, tile.p, tile.expert, bar);
+        else
+          for (int i = 0; i < 2; ++i)
+            tile_load(to_p + i * kDepth * 128, &p_map, tile.p + i * 64, b * kDepth, tile.expert, bar);
+        for (int i = 0; i < boxes_q; ++i)
+          tile_load(to_q + i * kBox * 128, &q_map, b * 64, tile.row + tile.q + i * kBox, 0, bar);
+      }
+      used = min(used + 1, kStages);
+      s.next();
+    }
+  }
+  if (!ok) {
+    // what is under way lands before the block ends (a second each at most)
+    for (int i = 0; i < used; ++i) {
+      s.at = s.at == 0 ? kStages - 1 : s.at - 1;
+      s.parity ^= s.at == kStages - 1;
+      mbar_wait(&sh.full[s.at], s.parity);
+    }
+  }
+}
+
+// One warp: the products of the blocks that have landed.
+template <Kind K>
+__device__ void issue_products(const Sizes& z, char* stages, Control& sh)
+{
+  const int lane = threadIdx.x & 31, tiles = sh.tile_start[z.experts];
+  const uint32_t tmem = sh.tmem;
+  Ring<kStages> s;
+  Ring<2> d;
+  bool ok = true;
+  for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+    const Tile tile = tile_at<K>(t, z, sh);
+    const uint32_t instruction = z.instruction | (uint32_t)((tile.width + 15) / 16 * 2) << 17;
+    for (int b = 0; b < tile.blocks; ++b) {
+      // the sums of one block, or of all
+      const bool first = eight(K) || b == 0, last = eight(K) || b == tile.blocks - 1;
+      ok = (!first || wait(&sh.sums_empty[d.at], d.parity ^ 1, sh)) && wait(&sh.full[s.at], s.parity, sh);
+      ok = __all_sync(kAll, ok);
+      if (!ok)
+        break;
+      char* const from = stages + s.at * kStageBytes;
+      if constexpr (K == kWeights) {
+        // rows of the next expert, or of none, do not count
+        const int left = tile.rows - b * kDepth;
+        if (left < kDepth) {
+          const int copies = 2 + pieces(tile.width, 64);
+          for (int i = 0; i < copies; ++i)
+            for (int at = left * 128 + lane * 16; at < kDepth * 128; at += 512)
+              *reinterpret_cast<uint4*>(from + i * kDepth * 128 + at) = uint4{};
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+      }
+      fence_after_sync();
+      if (lane == 0) {
+        const uint64_t p = operand<p_by_rows(K)>(smem_addr(from)), q = operand<q_by_rows(K)>(smem_addr(from) + kBytesP);
+        // four products: 32 bytes of c on, or 16 rows of 128 bytes
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          multiply<eight(K)>(tmem + d.at * kTileQ, p + i * (p_by_rows(K) ? 2 : 128), q + i * (q_by_rows(K) ? 2 : 128),
+                             instruction, !first || i > 0);
+        commit(&sh.empty[s.at]);
+        if (last)
+          commit(&sh.sums_full[d.at]);
+      }
+      __syncwarp();
+      s.next();
+      if (last)
+        d.next();
+    }
+  }
+  if (!ok && lane == 0) {
+    commit(&sh.drained); // what is under way ends before the block does
+    mbar_wait(&sh.drained, 0);
+  }
+  __syncwarp();
+}
+
+// kSumWarps warps, 8-bit operands: each block's sums times their scales. A
+// thread has one row, so one factor for all its columns of a block, which lie
+// in one block of the weights' scales.
+template <class O>
+__device__ void add_scaled(const Sizes& z, O* out, Control& sh)
+{
+  const int warp = threadIdx.x / 32 - (kThreads / 32 - kSumWarps), lane = threadIdx.x & 31;
+  const int quarter = warp & 3, start = warp / 4 * 128;
+  const uint32_t lanes = sh.tmem + ((uint32_t)quarter * 32 << 16);
+  const int tiles = sh.tile_start[z.experts];
+  Ring<2> d;
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const Tile tile = tile_at<kForward8>(t, z, sh);
+    const int mine = (tile.width - start + 31) / 32; // steps of 32 columns
+    const int row = tile.p + quarter * 32 + lane;
+    const bool on = row < tile.rows && mine > 0;
+    const float* by_row = z.row_scales + (int64_t)(tile.row + row) * z.scale_stride;
+    const float* by_weight =
+      z.weight_scales + ((int64_t)tile.expert * pieces(z.q, 128) + (tile.q + start) / 128) * tile.blocks;
+    float2 sum[64] = {};
+    float scale = on ? by_row[0] * by_weight[0] : 0.0f;
+    for (int b = 0; b < tile.blocks; ++b) {
+      const float2 f = make_float2(scale, scale);
+      if (on && b + 1 < tile.blocks)
+        scale = by_row[b + 1] * by_weight[b + 1];
+      if (!__all_sync(kAll, wait(&sh.sums_full[d.at], d.parity, sh)))
+        return;
+      fence_after_sync();
+      const uint32_t from = lanes + d.at * kTileQ + start;
+      uint32_t v[2][32];
+      if (mine > 0)
+        sums_load(v[0], from);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < mine) {
+          sums_wait(v[c & 1]);
+          if (c + 1 < mine)
+            sums_load(v[(c + 1) & 1], from + (c + 1) * 32);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            sum[c * 16 + i] =
+              __ffma2_rn(make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), f,
+                         sum[c * 16 + i]);
+        }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0)
+        arrive(&sh.sums_empty[d.at]);
+      d.next();
+    }
+    if (on) {
+      O* const to = out + (int64_t)(tile.row + row) * z.out_stride + tile.q + start;
+      const int left = min(128, tile.width - start);
+      if (z.out_vectors) { // left is a multiple of V
+        constexpr int V = 16 / (int)sizeof(O);
+#pragma unroll
+        for (int c = 0; c < 128; c += V)
+          if (c < left) {
+            float x[V];
+#pragma unroll
+            for (int i = 0; i < V; i += 2)
+              x[i] = sum[(c + i) / 2].x, x[i + 1] = sum[(c + i) / 2].y;
+            store_f32<O, V>(to + c, x);
+          }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c < left)
+            to[c] = from_f32<O>(c & 1 ? sum[c / 2].y : sum[c / 2].x);
+      }
+    }
+  }
+}
+
+// kSumWarps warps, 16-bit operands: sums to memory. Lanes are neighbours
+// there.
+template <Kind K, class O>
+__device__ void write_sums(const Sizes& z, O* out, Control& sh)
+{
+  const int warp = threadIdx.x / 32 - (kThreads / 32 - kSumWarps), lane = threadIdx.x & 31;
+  const int quarter = warp & 3;
+  const uint32_t lanes = sh.tmem + ((uint32_t)quarter * 32 << 16);
+  const int tiles = sh.tile_start[z.experts];
+  Ring<2> d;
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const Tile tile = tile_at<K>(t, z, sh);
+    // half of the columns, in steps of 16
+    const int steps = (tile.width + 15) / 16, steps0 = (steps + 1) / 2;
+    const int start = warp < 4 ? 0 : steps0 * 16, mine = warp < 4 ? steps0 : steps - steps0;
+    const int p = tile.p + quarter * 32 + lane;
+    const int left = p < z.p ? tile.width - start : 0; // columns to write
+    const int64_t row = K == kWeights ? (int64_t)tile.expert * z.q + tile.q : tile.row + tile.q;
+    O* at = out + (row + start) * z.out_stride + p;
+    const bool any = tile.blocks > 0; // none: an expert without rows has a gradient of zeros
+    if (any) {
+      if (!__all_sync(kAll, wait(&sh.sums_full[d.at], d.parity, sh)))
+        return;
+      fence_after_sync();
+    }
+    for (int c = 0; c < mine; ++c) {
+      uint32_t v[16] = {};
+      if (any) {
+        sums_load(v, lanes + d.at * kTileQ + start + c * 16);
+        sums_wait(v);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (c * 16 + i < left)
+          *at = from_f32<O>(__uint_as_float(v[i]));
+        at += z.out_stride;
+      }
+    }
+    if (any) {
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0)
+        arrive(&sh.sums_empty[d.at]);
+      d.next();
+    }
+  }
+}
+
 template <Kind K, class O>
 __global__ void __launch_bounds__(kThreads, 1)
 product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                const int64_t* offsets, const __grid_constant__ Sizes z, O* out)
 {
-  constexpr bool kEight = K == kForward8;
-  constexpr bool kRowsP = K == kForward8 || K == kForward; // rows of c in shared memory
-  constexpr bool kRowsQ = K != kWeights;
   extern __shared__ char dynamic[];
   char* const stages = dynamic + (-smem_addr(dynamic) & 1023);
-  float* const scales = reinterpret_cast<float*>(stages + kStages * kStageBytes);
-  Control& sh = *reinterpret_cast<Control*>(stages + kStages * kStageBytes + kScaleBytes);
+  Control& sh = *reinterpret_cast<Control*>(stages + kStages * kStageBytes);
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -319,10 +578,6 @@ product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant_
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.sums_full[i], 1);
       mbar_init(&sh.sums_empty[i], kSumWarps);
-    }
-    for (int i = 0; i < kScaleSlots; ++i) {
-      mbar_init(&sh.scales_full[i], 1);
-      mbar_init(&sh.scales_empty[i], kSumWarps);
     }
     mbar_init(&sh.drained, 1);
     fence_mbar_init();
@@ -338,257 +593,32 @@ product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant_
   allow_next();
   find_tiles<K>(offsets, z, sh); // ends with a barrier
   fence_after_sync();
-  const uint32_t tmem = sh.tmem;
-  const int tiles = sh.tile_start[z.experts];
 
-  if (warp == 0) {
-    // ---- copies ----
-    if (lane == 0) {
-      Ring<kStages> s;
-      uint32_t used = 0; // stages that have copies under way or landed
-      for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const Tile tile = tile_at<K>(t, z, sh);
-        const int boxes = kRowsQ ? pieces(tile.width, kBoxQ) : pieces(tile.width, 64);
-        const int bytes = kBytesP + boxes * (kRowsQ ? kBoxQ : 64) * 128;
-        for (int b = 0; b < tile.blocks; ++b) {
-          if (!wait(&sh.empty[s.at], s.parity ^ 1, sh))
-            goto copies_end;
-          char* const to = stages + s.at * kStageBytes;
-          mbar_arrive_expect_tx(&sh.full[s.at], bytes);
-          if constexpr (kRowsP) {
-            tile_load(to, &p_map, b * (kEight ? 128 : 64), tile.p, tile.expert, &sh.full[s.at]);
-          } else {
-            const int y = K == kWeights ? tile.row + b * kDepth : b * kDepth;
-            const int e = K == kWeights ? 0 : tile.expert;
-            tile_load(to, &p_map, tile.p, y, e, &sh.full[s.at]);
-            tile_load(to + kBytesP / 2, &p_map, tile.p + 64, y, e, &sh.full[s.at]);
-          }
-          for (int i = 0; i < boxes; ++i) {
-            if constexpr (kRowsQ)
-              tile_load(to + kBytesP + i * kBoxQ * 128, &q_map, b * (kEight ? 128 : 64), tile.row + tile.q + i * kBoxQ,
-                        0, &sh.full[s.at]);
-            else
-              tile_load(to + kBytesP + i * 64 * 128, &q_map, tile.q + i * 64, tile.row + b * kDepth, 0,
-                        &sh.full[s.at]);
-          }
-          used = min(used + 1, (uint32_t)kStages);
-          s.next();
-        }
-      }
-    copies_end:
-      if (*(volatile int*)&sh.failed) {
-        // whatever is under way lands before the block ends (again no longer than a second each)
-        for (uint32_t i = 0; i < used; ++i) {
-          s.at = s.at == 0 ? kStages - 1 : s.at - 1;
-          s.parity ^= s.at == kStages - 1;
-          mbar_wait(&sh.full[s.at], s.parity);
-        }
-      }
-    }
-  } else if (warp == 1) {
-    // ---- products ----
-    Ring<kStages> s;
-    Ring<2> d;
-    bool ok = true;
-    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const Tile tile = tile_at<K>(t, z, sh);
-      const uint32_t instruction = z.instruction | (uint32_t)((tile.width + 15) / 16 * 2) << 17;
-      for (int b = 0; ok && b < tile.blocks; ++b) {
-        const bool first = kEight || b == 0; // of a set of sums
-        ok = (!first || wait(&sh.sums_empty[d.at], d.parity ^ 1, sh)) && wait(&sh.full[s.at], s.parity, sh);
-        ok = __all_sync(kAll, ok);
-        if (!ok)
-          break;
-        char* const from = stages + s.at * kStageBytes;
-        if constexpr (K == kWeights) {
-          // rows of the next expert, or of none, do not count
-          const int left = tile.rows - b * kDepth;
-          if (left < kDepth) {
-            const int copies = 2 + pieces(tile.width, 64);
-            for (int i = 0; i < copies; ++i)
-              for (int at = left * 128 + lane * 16; at < kDepth * 128; at += 512)
-                *reinterpret_cast<uint4*>(from + i * kDepth * 128 + at) = uint4{};
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-          }
-        }
-        fence_after_sync();
-        if (lane == 0) {
-          const uint64_t p = operand<kRowsP>(smem_addr(from)), q = operand<kRowsQ>(smem_addr(from) + kBytesP);
-          // four products: 32 bytes of c on, or 16 rows of 128 bytes
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            multiply<kEight>(tmem + d.at * kTileQ, p + i * (kRowsP ? 2 : 128), q + i * (kRowsQ ? 2 : 128),
-                             instruction, !first || i > 0);
-          commit(&sh.empty[s.at]);
-          if (kEight || b == tile.blocks - 1)
-            commit(&sh.sums_full[d.at]);
-        }
-        __syncwarp();
-        s.next();
-        if (kEight || b == tile.blocks - 1)
-          d.next();
-      }
-    }
-    if (*(volatile int*)&sh.failed && lane == 0) {
-      commit(&sh.drained);
-      mbar_wait(&sh.drained, 0);
-    }
-    __syncwarp();
-  } else if (warp < 4) {
-    // ---- scales: a row's times the weights', for each block of c ----
-    if constexpr (kEight) {
-      Ring<kScaleSlots> s;
-      bool ok = true, mine = warp == 2; // the two warps take turns
-      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        const Tile tile = tile_at<K>(t, z, sh);
-        const float* from = z.row_scales + (int64_t)(tile.row + tile.q) * z.scale_stride;
-        const float* by = z.weight_scales +
-                          ((int64_t)tile.expert * pieces(z.p, 128) + tile.p / 128) * pieces(z.c, 128);
-        for (int b = 0; ok && b < tile.blocks; b += kScaleRun, mine = !mine) {
-          const int n = min(kScaleRun, tile.blocks - b);
-          if (!mine) {
-            for (int i = 0; i < n; ++i)
-              s.next();
-            continue;
-          }
-          float w[kScaleRun], x[kTileQ / 32][kScaleRun];
-#pragma unroll
-          for (int i = 0; i < kScaleRun; ++i)
-            w[i] = i < n ? by[b + i] : 0.0f;
-#pragma unroll
-          for (int j = 0; j < kTileQ / 32; ++j) {
-            const int r = j * 32 + lane;
-            const float* row = from + r * z.scale_stride + b;
-            if (z.scale_vectors && n == kScaleRun) {
-              const float4 v = r < tile.width ? *reinterpret_cast<const float4*>(row) : float4{};
-              x[j][0] = v.x, x[j][1] = v.y, x[j][2] = v.z, x[j][3] = v.w;
-            } else {
-#pragma unroll
-              for (int i = 0; i < kScaleRun; ++i)
-                x[j][i] = r < tile.width && i < n ? row[i] : 0.0f;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < kScaleRun; ++i) {
-            if (i >= n)
-              break;
-            ok = __all_sync(kAll, ok && wait(&sh.scales_empty[s.at], s.parity ^ 1, sh));
-            if (!ok)
-              break;
-#pragma unroll
-            for (int j = 0; j < kTileQ / 32; ++j)
-              scales[s.at * kTileQ + j * 32 + lane] = x[j][i] * w[i];
-            __syncwarp();
-            if (lane == 0)
-              arrive(&sh.scales_full[s.at]);
-            s.next();
-          }
-        }
-      }
+  // With 8-bit operands a thread that adds up has 128 sums. What the other
+  // warps give up of the 168 registers that each thread starts with, these
+  // take: 128 * 72 + 256 * 216 = 384 * 168.
+  if (warp < kThreads / 32 - kSumWarps) {
+    if constexpr (eight(K))
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0) {
+      if (lane == 0)
+        copy_operands<K>(p_map, q_map, z, stages, sh);
+    } else if (warp == 1) {
+      issue_products<K>(z, stages, sh);
     }
   } else {
-    // ---- sums ----
-    const int quarter = warp & 3, half = (warp - 4) / 4;
-    const uint32_t lanes = tmem + ((uint32_t)quarter * 32 << 16);
-    Ring<2> d;
-    Ring<kScaleSlots> s;
-    bool ok = true;
-    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const Tile tile = tile_at<K>(t, z, sh);
-      const int chunks = (tile.width + 15) / 16, chunks0 = (chunks + 1) / 2;
-      const int start = half ? chunks0 * 16 : 0;               // this warp's columns
-      const int mine = half ? chunks - chunks0 : chunks0;      // in chunks of 16
-      // the tile's first row of the result, and how many of its rows from `start` on this lane writes
-      const int64_t out_row = K == kWeights ? (int64_t)tile.expert * z.q + tile.q : tile.row + tile.q;
-      const auto left_at = [&](int p) { return p < z.p ? tile.width - start : 0; };
-      if constexpr (kEight) {
-        float2 sum[16][4] = {};
-        for (int b = 0; ok && b < tile.blocks; ++b) {
-          ok = __all_sync(kAll, wait(&sh.scales_full[s.at], s.parity, sh) && wait(&sh.sums_full[d.at], d.parity, sh));
-          if (!ok)
-            break;
-          fence_after_sync();
-          const uint32_t from = lanes + d.at * kTileQ + start;
-          const float* by = scales + s.at * kTileQ + start;
-          uint32_t v[2][8];
-          if (mine > 0)
-            sums_load(v[0], from);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            if (c < 2 * mine) {
-              sums_wait(v[c & 1]);
-              if (c + 1 < 2 * mine)
-                sums_load(v[(c + 1) & 1], from + (c + 1) * 8);
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const float4 f = *reinterpret_cast<const float4*>(by + c * 8 + i * 4);
-                sum[c][2 * i] = __ffma2_rn(make_float2(__uint_as_float(v[c & 1][4 * i]), __uint_as_float(v[c & 1][4 * i + 1])),
-                                        make_float2(f.x, f.y), sum[c][2 * i]);
-                sum[c][2 * i + 1] = __ffma2_rn(make_float2(__uint_as_float(v[c & 1][4 * i + 2]), __uint_as_float(v[c & 1][4 * i + 3])),
-                                            make_float2(f.z, f.w), sum[c][2 * i + 1]);
-              }
-            }
-          }
-          fence_before_sync();
-          __syncwarp();
-          if (lane == 0) {
-            arrive(&sh.sums_empty[d.at]);
-            arrive(&sh.scales_empty[s.at]);
-          }
-          d.next();
-          s.next();
-        }
-        if (ok) {
-          const int p = tile.p + quarter * 32 + lane, left = left_at(p);
-          O* at = out + (out_row + start) * z.out_stride + p;
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            if (c < 2 * mine)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                if (c * 8 + i < left)
-                  *at = from_f32<O>(i & 1 ? sum[c][i / 2].y : sum[c][i / 2].x);
-                at += z.out_stride;
-              }
-        }
-      } else {
-        if (tile.blocks > 0) {
-          ok = __all_sync(kAll, wait(&sh.sums_full[d.at], d.parity, sh));
-          if (!ok)
-            break;
-          fence_after_sync();
-        }
-        const int p = tile.p + quarter * 32 + lane, left = left_at(p);
-        O* at = out + (out_row + start) * z.out_stride + p;
-        for (int c = 0; c < mine; ++c) {
-          uint32_t v[16] = {};
-          if (tile.blocks > 0) {
-            sums_load(v, lanes + d.at * kTileQ + start + c * 16);
-            sums_wait(v);
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (c * 16 + i < left)
-              *at = from_f32<O>(__uint_as_float(v[i]));
-            at += z.out_stride;
-          }
-        }
-        if (tile.blocks > 0) {
-          fence_before_sync();
-          __syncwarp();
-          if (lane == 0)
-            arrive(&sh.sums_empty[d.at]);
-          d.next();
-        }
-      }
+    if constexpr (eight(K)) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+      add_scaled<O>(z, out, sh);
+    } else {
+      write_sums<K, O>(z, out, sh);
     }
     if constexpr (K != kWeights) {
       // rows that no expert has
-      const int64_t kept = sh.row_start[z.experts];
-      for (int64_t r = kept + (int64_t)blockIdx.x * kSumWarps + warp - 4; r < z.num_rows;
-           r += (int64_t)gridDim.x * kSumWarps)
-        for (int i = lane; i < z.p; i += 32)
+      const int all = (int)gridDim.x * kSumWarps;
+      const int first = (int)blockIdx.x * kSumWarps + warp - (kThreads / 32 - kSumWarps);
+      for (int64_t r = sh.row_start[z.experts] + first; r < z.num_rows; r += all)
+        for (int i = lane; i < z.out_stride; i += 32)
           out[r * z.out_stride + i] = from_f32<O>(0.0f);
     }
     fence_before_sync();
@@ -596,7 +626,7 @@ product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant_
   __syncthreads();
   if (warp == 2) {
     fence_after_sync();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sh.tmem));
   }
 }
 
@@ -690,10 +720,11 @@ int check_sizes(int64_t num_rows, int64_t width, int64_t out_width, int32_t expe
     return SEGTOPK_ERROR_NOT_SUPPORTED;
   return SEGTOPK_SUCCESS;
 }
-int64_t forward_tiles(int64_t num_rows, int64_t out_width, int32_t experts)
+// At most as many tiles there are of `by` rows and `by_out` outputs: an expert
+// with r rows has at most r / by + 1 of each outputs, one without none.
+int64_t forward_tiles(int64_t num_rows, int by, int64_t out_width, int by_out, int32_t experts)
 {
-  // an expert with r rows has at most r / kTileQ + 1 tiles of each 128 outputs, and one without none
-  return (num_rows / kTileQ + std::min<int64_t>(experts, num_rows)) * ((out_width + kTileP - 1) / kTileP);
+  return (num_rows / by + std::min<int64_t>(experts, num_rows)) * ((out_width + by_out - 1) / by_out);
 }
 
 } // namespace
@@ -725,7 +756,7 @@ extern "C" int segtopk_expert_matmul(segtopk_dtype dtype, const void* rows, int6
   const int64_t line = turned ? in_stride : out_stride; // between rows of the weights in memory
   if (rc != SEGTOPK_SUCCESS || (dtype != SEGTOPK_F16 && dtype != SEGTOPK_BF16) || !float_type_of(out_dtype) ||
       width % 8 != 0 || (turned && out_width % 8 != 0) || row_stride > kMaxStride || line > kMaxStride ||
-      expert_stride > kMaxStride || forward_tiles(num_rows, out_width, experts) > kMaxTiles)
+      expert_stride > kMaxStride || forward_tiles(num_rows, kTileQ, out_width, kTileP, experts) > kMaxTiles)
     return SEGTOPK_ERROR_NOT_SUPPORTED;
   if (num_rows == 0)
     return SEGTOPK_SUCCESS;
@@ -741,7 +772,7 @@ extern "C" int segtopk_expert_matmul(segtopk_dtype dtype, const void* rows, int6
   cudaError_t e = turned ? describe(&p, map_type(dtype), 2, weights, out_width, width, experts, line, expert_stride, kDepth)
                          : describe(&p, map_type(dtype), 2, weights, width, out_width, experts, line, expert_stride, kTileP);
   if (e == cudaSuccess)
-    e = describe(&q, map_type(dtype), 2, rows, width, num_rows, 1, row_stride, num_rows * row_stride, kBoxQ);
+    e = describe(&q, map_type(dtype), 2, rows, width, num_rows, 1, row_stride, num_rows * row_stride, kBox);
   if (e != cudaSuccess)
     return record_cuda_error(e);
   Sizes z = {};
@@ -751,7 +782,7 @@ extern "C" int segtopk_expert_matmul(segtopk_dtype dtype, const void* rows, int6
   z.c = (int)width;
   z.instruction = instruction(dtype, !turned, true);
   z.out_stride = out_width;
-  const int64_t tiles = forward_tiles(num_rows, out_width, experts);
+  const int64_t tiles = forward_tiles(num_rows, kTileQ, out_width, kTileP, experts);
   return with_float_type(out_dtype, [&](auto zero) {
     using O = decltype(zero);
     return turned ? run<kForwardTurned, O>(p, q, offsets, z, out, sms, tiles, stream)
@@ -771,7 +802,7 @@ extern "C" int segtopk_expert_matmul_f8(const void* rows, int64_t num_rows, int6
       (out_width > 1 && out_stride < width) || expert_stride < 0 || scale_stride < 0)
     return SEGTOPK_ERROR_INVALID_VALUE;
   if (rc != SEGTOPK_SUCCESS || !float_type_of(out_dtype) || width % 16 != 0 || row_stride > kMaxStride ||
-      out_stride > kMaxStride || expert_stride > kMaxStride || forward_tiles(num_rows, out_width, experts) > kMaxTiles)
+      out_stride > kMaxStride || expert_stride > kMaxStride || forward_tiles(num_rows, kTileP, out_width, kTileP, experts) > kMaxTiles)
     return SEGTOPK_ERROR_NOT_SUPPORTED;
   if (num_rows == 0)
     return SEGTOPK_SUCCESS;
@@ -785,26 +816,31 @@ extern "C" int segtopk_expert_matmul_f8(const void* rows, int64_t num_rows, int6
   if ((rc = check_device(&sms)) != SEGTOPK_SUCCESS)
     return rc;
   CUtensorMap p, q;
-  cudaError_t e = describe(&p, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, weights, width, out_width, experts, out_stride,
-                           expert_stride, kTileP);
+  cudaError_t e = describe(&p, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, width, num_rows, 1, row_stride,
+                           num_rows * row_stride, kBox);
   if (e == cudaSuccess)
-    e = describe(&q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, width, num_rows, 1, row_stride, num_rows * row_stride, kBoxQ);
+    e = describe(&q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, weights, width, out_width, experts, out_stride, expert_stride,
+                 kTileP);
   if (e != cudaSuccess)
     return record_cuda_error(e);
+  // Tiles of 128 columns where those of 256 would leave SMs idle.
+  const int step = forward_tiles(num_rows, kTileP, out_width, kTileQ, experts) < 2 * sms ? kTileP : kTileQ;
+  const int64_t tiles = forward_tiles(num_rows, kTileP, out_width, step, experts);
   Sizes z = {};
   z.num_rows = num_rows;
   z.experts = experts;
-  z.p = (int)out_width;
+  z.q = (int)out_width;
   z.c = (int)width;
   z.instruction = instruction(SEGTOPK_F16, true, true); // e4m3, as code 0 of 8-bit types
   z.out_stride = out_width;
   z.row_scales = row_scales;
   z.scale_stride = scale_stride;
-  z.scale_vectors = aligned(row_scales, 16) && scale_stride % 4 == 0;
   z.weight_scales = weight_scales;
-  const int64_t tiles = forward_tiles(num_rows, out_width, experts);
+  z.step = step;
   return with_float_type(out_dtype, [&](auto zero) {
-    return run<kForward8, decltype(zero)>(p, q, offsets, z, out, sms, tiles, stream);
+    using O = decltype(zero);
+    z.out_vectors = rows_fit(out, out_width, out_width, sizeof(O), 16 / (int)sizeof(O));
+    return run<kForward8, O>(p, q, offsets, z, out, sms, tiles, stream);
   });
 }
 
