@@ -36,20 +36,35 @@ using namespace rows;
 
 constexpr int kThreads = 384;
 constexpr int kSumWarps = 8;     // of them the last
-constexpr int kTileP = 128;      // lanes of TMEM
+constexpr int kTileP = 128;      // of a block: the lanes of TMEM
 constexpr int kTileQ = 256;      // half of its columns
-constexpr int kStages = 4;
-constexpr int kBytesP = kTileP * 128, kBytesQ = kTileQ * 128;
-constexpr int kStageBytes = kBytesP + kBytesQ;
+constexpr int kOperandBytes = 192 << 10;
+constexpr int kMaxStages = 6;
+constexpr int kBytesP = kTileP * 128;
 constexpr int kBox = 32;         // rows of one copy of an expert's rows
 constexpr int kDepth = 64;       // rows of one copy where c runs over rows
+constexpr int kStepQ = 32;       // 16 for each block of a pair
 constexpr int kMaxExperts = SEGTOPK_MAX_EXPERTS;
 
-enum Kind { kForward8, kForward, kForwardTurned, kWeights };
+enum Kind { kForward8, kForward8Pair, kForward, kForwardTurned, kWeights };
+constexpr bool eight(Kind k) { return k == kForward8 || k == kForward8Pair; }
+// Two blocks, of one cluster, on a tile: 256 p, half of them in each block's
+// TMEM, and each reads half of the q for both.
+constexpr bool pair(Kind k) { return k != kForward8; }
+constexpr int blocks_of(Kind k) { return pair(k) ? 2 : 1; }
+constexpr bool p_by_rows(Kind k) { return eight(k) || k == kForward; } // rows of c in shared memory
+constexpr bool q_by_rows(Kind k) { return k != kWeights; }
+constexpr int tile_p(Kind k) { return kTileP * blocks_of(k); }
+constexpr int bytes_q(Kind k) { return kTileQ / blocks_of(k) * 128; }
+constexpr int stage_bytes(Kind k) { return kBytesP + bytes_q(k); }
+constexpr int stages_of(Kind k) { return kOperandBytes / stage_bytes(k); }
+static_assert(stages_of(kForward) <= kMaxStages);
 
 struct Control {
-  uint64_t full[kStages], empty[kStages];       // copies have landed; products have read them
-  uint64_t sums_full[2], sums_empty[2];         // TMEM's halves
+  uint64_t full[kMaxStages], empty[kMaxStages]; // copies (a pair's: at its first block) have landed; products have read them
+  uint64_t sums_full[2], sums_empty[2];         // TMEM's halves (empty: at the first block)
+  uint64_t end_full[kMaxStages];                // kWeights: an expert's last rows have landed,
+  uint64_t end_ready[kMaxStages];               // and in the second block those of others are gone
   uint64_t drained;                             // products behind a wait that ran out
   uint32_t tmem;
   int failed;                                   // a wait ran out: everybody leaves
@@ -57,7 +72,7 @@ struct Control {
   int tile_start[kMaxExperts + 1];              // experts' first tiles
   int row_start[kMaxExperts + 1];               // and rows
 };
-constexpr size_t kShared = 1024 + (size_t)kStages * kStageBytes + sizeof(Control);
+constexpr size_t kShared = 1024 + (size_t)kOperandBytes + sizeof(Control);
 static_assert(kShared <= 227 * 1024, "shared memory of a block");
 
 struct Sizes {
@@ -79,12 +94,21 @@ struct Sizes {
 __device__ __forceinline__ void fence_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-__device__ __forceinline__ void tile_load(void* to, const CUtensorMap* map, int x, int y, int z, uint64_t* bar)
+// A copy that counts at `bar`: an address in the cluster's shared memory, of
+// either block of a pair.
+template <bool PAIR>
+__device__ __forceinline__ void tile_load(void* to, const CUtensorMap* map, int x, int y, int z, uint32_t bar)
 {
-  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-               "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(to)),
-               "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
-               : "memory");
+  if constexpr (PAIR)
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(to)),
+                 "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(to)),
+                 "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+                 : "memory");
 }
 
 // Shared-memory operand of 128-byte rows, swizzled over eight of them. Rows
@@ -97,29 +121,51 @@ __device__ __forceinline__ uint64_t operand(uint32_t address)
   return (uint64_t)(address >> 4) | lead << 16 | (uint64_t)(1024 / 16) << 32 | 1ull << 46 | 2ull << 61;
 }
 
-template <bool EIGHT>
+template <Kind K>
 __device__ __forceinline__ void multiply(uint32_t sums, uint64_t p, uint64_t q, uint32_t instruction, bool add)
 {
-  if constexpr (EIGHT)
-    asm volatile("{\n .reg .pred a;\n setp.ne.b32 a, %4, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, a;\n}" ::"r"(sums),
-                 "l"(p), "l"(q), "r"(instruction), "r"((uint32_t)add)
-                 : "memory");
+#define SEGTOPK_MULTIPLY(GROUP, TYPE)                                                                            \
+  asm volatile("{\n .reg .pred a;\n setp.ne.b32 a, %4, 0;\n"                                                    \
+               " tcgen05.mma.cta_group::" GROUP ".kind::" TYPE " [%0], %1, %2, %3, a;\n}" ::"r"(sums),           \
+               "l"(p), "l"(q), "r"(instruction), "r"((uint32_t)add)                                              \
+               : "memory")
+  if constexpr (eight(K) && pair(K))
+    SEGTOPK_MULTIPLY("2", "f8f6f4");
+  else if constexpr (eight(K))
+    SEGTOPK_MULTIPLY("1", "f8f6f4");
   else
-    asm volatile("{\n .reg .pred a;\n setp.ne.b32 a, %4, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, a;\n}" ::"r"(sums),
-                 "l"(p), "l"(q), "r"(instruction), "r"((uint32_t)add)
-                 : "memory");
+    SEGTOPK_MULTIPLY("2", "f16");
+#undef SEGTOPK_MULTIPLY
 }
-// Arrives at `bar` once the products issued so far are done.
+// Arrives at `bar`, a pair's at both blocks', once the products issued so far
+// are done.
+template <bool PAIR>
 __device__ __forceinline__ void commit(uint64_t* bar)
 {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
+  if constexpr (PAIR)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                   smem_addr(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
 }
-__device__ __forceinline__ void arrive(uint64_t* bar)
+// At a barrier of either block of a pair.
+__device__ __forceinline__ void arrive(uint32_t bar)
 {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The address of the first block's `bar`.
+template <Kind K>
+__device__ __forceinline__ uint32_t at_first(uint64_t* bar)
+{
+  return pair(K) ? dsmem_map(smem_addr(bar), 0) : smem_addr(bar);
+}
+template <Kind K>
+__device__ __forceinline__ int rank() // in the pair
+{
+  return pair(K) ? (int)(blockIdx.x & 1) : 0;
 }
 
 // Columns of this warp's 32 lanes; the values are there after sums_wait()
@@ -140,26 +186,36 @@ __device__ __forceinline__ void sums_wait(uint32_t (&v)[16])
                :
                : "memory");
 }
-__device__ __forceinline__ void sums_load(uint32_t (&v)[32], uint32_t at)
+__device__ __forceinline__ void sums_load(uint32_t (&v)[64], uint32_t at)
 {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 "
                "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
-               "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+               "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, "
+               "%38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, "
+               "%56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
                  "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
                  "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]),
                  "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]),
-                 "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+                 "=r"(v[29]), "=r"(v[30]), "=r"(v[31]), "=r"(v[32]), "=r"(v[33]), "=r"(v[34]), "=r"(v[35]),
+                 "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]), "=r"(v[40]), "=r"(v[41]), "=r"(v[42]),
+                 "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]), "=r"(v[48]), "=r"(v[49]),
+                 "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]), "=r"(v[56]),
+                 "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
                : "r"(at));
 }
-__device__ __forceinline__ void sums_wait(uint32_t (&v)[32])
+__device__ __forceinline__ void sums_wait(uint32_t (&v)[64])
 {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
                  "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
                  "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
                  "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
-                 "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 "+r"(v[29]), "+r"(v[30]), "+r"(v[31]), "+r"(v[32]), "+r"(v[33]), "+r"(v[34]), "+r"(v[35]),
+                 "+r"(v[36]), "+r"(v[37]), "+r"(v[38]), "+r"(v[39]), "+r"(v[40]), "+r"(v[41]), "+r"(v[42]),
+                 "+r"(v[43]), "+r"(v[44]), "+r"(v[45]), "+r"(v[46]), "+r"(v[47]), "+r"(v[48]), "+r"(v[49]),
+                 "+r"(v[50]), "+r"(v[51]), "+r"(v[52]), "+r"(v[53]), "+r"(v[54]), "+r"(v[55]), "+r"(v[56]),
+                 "+r"(v[57]), "+r"(v[58]), "+r"(v[59]), "+r"(v[60]), "+r"(v[61]), "+r"(v[62]), "+r"(v[63])
                :
                : "memory");
 }
@@ -205,20 +261,20 @@ __host__ __device__ __forceinline__ int pieces(int n, int size) { return (n + si
 struct Tile {
   int expert;
   int p;          // first
-  int q, width;   // first and how many; rounded up to 16 there are
+  int q, width;   // first and how many; kStepQ times as many as hold them are computed
   int row, rows;  // the expert's rows
   int blocks;     // of c
 };
 
 // Tiles of an expert with this many rows. Where q are its rows, or its inputs
 // or outputs, it goes to as few tiles as hold it, of even widths in steps of
-// 16; none is empty, since all but the last are no wider than kTileQ.
+// kStepQ; none is empty, since all but the last are no wider than kTileQ.
 template <Kind K>
-__device__ __forceinline__ int parts_p(int rows, const Sizes& z) { return pieces(K == kForward8 ? rows : z.p, kTileP); }
+__device__ __forceinline__ int parts_p(int rows, const Sizes& z) { return pieces(eight(K) ? rows : z.p, tile_p(K)); }
 template <Kind K>
 __device__ __forceinline__ int parts_q(int rows, const Sizes& z)
 {
-  return K == kForward8 ? pieces(z.q, z.step) : pieces(K == kWeights ? z.q : rows, kTileQ);
+  return eight(K) ? pieces(z.q, z.step) : pieces(K == kWeights ? z.q : rows, kTileQ);
 }
 
 template <Kind K>
@@ -237,19 +293,19 @@ __device__ __forceinline__ Tile tile_at(int t, const Sizes& z, const Control& sh
   r.row = sh.row_start[low];
   r.rows = sh.row_start[low + 1] - r.row;
   const int i = t - sh.tile_start[low];
-  if constexpr (K == kForward8) {
+  if constexpr (eight(K)) {
     const int parts = parts_p<K>(r.rows, z);
-    r.p = i % parts * kTileP;
+    r.p = i % parts * tile_p(K);
     r.q = i / parts * z.step;
     r.width = min(z.step, z.q - r.q);
     r.blocks = pieces(z.c, 128);
   } else {
     const int q = K == kWeights ? z.q : r.rows;
     const int parts = parts_q<K>(r.rows, z);
-    const int step = (pieces(q, parts) + 15) / 16 * 16;
+    const int step = pieces(pieces(q, parts), kStepQ) * kStepQ;
     r.q = i % parts * step;
     r.width = min(step, q - r.q);
-    r.p = i / parts * kTileP;
+    r.p = i / parts * tile_p(K);
     r.blocks = K == kWeights ? pieces(r.rows, kDepth) : pieces(z.c, 64);
   }
   return r;
@@ -321,58 +377,70 @@ __device__ void find_tiles(const int64_t* offsets, const Sizes& z, Control& sh)
 // ---------------------------------------------------------------------------
 // Kernel
 // ---------------------------------------------------------------------------
-constexpr bool eight(Kind k) { return k == kForward8; }
-constexpr bool p_by_rows(Kind k) { return k == kForward8 || k == kForward; } // rows of c in shared memory
-constexpr bool q_by_rows(Kind k) { return k != kWeights; }
-
-// One thread: copies of the tiles' operands, as stages get free.
+// One thread: copies of this block's operands, as stages get free. A pair's
+// count at the first block, which expects those of both.
 template <Kind K>
 __device__ void copy_operands(const CUtensorMap& p_map, const CUtensorMap& q_map, const Sizes& z, char* stages, Control& sh)
 {
-  const int tiles = sh.tile_start[z.experts];
+  constexpr int kStages = stages_of(K);
+  const int tiles = sh.tile_start[z.experts], me = rank<K>();
   Ring<kStages> s;
   int used = 0; // stages whose copies are under way or have landed
   bool ok = true;
-  for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+  for (int t = blockIdx.x / blocks_of(K); ok && t < tiles; t += gridDim.x / blocks_of(K)) {
     const Tile tile = tile_at<K>(t, z, sh);
+    const int width = pieces(tile.width, kStepQ) * kStepQ / blocks_of(K); // of q in this block
+    const int first_p = tile.p + me * kTileP, first_q = tile.q + me * width;
     // boxes are copied whole, whatever of them there is
-    const int boxes_p = K == kForward8 ? pieces(min(kTileP, tile.rows - tile.p), kBox) : 0;
-    const int boxes_q = pieces(tile.width, K == kForward8 ? kTileP : q_by_rows(K) ? kBox : 64);
-    const int bytes = K == kForward8 ? (boxes_p * kBox + boxes_q * kTileP) * 128
-                                     : (kTileP + boxes_q * (q_by_rows(K) ? kBox : 64)) * 128;
+    auto boxes_p = [&](int p) { return pieces(max(0, min(kTileP, tile.rows - p)), kBox); }; // 8 bits: rows
+    const int boxes_q = pieces(width, eight(K) ? kTileP : q_by_rows(K) ? kBox : 64);
+    int bytes = boxes_q * (eight(K) ? kTileP : q_by_rows(K) ? kBox : 64) * 128;
+    if constexpr (eight(K))
+      bytes += boxes_p(first_p) * kBox * 128;
+    else
+      bytes += kBytesP;
+    const int bytes_other = !pair(K) ? 0 : eight(K) ? bytes + (boxes_p(tile.p + kTileP) - boxes_p(tile.p)) * kBox * 128 : bytes;
     for (int b = 0; b < tile.blocks; ++b) {
       ok = wait(&sh.empty[s.at], s.parity ^ 1, sh);
       if (!ok)
         break;
-      char *const to_p = stages + s.at * kStageBytes, *const to_q = to_p + kBytesP;
-      uint64_t* const bar = &sh.full[s.at];
-      mbar_arrive_expect_tx(bar, bytes);
-      if constexpr (K == kForward8) {
-        for (int i = 0; i < boxes_p; ++i)
-          tile_load(to_p + i * kBox * 128, &p_map, b * 128, tile.row + tile.p + i * kBox, 0, bar);
+      char *const to_p = stages + s.at * stage_bytes(K), *const to_q = to_p + kBytesP;
+      uint32_t bar = at_first<K>(&sh.full[s.at]);
+      if (K == kWeights && (b + 1) * kDepth > tile.rows) {
+        // an expert's last rows: each block of the pair first takes out those of others
+        if (me == 0)
+          arrive(bar);
+        bar = smem_addr(&sh.end_full[s.at]);
+        mbar_arrive_expect_tx(&sh.end_full[s.at], bytes);
+      } else if (me == 0) {
+        mbar_arrive_expect_tx(&sh.full[s.at], bytes + bytes_other);
+      }
+      if constexpr (eight(K)) {
+        for (int i = 0, n = boxes_p(first_p); i < n; ++i)
+          tile_load<pair(K)>(to_p + i * kBox * 128, &p_map, b * 128, tile.row + first_p + i * kBox, 0, bar);
         for (int i = 0; i < boxes_q; ++i)
-          tile_load(to_q + i * kTileP * 128, &q_map, b * 128, tile.q + i * kTileP, tile.expert, bar);
+          tile_load<pair(K)>(to_q + i * kTileP * 128, &q_map, b * 128, first_q + i * kTileP, tile.expert, bar);
       } else if constexpr (K == kWeights) {
         const int y = tile.row + b * kDepth;
         for (int i = 0; i < 2; ++i)
-          tile_load(to_p + i * kDepth * 128, &p_map, tile.p + i * 64, y, 0, bar);
+          tile_load<true>(to_p + i * kDepth * 128, &p_map, first_p + i * 64, y, 0, bar);
         for (int i = 0; i < boxes_q; ++i)
-          tile_load(to_q + i * kDepth * 128, &q_map, tile.q + i * 64, y, 0, bar);
+          tile_load<true>(to_q + i * kDepth * 128, &q_map, first_q + i * 64, y, 0, bar);
       } else {
         if constexpr (K == kForward)
-          tile_load(to_p, &p_map, b * 64, tile.p, tile.expert, bar);
+          tile_load<true>(to_p, &p_map, b * 64, first_p, tile.expert, bar);
         else
           for (int i = 0; i < 2; ++i)
-            tile_load(to_p + i * kDepth * 128, &p_map, tile.p + i * 64, b * kDepth, tile.expert, bar);
+            tile_load<true>(to_p + i * kDepth * 128, &p_map, first_p + i * 64, b * kDepth, tile.expert, bar);
         for (int i = 0; i < boxes_q; ++i)
-          tile_load(to_q + i * kBox * 128, &q_map, b * 64, tile.row + tile.q + i * kBox, 0, bar);
+          tile_load<true>(to_q + i * kBox * 128, &q_map, b * 64, tile.row + first_q + i * kBox, 0, bar);
       }
       used = min(used + 1, kStages);
       s.next();
     }
   }
-  if (!ok) {
-    // what is under way lands before the block ends (a second each at most)
+  if (!ok && me == 0) {
+    // what is under way lands before the blocks end (a second each at most)
     for (int i = 0; i < used; ++i) {
       s.at = s.at == 0 ? kStages - 1 : s.at - 1;
       s.parity ^= s.at == kStages - 1;
@@ -381,58 +449,79 @@ __device__ void copy_operands(const CUtensorMap& p_map, const CUtensorMap& q_map
   }
 }
 
-// One warp: the products of the blocks that have landed.
+// kWeights, one warp of each block: in an expert's last block of rows, once it
+// has landed, the rows from `left` on become zeros, as the products read them.
+__device__ bool clear_rows(char* stage, int copies, int left, uint64_t* landed, uint32_t parity, Control& sh)
+{
+  const int lane = threadIdx.x & 31;
+  if (!__all_sync(kAll, wait(landed, parity, sh)))
+    return false;
+  for (int i = 0; i < copies; ++i)
+    for (int at = left * 128 + lane * 16; at < kDepth * 128; at += 512)
+      *reinterpret_cast<uint4*>(stage + i * kDepth * 128 + at) = uint4{};
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  return true;
+}
+
+// One warp: the products of the blocks that have landed; the first block
+// issues a pair's.
 template <Kind K>
 __device__ void issue_products(const Sizes& z, char* stages, Control& sh)
 {
-  const int lane = threadIdx.x & 31, tiles = sh.tile_start[z.experts];
+  const int lane = threadIdx.x & 31, tiles = sh.tile_start[z.experts], me = rank<K>();
   const uint32_t tmem = sh.tmem;
-  Ring<kStages> s;
+  Ring<stages_of(K)> s;
   Ring<2> d;
+  uint32_t ends_before = 0; // kWeights: a bit for each stage, the parity of its last blocks of rows
   bool ok = true;
-  for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+  for (int t = blockIdx.x / blocks_of(K); ok && t < tiles; t += gridDim.x / blocks_of(K)) {
     const Tile tile = tile_at<K>(t, z, sh);
-    const uint32_t instruction = z.instruction | (uint32_t)((tile.width + 15) / 16 * 2) << 17;
+    const int width = pieces(tile.width, kStepQ) * kStepQ;
+    const uint32_t instruction = z.instruction | (uint32_t)(width / 8) << 17;
     for (int b = 0; b < tile.blocks; ++b) {
       // the sums of one block, or of all
       const bool first = eight(K) || b == 0, last = eight(K) || b == tile.blocks - 1;
-      ok = (!first || wait(&sh.sums_empty[d.at], d.parity ^ 1, sh)) && wait(&sh.full[s.at], s.parity, sh);
-      ok = __all_sync(kAll, ok);
+      char* const from = stages + s.at * stage_bytes(K);
+      const int left = tile.rows - b * kDepth;
+      const bool ends = K == kWeights && left < kDepth;
+      if (me == 0) {
+        ok = (!first || wait(&sh.sums_empty[d.at], d.parity ^ 1, sh)) && wait(&sh.full[s.at], s.parity, sh);
+        ok = __all_sync(kAll, ok);
+      }
+      if (ok && ends) {
+        const uint32_t parity = ends_before >> s.at & 1;
+        ends_before ^= 1u << s.at;
+        ok = clear_rows(from, 2 + pieces(width / 2, 64), left, &sh.end_full[s.at], parity, sh);
+        if (ok && me == 0)
+          ok = __all_sync(kAll, wait(&sh.end_ready[s.at], parity, sh));
+        else if (ok && lane == 0)
+          arrive(at_first<K>(&sh.end_ready[s.at]));
+      }
       if (!ok)
         break;
-      char* const from = stages + s.at * kStageBytes;
-      if constexpr (K == kWeights) {
-        // rows of the next expert, or of none, do not count
-        const int left = tile.rows - b * kDepth;
-        if (left < kDepth) {
-          const int copies = 2 + pieces(tile.width, 64);
-          for (int i = 0; i < copies; ++i)
-            for (int at = left * 128 + lane * 16; at < kDepth * 128; at += 512)
-              *reinterpret_cast<uint4*>(from + i * kDepth * 128 + at) = uint4{};
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-        }
-      }
-      fence_after_sync();
-      if (lane == 0) {
-        const uint64_t p = operand<p_by_rows(K)>(smem_addr(from)), q = operand<q_by_rows(K)>(smem_addr(from) + kBytesP);
-        // four products: 32 bytes of c on, or 16 rows of 128 bytes
+      if (me == 0) {
+        fence_after_sync();
+        if (lane == 0) {
+          const uint64_t p = operand<p_by_rows(K)>(smem_addr(from)), q = operand<q_by_rows(K)>(smem_addr(from) + kBytesP);
+          // four products: 32 bytes of c on, or 16 rows of 128 bytes
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          multiply<eight(K)>(tmem + d.at * kTileQ, p + i * (p_by_rows(K) ? 2 : 128), q + i * (q_by_rows(K) ? 2 : 128),
-                             instruction, !first || i > 0);
-        commit(&sh.empty[s.at]);
-        if (last)
-          commit(&sh.sums_full[d.at]);
+          for (int i = 0; i < 4; ++i)
+            multiply<K>(tmem + d.at * kTileQ, p + i * (p_by_rows(K) ? 2 : 128), q + i * (q_by_rows(K) ? 2 : 128),
+                        instruction, !first || i > 0);
+          commit<pair(K)>(&sh.empty[s.at]);
+          if (last)
+            commit<pair(K)>(&sh.sums_full[d.at]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
       s.next();
       if (last)
         d.next();
     }
   }
-  if (!ok && lane == 0) {
-    commit(&sh.drained); // what is under way ends before the block does
+  if (!ok && me == 0 && lane == 0) {
+    commit<pair(K)>(&sh.drained); // what is under way ends before the blocks do
     mbar_wait(&sh.drained, 0);
   }
   __syncwarp();
@@ -441,7 +530,7 @@ __device__ void issue_products(const Sizes& z, char* stages, Control& sh)
 // kSumWarps warps, 8-bit operands: each block's sums times their scales. A
 // thread has one row, so one factor for all its columns of a block, which lie
 // in one block of the weights' scales.
-template <class O>
+template <Kind K, class O>
 __device__ void add_scaled(const Sizes& z, O* out, Control& sh)
 {
   const int warp = threadIdx.x / 32 - (kThreads / 32 - kSumWarps), lane = threadIdx.x & 31;
@@ -449,11 +538,11 @@ __device__ void add_scaled(const Sizes& z, O* out, Control& sh)
   const uint32_t lanes = sh.tmem + ((uint32_t)quarter * 32 << 16);
   const int tiles = sh.tile_start[z.experts];
   Ring<2> d;
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const Tile tile = tile_at<kForward8>(t, z, sh);
-    const int mine = (tile.width - start + 31) / 32; // steps of 32 columns
-    const int row = tile.p + quarter * 32 + lane;
-    const bool on = row < tile.rows && mine > 0;
+  for (int t = blockIdx.x / blocks_of(K); t < tiles; t += gridDim.x / blocks_of(K)) {
+    const Tile tile = tile_at<K>(t, z, sh);
+    const int columns = tile.width - start; // the rest of them
+    const int row = tile.p + rank<K>() * kTileP + quarter * 32 + lane;
+    const bool on = row < tile.rows && columns > 0;
     const float* by_row = z.row_scales + (int64_t)(tile.row + row) * z.scale_stride;
     const float* by_weight =
       z.weight_scales + ((int64_t)tile.expert * pieces(z.q, 128) + (tile.q + start) / 128) * tile.blocks;
@@ -467,30 +556,26 @@ __device__ void add_scaled(const Sizes& z, O* out, Control& sh)
         return;
       fence_after_sync();
       const uint32_t from = lanes + d.at * kTileQ + start;
-      uint32_t v[2][32];
-      if (mine > 0)
-        sums_load(v[0], from);
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c < mine) {
-          sums_wait(v[c & 1]);
-          if (c + 1 < mine)
-            sums_load(v[(c + 1) & 1], from + (c + 1) * 32);
+      for (int c = 0; c < 2; ++c)
+        if (c * 64 < columns) {
+          uint32_t v[64];
+          sums_load(v, from + c * 64);
+          sums_wait(v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            sum[c * 16 + i] =
-              __ffma2_rn(make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), f,
-                         sum[c * 16 + i]);
+          for (int i = 0; i < 32; ++i)
+            sum[c * 32 + i] =
+              __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f, sum[c * 32 + i]);
         }
       fence_before_sync();
       __syncwarp();
       if (lane == 0)
-        arrive(&sh.sums_empty[d.at]);
+        arrive(at_first<K>(&sh.sums_empty[d.at]));
       d.next();
     }
     if (on) {
       O* const to = out + (int64_t)(tile.row + row) * z.out_stride + tile.q + start;
-      const int left = min(128, tile.width - start);
+      const int left = min(128, columns);
       if (z.out_vectors) { // left is a multiple of V
         constexpr int V = 16 / (int)sizeof(O);
 #pragma unroll
@@ -522,12 +607,12 @@ __device__ void write_sums(const Sizes& z, O* out, Control& sh)
   const uint32_t lanes = sh.tmem + ((uint32_t)quarter * 32 << 16);
   const int tiles = sh.tile_start[z.experts];
   Ring<2> d;
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+  for (int t = blockIdx.x / blocks_of(K); t < tiles; t += gridDim.x / blocks_of(K)) {
     const Tile tile = tile_at<K>(t, z, sh);
     // half of the columns, in steps of 16
     const int steps = (tile.width + 15) / 16, steps0 = (steps + 1) / 2;
     const int start = warp < 4 ? 0 : steps0 * 16, mine = warp < 4 ? steps0 : steps - steps0;
-    const int p = tile.p + quarter * 32 + lane;
+    const int p = tile.p + rank<K>() * kTileP + quarter * 32 + lane;
     const int left = p < z.p ? tile.width - start : 0; // columns to write
     const int64_t row = K == kWeights ? (int64_t)tile.expert * z.q + tile.q : tile.row + tile.q;
     O* at = out + (row + start) * z.out_stride + p;
@@ -554,44 +639,52 @@ __device__ void write_sums(const Sizes& z, O* out, Control& sh)
       fence_before_sync();
       __syncwarp();
       if (lane == 0)
-        arrive(&sh.sums_empty[d.at]);
+        arrive(at_first<K>(&sh.sums_empty[d.at]));
       d.next();
     }
   }
 }
 
 template <Kind K, class O>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(blocks_of(K), 1, 1) __launch_bounds__(kThreads, 1)
 product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                const int64_t* offsets, const __grid_constant__ Sizes z, O* out)
 {
   extern __shared__ char dynamic[];
   char* const stages = dynamic + (-smem_addr(dynamic) & 1023);
-  Control& sh = *reinterpret_cast<Control*>(stages + kStages * kStageBytes);
+  Control& sh = *reinterpret_cast<Control*>(stages + kOperandBytes);
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.end_full[i], 1);
+      mbar_init(&sh.end_ready[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.sums_full[i], 1);
-      mbar_init(&sh.sums_empty[i], kSumWarps);
+      mbar_init(&sh.sums_empty[i], kSumWarps * blocks_of(K));
     }
     mbar_init(&sh.drained, 1);
     fence_mbar_init();
     sh.failed = 0;
   }
   if (warp == 2) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem))
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if constexpr (pair(K)) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
     fence_before_sync();
   }
   wait_for_previous();
   allow_next();
   find_tiles<K>(offsets, z, sh); // ends with a barrier
+  if constexpr (pair(K))
+    cluster_sync(); // the other block's barriers are there too
   fence_after_sync();
 
   // With 8-bit operands a thread that adds up has 128 sums. What the other
@@ -609,7 +702,7 @@ product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant_
   } else {
     if constexpr (eight(K)) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-      add_scaled<O>(z, out, sh);
+      add_scaled<K, O>(z, out, sh);
     } else {
       write_sums<K, O>(z, out, sh);
     }
@@ -623,10 +716,17 @@ product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant_
     }
     fence_before_sync();
   }
-  __syncthreads();
+  __syncwarp();
+  if constexpr (pair(K))
+    cluster_sync(); // nothing arrives here or reads from here any more
+  else
+    __syncthreads();
   if (warp == 2) {
     fence_after_sync();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sh.tmem));
+    if constexpr (pair(K))
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(sh.tmem));
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sh.tmem));
   }
 }
 
@@ -688,7 +788,7 @@ int run(const CUtensorMap& p, const CUtensorMap& q, const int64_t* offsets, cons
   const cudaError_t e = allow_shared<K, O>();
   if (e != cudaSuccess)
     return record_cuda_error(e);
-  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(sms, most_tiles));
+  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(sms / blocks_of(K), most_tiles)) * blocks_of(K);
   return finish(launch(product_kernel<K, O>, dim3(grid), kThreads, kShared, (cudaStream_t)stream, p, q, offsets, z, (O*)out), 1);
 }
 
@@ -701,11 +801,11 @@ constexpr int64_t kMaxSide = 1 << 20;
 constexpr int64_t kMaxTiles = 1 << 30;
 constexpr int64_t kMaxStride = 1ll << 36;
 
-uint32_t instruction(int dtype, bool p_by_rows, bool q_by_rows) // sums in 32 bits, 128 lanes
+// Sums in 32 bits; type: 0 for f16 and e4m3, 1 for bf16.
+uint32_t instruction(Kind k, uint32_t type)
 {
-  const uint32_t type = dtype == SEGTOPK_BF16 ? 1 : 0;
-  return 1u << 4 | type << 7 | type << 10 | (uint32_t)!p_by_rows << 15 | (uint32_t)!q_by_rows << 16 |
-         (uint32_t)(kTileP / 16) << 24;
+  return 1u << 4 | type << 7 | type << 10 | (uint32_t)!p_by_rows(k) << 15 | (uint32_t)!q_by_rows(k) << 16 |
+         (uint32_t)(tile_p(k) / 16) << 24;
 }
 CUtensorMapDataType map_type(int dtype)
 {
@@ -780,7 +880,7 @@ extern "C" int segtopk_expert_matmul(segtopk_dtype dtype, const void* rows, int6
   z.experts = experts;
   z.p = (int)out_width;
   z.c = (int)width;
-  z.instruction = instruction(dtype, !turned, true);
+  z.instruction = instruction(turned ? kForwardTurned : kForward, dtype == SEGTOPK_BF16);
   z.out_stride = out_width;
   const int64_t tiles = forward_tiles(num_rows, kTileQ, out_width, kTileP, experts);
   return with_float_type(out_dtype, [&](auto zero) {
@@ -823,15 +923,17 @@ extern "C" int segtopk_expert_matmul_f8(const void* rows, int64_t num_rows, int6
                  kTileP);
   if (e != cudaSuccess)
     return record_cuda_error(e);
-  // Tiles of 128 columns where those of 256 would leave SMs idle.
+  // Tiles of 128 columns where those of 256 would leave SMs idle. Pairs where
+  // experts have rows for both blocks.
   const int step = forward_tiles(num_rows, kTileP, out_width, kTileQ, experts) < 2 * sms ? kTileP : kTileQ;
+  const bool by_pairs = step == kTileQ && num_rows / experts >= 256;
   const int64_t tiles = forward_tiles(num_rows, kTileP, out_width, step, experts);
   Sizes z = {};
   z.num_rows = num_rows;
   z.experts = experts;
   z.q = (int)out_width;
   z.c = (int)width;
-  z.instruction = instruction(SEGTOPK_F16, true, true); // e4m3, as code 0 of 8-bit types
+  z.instruction = instruction(by_pairs ? kForward8Pair : kForward8, 0);
   z.out_stride = out_width;
   z.row_scales = row_scales;
   z.scale_stride = scale_stride;
@@ -840,7 +942,8 @@ extern "C" int segtopk_expert_matmul_f8(const void* rows, int64_t num_rows, int6
   return with_float_type(out_dtype, [&](auto zero) {
     using O = decltype(zero);
     z.out_vectors = rows_fit(out, out_width, out_width, sizeof(O), 16 / (int)sizeof(O));
-    return run<kForward8, O>(p, q, offsets, z, out, sms, tiles, stream);
+    return by_pairs ? run<kForward8Pair, O>(p, q, offsets, z, out, sms, tiles, stream)
+                    : run<kForward8, O>(p, q, offsets, z, out, sms, tiles, stream);
   });
 }
 
@@ -882,7 +985,7 @@ extern "C" int segtopk_expert_matmul_weights(segtopk_dtype dtype, const void* a_
   z.experts = experts;
   z.p = (int)b_width;
   z.q = (int)a_width;
-  z.instruction = instruction(dtype, false, false);
+  z.instruction = instruction(kWeights, dtype == SEGTOPK_BF16);
   z.out_stride = b_width;
   return with_float_type(out_dtype, [&](auto zero) {
     return run<kWeights, decltype(zero)>(p, q, offsets, z, out, sms, tiles, stream);
