@@ -151,8 +151,15 @@ __device__ __forceinline__ void commit(uint64_t* bar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
                  : "memory");
 }
-// At a barrier of either block of a pair.
+// At a barrier of either block of a pair. What the other block has to see of
+// this one's memory goes with the second form only: it waits until all of it
+// is visible there, and once every block of 8-bit operands that doubled the
+// time of a product.
 __device__ __forceinline__ void arrive(uint32_t bar)
+{
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void release(uint32_t bar)
 {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -168,22 +175,17 @@ __device__ __forceinline__ int rank() // in the pair
   return pair(K) ? (int)(blockIdx.x & 1) : 0;
 }
 
-// Columns of this warp's 32 lanes; the values are there after sums_wait()
-// has been given them.
+// Columns of this warp's 32 lanes. Load and wait are one statement: values
+// that pass through a second one as operands were copied, 64 of them, which
+// took longer than the products.
 __device__ __forceinline__ void sums_load(uint32_t (&v)[16], uint32_t at)
 {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+               "tcgen05.wait::ld.sync.aligned;"
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
                  "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-               : "r"(at));
-}
-__device__ __forceinline__ void sums_wait(uint32_t (&v)[16])
-{
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
-               :
+               : "r"(at)
                : "memory");
 }
 __device__ __forceinline__ void sums_load(uint32_t (&v)[64], uint32_t at)
@@ -192,7 +194,8 @@ __device__ __forceinline__ void sums_load(uint32_t (&v)[64], uint32_t at)
                "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
                "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, "
                "%38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, "
-               "%56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+               "%56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n"
+               "tcgen05.wait::ld.sync.aligned;"
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
                  "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
                  "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]),
@@ -202,21 +205,7 @@ __device__ __forceinline__ void sums_load(uint32_t (&v)[64], uint32_t at)
                  "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]), "=r"(v[48]), "=r"(v[49]),
                  "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]), "=r"(v[56]),
                  "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
-               : "r"(at));
-}
-__device__ __forceinline__ void sums_wait(uint32_t (&v)[64])
-{
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
-                 "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
-                 "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
-                 "+r"(v[29]), "+r"(v[30]), "+r"(v[31]), "+r"(v[32]), "+r"(v[33]), "+r"(v[34]), "+r"(v[35]),
-                 "+r"(v[36]), "+r"(v[37]), "+r"(v[38]), "+r"(v[39]), "+r"(v[40]), "+r"(v[41]), "+r"(v[42]),
-                 "+r"(v[43]), "+r"(v[44]), "+r"(v[45]), "+r"(v[46]), "+r"(v[47]), "+r"(v[48]), "+r"(v[49]),
-                 "+r"(v[50]), "+r"(v[51]), "+r"(v[52]), "+r"(v[53]), "+r"(v[54]), "+r"(v[55]), "+r"(v[56]),
-                 "+r"(v[57]), "+r"(v[58]), "+r"(v[59]), "+r"(v[60]), "+r"(v[61]), "+r"(v[62]), "+r"(v[63])
-               :
+               : "r"(at)
                : "memory");
 }
 
@@ -496,7 +485,7 @@ __device__ void issue_products(const Sizes& z, char* stages, Control& sh)
         if (ok && me == 0)
           ok = __all_sync(kAll, wait(&sh.end_ready[s.at], parity, sh));
         else if (ok && lane == 0)
-          arrive(at_first<K>(&sh.end_ready[s.at]));
+          release(at_first<K>(&sh.end_ready[s.at]));
       }
       if (!ok)
         break;
@@ -557,16 +546,16 @@ __device__ void add_scaled(const Sizes& z, O* out, Control& sh)
       fence_after_sync();
       const uint32_t from = lanes + d.at * kTileQ + start;
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (c * 64 < columns) {
-          uint32_t v[64];
-          sums_load(v, from + c * 64);
-          sums_wait(v);
+      for (int c = 0; c < 2; ++c) {
+        if (columns <= 0)
+          break;
+        uint32_t v[64];
+        sums_load(v, from + c * 64);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            sum[c * 32 + i] =
-              __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f, sum[c * 32 + i]);
-        }
+        for (int i = 0; i < 32; ++i)
+          sum[c * 32 + i] =
+            __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f, sum[c * 32 + i]);
+      }
       fence_before_sync();
       __syncwarp();
       if (lane == 0)
@@ -626,7 +615,6 @@ __device__ void write_sums(const Sizes& z, O* out, Control& sh)
       uint32_t v[16] = {};
       if (any) {
         sums_load(v, lanes + d.at * kTileQ + start + c * 16);
-        sums_wait(v);
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
