@@ -64,7 +64,7 @@ struct Control {
   uint64_t full[kMaxStages], empty[kMaxStages]; // copies (a pair's: at its first block) have landed; products have read them
   uint64_t sums_full[2], sums_empty[2];         // TMEM's halves (empty: at the first block)
   uint64_t end_full[kMaxStages];                // kWeights: an expert's last rows have landed,
-  uint64_t end_ready[kMaxStages];               // and in the second block those of others are gone
+  uint64_t end_ready[kMaxStages];               // and in both blocks those of others are gone
   uint64_t drained;                             // products behind a wait that ran out
   uint32_t tmem;
   int failed;                                   // a wait ran out: everybody leaves
@@ -439,81 +439,79 @@ __device__ void copy_operands(const CUtensorMap& p_map, const CUtensorMap& q_map
 }
 
 // kWeights, one warp of each block: in an expert's last block of rows, once it
-// has landed, the rows from `left` on become zeros, as the products read them.
-__device__ bool clear_rows(char* stage, int copies, int left, uint64_t* landed, uint32_t parity, Control& sh)
+// has landed, the rows of the next expert, or of none, become zeros, as the
+// products read them.
+__device__ void clear_ends(const Sizes& z, char* stages, Control& sh)
 {
-  const int lane = threadIdx.x & 31;
-  if (!__all_sync(kAll, wait(landed, parity, sh)))
-    return false;
-  for (int i = 0; i < copies; ++i)
-    for (int at = left * 128 + lane * 16; at < kDepth * 128; at += 512)
-      *reinterpret_cast<uint4*>(stage + i * kDepth * 128 + at) = uint4{};
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  __syncwarp();
-  return true;
+  const int lane = threadIdx.x & 31, tiles = sh.tile_start[z.experts];
+  Ring<stages_of(kWeights)> s;
+  uint32_t before = 0; // a bit for each stage: the parity of its last blocks of rows
+  for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2) {
+    const Tile tile = tile_at<kWeights>(t, z, sh);
+    const int copies = 2 + pieces(pieces(tile.width, kStepQ) * kStepQ / 2, 64), left = tile.rows % kDepth;
+    for (int b = 0; b < tile.blocks; ++b) {
+      if (left != 0 && b == tile.blocks - 1) {
+        if (!__all_sync(kAll, wait(&sh.end_full[s.at], before >> s.at & 1, sh)))
+          return;
+        before ^= 1u << s.at;
+        for (int i = 0; i < copies; ++i)
+          for (int at = left * 128 + lane * 16; at < kDepth * 128; at += 512)
+            *reinterpret_cast<uint4*>(stages + s.at * stage_bytes(kWeights) + i * kDepth * 128 + at) = uint4{};
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0)
+          release(at_first<kWeights>(&sh.end_ready[s.at]));
+      }
+      s.next();
+    }
+  }
 }
 
-// One warp: the products of the blocks that have landed; the first block
-// issues a pair's.
+// One thread, of a pair's first block: the products of the blocks that have
+// landed. It alone, since the tensor cores are as fast as it can issue: with a
+// warp that agrees on every wait it took 730 cycles for a block of 512.
 template <Kind K>
 __device__ void issue_products(const Sizes& z, char* stages, Control& sh)
 {
-  const int lane = threadIdx.x & 31, tiles = sh.tile_start[z.experts], me = rank<K>();
+  const int tiles = sh.tile_start[z.experts];
   const uint32_t tmem = sh.tmem;
+  const uint64_t p0 = operand<p_by_rows(K)>(smem_addr(stages)), q0 = operand<q_by_rows(K)>(smem_addr(stages) + kBytesP);
   Ring<stages_of(K)> s;
   Ring<2> d;
-  uint32_t ends_before = 0; // kWeights: a bit for each stage, the parity of its last blocks of rows
+  uint32_t ends_before = 0;
   bool ok = true;
   for (int t = blockIdx.x / blocks_of(K); ok && t < tiles; t += gridDim.x / blocks_of(K)) {
     const Tile tile = tile_at<K>(t, z, sh);
-    const int width = pieces(tile.width, kStepQ) * kStepQ;
-    const uint32_t instruction = z.instruction | (uint32_t)(width / 8) << 17;
+    const uint32_t instruction = z.instruction | (uint32_t)(pieces(tile.width, kStepQ) * kStepQ / 8) << 17;
     for (int b = 0; b < tile.blocks; ++b) {
       // the sums of one block, or of all
       const bool first = eight(K) || b == 0, last = eight(K) || b == tile.blocks - 1;
-      char* const from = stages + s.at * stage_bytes(K);
-      const int left = tile.rows - b * kDepth;
-      const bool ends = K == kWeights && left < kDepth;
-      if (me == 0) {
-        ok = (!first || wait(&sh.sums_empty[d.at], d.parity ^ 1, sh)) && wait(&sh.full[s.at], s.parity, sh);
-        ok = __all_sync(kAll, ok);
-      }
-      if (ok && ends) {
-        const uint32_t parity = ends_before >> s.at & 1;
+      ok = (!first || wait(&sh.sums_empty[d.at], d.parity ^ 1, sh)) && wait(&sh.full[s.at], s.parity, sh);
+      if (K == kWeights && ok && last && tile.rows % kDepth != 0) {
+        ok = wait(&sh.end_ready[s.at], ends_before >> s.at & 1, sh);
         ends_before ^= 1u << s.at;
-        ok = clear_rows(from, 2 + pieces(width / 2, 64), left, &sh.end_full[s.at], parity, sh);
-        if (ok && me == 0)
-          ok = __all_sync(kAll, wait(&sh.end_ready[s.at], parity, sh));
-        else if (ok && lane == 0)
-          release(at_first<K>(&sh.end_ready[s.at]));
       }
       if (!ok)
         break;
-      if (me == 0) {
-        fence_after_sync();
-        if (lane == 0) {
-          const uint64_t p = operand<p_by_rows(K)>(smem_addr(from)), q = operand<q_by_rows(K)>(smem_addr(from) + kBytesP);
-          // four products: 32 bytes of c on, or 16 rows of 128 bytes
+      fence_after_sync();
+      const uint64_t p = p0 + s.at * (stage_bytes(K) / 16), q = q0 + s.at * (stage_bytes(K) / 16);
+      // four products: 32 bytes of c on, or 16 rows of 128 bytes
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            multiply<K>(tmem + d.at * kTileQ, p + i * (p_by_rows(K) ? 2 : 128), q + i * (q_by_rows(K) ? 2 : 128),
-                        instruction, !first || i > 0);
-          commit<pair(K)>(&sh.empty[s.at]);
-          if (last)
-            commit<pair(K)>(&sh.sums_full[d.at]);
-        }
-        __syncwarp();
-      }
+      for (int i = 0; i < 4; ++i)
+        multiply<K>(tmem + d.at * kTileQ, p + i * (p_by_rows(K) ? 2 : 128), q + i * (q_by_rows(K) ? 2 : 128),
+                    instruction, !first || i > 0);
+      commit<pair(K)>(&sh.empty[s.at]);
+      if (last)
+        commit<pair(K)>(&sh.sums_full[d.at]);
       s.next();
       if (last)
         d.next();
     }
   }
-  if (!ok && me == 0 && lane == 0) {
+  if (!ok) {
     commit<pair(K)>(&sh.drained); // what is under way ends before the blocks do
     mbar_wait(&sh.drained, 0);
   }
-  __syncwarp();
 }
 
 // kSumWarps warps, 8-bit operands: each block's sums times their scales. A
@@ -648,7 +646,7 @@ product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant_
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
       mbar_init(&sh.end_full[i], 1);
-      mbar_init(&sh.end_ready[i], 1);
+      mbar_init(&sh.end_ready[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.sums_full[i], 1);
@@ -685,7 +683,10 @@ product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant_
       if (lane == 0)
         copy_operands<K>(p_map, q_map, z, stages, sh);
     } else if (warp == 1) {
-      issue_products<K>(z, stages, sh);
+      if (lane == 0 && rank<K>() == 0)
+        issue_products<K>(z, stages, sh);
+    } else if (K == kWeights && warp == 2) {
+      clear_ends(z, stages, sh);
     }
   } else {
     if constexpr (eight(K)) {
