@@ -41,7 +41,7 @@ constexpr int kTileQ = 256;      // half of its columns
 constexpr int kOperandBytes = 192 << 10;
 constexpr int kMaxStages = 6;
 constexpr int kBytesP = kTileP * 128;
-constexpr int kBox = 32;         // rows of one copy of an expert's rows
+constexpr int kBox = 32;         // rows of one copy of few of an expert's rows
 constexpr int kDepth = 64;       // rows of one copy where c runs over rows
 constexpr int kStepQ = 32;       // 16 for each block of a pair
 constexpr int kMaxExperts = SEGTOPK_MAX_EXPERTS;
@@ -228,6 +228,20 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Control& sh
   return true;
 }
 
+// Whether that phase is over already; does not wait. Asked a step ahead, so
+// that the answer is there when the step comes: a wait alone takes a hundred
+// cycles or two even where there is nothing to wait for.
+__device__ __forceinline__ bool over(uint64_t* bar, uint32_t parity)
+{
+  uint32_t ok;
+  asm volatile(
+    "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+    : "=r"(ok)
+    : "r"(smem_addr(bar)), "r"(parity)
+    : "memory");
+  return ok != 0;
+}
+
 // A place in a ring of N and the parity of the passes over it.
 template <int N>
 struct Ring {
@@ -366,69 +380,73 @@ __device__ void find_tiles(const int64_t* offsets, const Sizes& z, Control& sh)
 // ---------------------------------------------------------------------------
 // Kernel
 // ---------------------------------------------------------------------------
-// One thread: copies of this block's operands, as stages get free. A pair's
-// count at the first block, which expects those of both.
+// One thread each for p and q: copies of this block's operands, as stages get
+// free. A pair's count at the first block, whose thread for p expects those of
+// both; they may land before it says so, since the phase waits for that too.
+// An expert's rows come in boxes of kTileP, or of kBox where that is less; all
+// boxes are copied whole, whatever of them there is.
+__device__ __forceinline__ int boxed(int rows) { return rows > kTileP / 2 ? kTileP : pieces(max(rows, 0), kBox) * kBox; }
+
 template <Kind K>
-__device__ void copy_operands(const CUtensorMap& p_map, const CUtensorMap& q_map, const Sizes& z, char* stages, Control& sh)
+__device__ void copy_operands(bool is_p, const CUtensorMap& map, const CUtensorMap& large, const Sizes& z, char* stages,
+                              Control& sh)
 {
   constexpr int kStages = stages_of(K);
   const int tiles = sh.tile_start[z.experts], me = rank<K>();
   Ring<kStages> s;
   int used = 0; // stages whose copies are under way or have landed
-  bool ok = true;
+  bool ok = true, ready = false;
   for (int t = blockIdx.x / blocks_of(K); ok && t < tiles; t += gridDim.x / blocks_of(K)) {
     const Tile tile = tile_at<K>(t, z, sh);
     const int width = pieces(tile.width, kStepQ) * kStepQ / blocks_of(K); // of q in this block
-    const int first_p = tile.p + me * kTileP, first_q = tile.q + me * width;
-    // boxes are copied whole, whatever of them there is
-    auto boxes_p = [&](int p) { return pieces(max(0, min(kTileP, tile.rows - p)), kBox); }; // 8 bits: rows
-    const int boxes_q = pieces(width, eight(K) ? kTileP : q_by_rows(K) ? kBox : 64);
-    int bytes = boxes_q * (eight(K) ? kTileP : q_by_rows(K) ? kBox : 64) * 128;
-    if constexpr (eight(K))
-      bytes += boxes_p(first_p) * kBox * 128;
-    else
-      bytes += kBytesP;
-    const int bytes_other = !pair(K) ? 0 : eight(K) ? bytes + (boxes_p(tile.p + kTileP) - boxes_p(tile.p)) * kBox * 128 : bytes;
+    const int first = is_p ? tile.p + me * kTileP : tile.q + me * width;
+    // rows of 128 bytes that land
+    int lines_p = kTileP, lines_q;
+    if constexpr (eight(K)) {
+      lines_p = boxed(tile.rows - tile.p - me * kTileP);
+      lines_q = pieces(width, kTileP) * kTileP;
+    } else {
+      lines_q = K == kWeights ? pieces(width, 64) * 64 : boxed(width);
+    }
+    int expected = lines_p + lines_q;
+    if constexpr (pair(K))
+      expected += eight(K) ? boxed(tile.rows - tile.p - kTileP) + lines_q : expected;
+    const int lines = is_p ? lines_p : lines_q;
+    const bool by_rows = is_p == eight(K) && K != kWeights; // these are the expert's rows
+    const CUtensorMap& from = by_rows && lines == kTileP ? large : map;
+    const int box = K == kWeights || (is_p && K == kForwardTurned) ? 64 : by_rows && lines < kTileP ? kBox : kTileP;
     for (int b = 0; b < tile.blocks; ++b) {
-      ok = wait(&sh.empty[s.at], s.parity ^ 1, sh);
+      if (!ready)
+        ok = wait(&sh.empty[s.at], s.parity ^ 1, sh);
       if (!ok)
         break;
-      char *const to_p = stages + s.at * stage_bytes(K), *const to_q = to_p + kBytesP;
+      char* const to = stages + s.at * stage_bytes(K) + (is_p ? 0 : kBytesP);
       uint32_t bar = at_first<K>(&sh.full[s.at]);
       if (K == kWeights && (b + 1) * kDepth > tile.rows) {
         // an expert's last rows: each block of the pair first takes out those of others
-        if (me == 0)
+        if (is_p && me == 0)
           arrive(bar);
         bar = smem_addr(&sh.end_full[s.at]);
-        mbar_arrive_expect_tx(&sh.end_full[s.at], bytes);
-      } else if (me == 0) {
-        mbar_arrive_expect_tx(&sh.full[s.at], bytes + bytes_other);
-      }
-      if constexpr (eight(K)) {
-        for (int i = 0, n = boxes_p(first_p); i < n; ++i)
-          tile_load<pair(K)>(to_p + i * kBox * 128, &p_map, b * 128, tile.row + first_p + i * kBox, 0, bar);
-        for (int i = 0; i < boxes_q; ++i)
-          tile_load<pair(K)>(to_q + i * kTileP * 128, &q_map, b * 128, first_q + i * kTileP, tile.expert, bar);
-      } else if constexpr (K == kWeights) {
-        const int y = tile.row + b * kDepth;
-        for (int i = 0; i < 2; ++i)
-          tile_load<true>(to_p + i * kDepth * 128, &p_map, first_p + i * 64, y, 0, bar);
-        for (int i = 0; i < boxes_q; ++i)
-          tile_load<true>(to_q + i * kDepth * 128, &q_map, first_q + i * 64, y, 0, bar);
-      } else {
-        if constexpr (K == kForward)
-          tile_load<true>(to_p, &p_map, b * 64, first_p, tile.expert, bar);
-        else
-          for (int i = 0; i < 2; ++i)
-            tile_load<true>(to_p + i * kDepth * 128, &p_map, first_p + i * 64, b * kDepth, tile.expert, bar);
-        for (int i = 0; i < boxes_q; ++i)
-          tile_load<true>(to_q + i * kBox * 128, &q_map, b * 64, tile.row + first_q + i * kBox, 0, bar);
+        if (is_p)
+          mbar_arrive_expect_tx(&sh.end_full[s.at], (lines_p + lines_q) * 128);
+      } else if (is_p && me == 0) {
+        mbar_arrive_expect_tx(&sh.full[s.at], expected * 128);
       }
       used = min(used + 1, kStages);
       s.next();
+      ready = over(&sh.empty[s.at], s.parity ^ 1);
+      for (int i = 0; i < lines; i += box) {
+        if constexpr (K == kWeights)
+          tile_load<true>(to + i * 128, &from, first + i, tile.row + b * kDepth, 0, bar);
+        else if (K == kForwardTurned && is_p)
+          tile_load<true>(to + i * 128, &from, first + i, b * kDepth, tile.expert, bar);
+        else
+          tile_load<pair(K)>(to + i * 128, &from, b * (eight(K) ? 128 : 64), (by_rows ? tile.row : 0) + first + i,
+                             by_rows ? 0 : tile.expert, bar);
+      }
     }
   }
-  if (!ok && me == 0) {
+  if (!ok && is_p && me == 0) {
     // what is under way lands before the blocks end (a second each at most)
     for (int i = 0; i < used; ++i) {
       s.at = s.at == 0 ? kStages - 1 : s.at - 1;
@@ -479,14 +497,15 @@ __device__ void issue_products(const Sizes& z, char* stages, Control& sh)
   Ring<stages_of(K)> s;
   Ring<2> d;
   uint32_t ends_before = 0;
-  bool ok = true;
+  bool ok = true, ready = false, sums_ready = false;
   for (int t = blockIdx.x / blocks_of(K); ok && t < tiles; t += gridDim.x / blocks_of(K)) {
     const Tile tile = tile_at<K>(t, z, sh);
     const uint32_t instruction = z.instruction | (uint32_t)(pieces(tile.width, kStepQ) * kStepQ / 8) << 17;
     for (int b = 0; b < tile.blocks; ++b) {
       // the sums of one block, or of all
       const bool first = eight(K) || b == 0, last = eight(K) || b == tile.blocks - 1;
-      ok = (!first || wait(&sh.sums_empty[d.at], d.parity ^ 1, sh)) && wait(&sh.full[s.at], s.parity, sh);
+      ok = (!first || sums_ready || wait(&sh.sums_empty[d.at], d.parity ^ 1, sh)) &&
+           (ready || wait(&sh.full[s.at], s.parity, sh));
       if (K == kWeights && ok && last && tile.rows % kDepth != 0) {
         ok = wait(&sh.end_ready[s.at], ends_before >> s.at & 1, sh);
         ends_before ^= 1u << s.at;
@@ -495,17 +514,22 @@ __device__ void issue_products(const Sizes& z, char* stages, Control& sh)
         break;
       fence_after_sync();
       const uint64_t p = p0 + s.at * (stage_bytes(K) / 16), q = q0 + s.at * (stage_bytes(K) / 16);
+      const uint32_t sums = tmem + d.at * kTileQ;
+      uint64_t *const empty = &sh.empty[s.at], *const sums_full = &sh.sums_full[d.at];
+      s.next();
+      ready = over(&sh.full[s.at], s.parity);
+      if (last) {
+        d.next();
+        sums_ready = over(&sh.sums_empty[d.at], d.parity ^ 1);
+      }
       // four products: 32 bytes of c on, or 16 rows of 128 bytes
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        multiply<K>(tmem + d.at * kTileQ, p + i * (p_by_rows(K) ? 2 : 128), q + i * (q_by_rows(K) ? 2 : 128),
+        multiply<K>(sums, p + i * (p_by_rows(K) ? 2 : 128), q + i * (q_by_rows(K) ? 2 : 128),
                     instruction, !first || i > 0);
-      commit<pair(K)>(&sh.empty[s.at]);
+      commit<pair(K)>(empty);
       if (last)
-        commit<pair(K)>(&sh.sums_full[d.at]);
-      s.next();
-      if (last)
-        d.next();
+        commit<pair(K)>(sums_full);
     }
   }
   if (!ok) {
@@ -634,7 +658,7 @@ __device__ void write_sums(const Sizes& z, O* out, Control& sh)
 template <Kind K, class O>
 __global__ void __cluster_dims__(blocks_of(K), 1, 1) __launch_bounds__(kThreads, 1)
 product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
-               const int64_t* offsets, const __grid_constant__ Sizes z, O* out)
+               const __grid_constant__ CUtensorMap large, const int64_t* offsets, const __grid_constant__ Sizes z, O* out)
 {
   extern __shared__ char dynamic[];
   char* const stages = dynamic + (-smem_addr(dynamic) & 1023);
@@ -679,9 +703,9 @@ product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant_
   if (warp < kThreads / 32 - kSumWarps) {
     if constexpr (eight(K))
       asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 0) {
+    if (warp == 0 || warp == 3) {
       if (lane == 0)
-        copy_operands<K>(p_map, q_map, z, stages, sh);
+        copy_operands<K>(warp == 0, warp == 0 ? p_map : q_map, large, z, stages, sh);
     } else if (warp == 1) {
       if (lane == 0 && rank<K>() == 0)
         issue_products<K>(z, stages, sh);
@@ -771,14 +795,14 @@ cudaError_t allow_shared()
 }
 
 template <Kind K, class O>
-int run(const CUtensorMap& p, const CUtensorMap& q, const int64_t* offsets, const Sizes& z, void* out, int sms,
+int run(const CUtensorMap& p, const CUtensorMap& q, const CUtensorMap& large, const int64_t* offsets, const Sizes& z, void* out, int sms,
         int64_t most_tiles, void* stream)
 {
   const cudaError_t e = allow_shared<K, O>();
   if (e != cudaSuccess)
     return record_cuda_error(e);
   const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(sms / blocks_of(K), most_tiles)) * blocks_of(K);
-  return finish(launch(product_kernel<K, O>, dim3(grid), kThreads, kShared, (cudaStream_t)stream, p, q, offsets, z, (O*)out), 1);
+  return finish(launch(product_kernel<K, O>, dim3(grid), kThreads, kShared, (cudaStream_t)stream, p, q, large, offsets, z, (O*)out), 1);
 }
 
 bool float_type_of(int dtype) { return dtype == SEGTOPK_F16 || dtype == SEGTOPK_BF16 || dtype == SEGTOPK_F32; }
@@ -857,11 +881,13 @@ extern "C" int segtopk_expert_matmul(segtopk_dtype dtype, const void* rows, int6
   int sms;
   if ((rc = check_device(&sms)) != SEGTOPK_SUCCESS)
     return rc;
-  CUtensorMap p, q;
+  CUtensorMap p, q, large = {};
   cudaError_t e = turned ? describe(&p, map_type(dtype), 2, weights, out_width, width, experts, line, expert_stride, kDepth)
                          : describe(&p, map_type(dtype), 2, weights, width, out_width, experts, line, expert_stride, kTileP);
   if (e == cudaSuccess)
     e = describe(&q, map_type(dtype), 2, rows, width, num_rows, 1, row_stride, num_rows * row_stride, kBox);
+  if (e == cudaSuccess)
+    e = describe(&large, map_type(dtype), 2, rows, width, num_rows, 1, row_stride, num_rows * row_stride, kTileP);
   if (e != cudaSuccess)
     return record_cuda_error(e);
   Sizes z = {};
@@ -874,8 +900,8 @@ extern "C" int segtopk_expert_matmul(segtopk_dtype dtype, const void* rows, int6
   const int64_t tiles = forward_tiles(num_rows, kTileQ, out_width, kTileP, experts);
   return with_float_type(out_dtype, [&](auto zero) {
     using O = decltype(zero);
-    return turned ? run<kForwardTurned, O>(p, q, offsets, z, out, sms, tiles, stream)
-                  : run<kForward, O>(p, q, offsets, z, out, sms, tiles, stream);
+    return turned ? run<kForwardTurned, O>(p, q, large, offsets, z, out, sms, tiles, stream)
+                  : run<kForward, O>(p, q, large, offsets, z, out, sms, tiles, stream);
   });
 }
 
@@ -904,9 +930,12 @@ extern "C" int segtopk_expert_matmul_f8(const void* rows, int64_t num_rows, int6
   int sms;
   if ((rc = check_device(&sms)) != SEGTOPK_SUCCESS)
     return rc;
-  CUtensorMap p, q;
+  CUtensorMap p, q, large = {};
   cudaError_t e = describe(&p, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, width, num_rows, 1, row_stride,
                            num_rows * row_stride, kBox);
+  if (e == cudaSuccess)
+    e = describe(&large, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, width, num_rows, 1, row_stride, num_rows * row_stride,
+                 kTileP);
   if (e == cudaSuccess)
     e = describe(&q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, weights, width, out_width, experts, out_stride, expert_stride,
                  kTileP);
@@ -931,8 +960,8 @@ extern "C" int segtopk_expert_matmul_f8(const void* rows, int64_t num_rows, int6
   return with_float_type(out_dtype, [&](auto zero) {
     using O = decltype(zero);
     z.out_vectors = rows_fit(out, out_width, out_width, sizeof(O), 16 / (int)sizeof(O));
-    return by_pairs ? run<kForward8Pair, O>(p, q, offsets, z, out, sms, tiles, stream)
-                    : run<kForward8, O>(p, q, offsets, z, out, sms, tiles, stream);
+    return by_pairs ? run<kForward8Pair, O>(p, q, large, offsets, z, out, sms, tiles, stream)
+                    : run<kForward8, O>(p, q, large, offsets, z, out, sms, tiles, stream);
   });
 }
 
@@ -963,7 +992,7 @@ extern "C" int segtopk_expert_matmul_weights(segtopk_dtype dtype, const void* a_
     const cudaError_t e = cudaMemsetAsync(out, 0, bytes, (cudaStream_t)stream);
     return e == cudaSuccess ? SEGTOPK_SUCCESS : record_cuda_error(e);
   }
-  CUtensorMap p, q;
+  CUtensorMap p, q, large = {};
   cudaError_t e = describe(&p, map_type(dtype), 2, b_rows, b_width, num_rows, 1, b_stride, num_rows * b_stride, kDepth);
   if (e == cudaSuccess)
     e = describe(&q, map_type(dtype), 2, a_rows, a_width, num_rows, 1, a_stride, num_rows * a_stride, kDepth);
@@ -977,6 +1006,6 @@ extern "C" int segtopk_expert_matmul_weights(segtopk_dtype dtype, const void* a_
   z.instruction = instruction(kWeights, dtype == SEGTOPK_BF16);
   z.out_stride = b_width;
   return with_float_type(out_dtype, [&](auto zero) {
-    return run<kWeights, decltype(zero)>(p, q, offsets, z, out, sms, tiles, stream);
+    return run<kWeights, decltype(zero)>(p, q, large, offsets, z, out, sms, tiles, stream);
   });
 }
