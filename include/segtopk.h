@@ -451,6 +451,26 @@ SEGTOPK_API int segtopk_route(segtopk_dtype dtype, const void* logits, int64_t t
                               const float* bias, int32_t* expert_ids, float* weights, void* stream);
 
 /*
+ * The same choice limited to groups of experts: the experts are num_groups
+ * groups of equal size, in order; the groups_kept best groups are taken, and
+ * in them the k best experts. A group's score is its best expert's
+ * (SEGTOPK_GROUP_BEST), or the sum of its two best ones' score + bias
+ * (SEGTOPK_GROUP_BEST_TWO; an expert that is never chosen adds nothing). Ties
+ * go to the lower group. Weights, the softmax's sum among them, are over all
+ * experts as above, and so is the gradient (segtopk_route_backward). With
+ * SEGTOPK_GROUP_BEST and no bias the logits are compared, else scores of 32
+ * bits. 1 <= groups_kept <= num_groups <= SEGTOPK_MAX_GROUPS, experts a
+ * multiple of num_groups, k at most the experts of groups_kept groups.
+ */
+#define SEGTOPK_MAX_GROUPS 32
+typedef enum { SEGTOPK_GROUP_BEST = 0, SEGTOPK_GROUP_BEST_TWO = 1 } segtopk_group_score;
+SEGTOPK_API int segtopk_route_groups(segtopk_dtype dtype, const void* logits, int64_t tokens, int32_t experts,
+                                     int64_t row_stride, int32_t k, int32_t num_groups, int32_t groups_kept,
+                                     segtopk_group_score group_score, segtopk_score score, int renormalize,
+                                     float scale, const float* bias, int32_t* expert_ids, float* weights,
+                                     void* stream);
+
+/*
  * Gradient of the logits from that of the weights (tokens x k): dense,
  * tokens x experts of `dtype`. expert_ids are the ones segtopk_route chose
  * (distinct per token; those outside 0 .. experts - 1 contribute nothing, as
@@ -600,6 +620,53 @@ SEGTOPK_API int segtopk_expert_matmul_weights(segtopk_dtype dtype, const void* a
                                               int64_t b_stride, int64_t num_rows, int32_t experts,
                                               const int64_t* offsets, segtopk_dtype out_dtype, void* out,
                                               void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Layer norm, and rows in 8 bits
+ * ---------------------------------------------------------------------------
+ * Rows, strides, pointers and errors as for the row operators above.
+ */
+
+/* Widest row of segtopk_layer_norm. */
+#define SEGTOPK_MAX_NORM_WIDTH 16384
+
+/*
+ * out[t] = (x[t] - mean[t]) * rstd[t] * weight + bias, with the mean of the
+ * row's `width` values and rstd = 1 / sqrt(the mean of (x[t] - mean[t])^2 +
+ * eps), both of which are written too (num_rows floats each). weight and bias
+ * (NULL: none) hold `width` values of weight_dtype: dtype or F32. eps >= 0.
+ */
+SEGTOPK_API int segtopk_layer_norm(segtopk_dtype dtype, const void* x, int64_t num_rows, int64_t width,
+                                   int64_t row_stride, segtopk_dtype weight_dtype, const void* weight,
+                                   const void* bias, float eps, void* out, float* mean, float* rstd, void* stream);
+
+/*
+ * Its gradients, from that of out: of x (num_rows dense rows), of weight and
+ * of bias (of weight_dtype; sums over the rows in an order that depends on the
+ * sizes alone; zeros where there are no rows). mean and rstd are what the
+ * forward call wrote. workspace: at least
+ * segtopk_layer_norm_backward_workspace_bytes(...) bytes, 4-byte aligned
+ * (host-only arithmetic; 0 for no rows and for sizes out of range).
+ */
+SEGTOPK_API size_t segtopk_layer_norm_backward_workspace_bytes(int64_t num_rows, int64_t width);
+SEGTOPK_API int segtopk_layer_norm_backward(segtopk_dtype dtype, const void* grad_out, int64_t grad_stride,
+                                            const void* x, int64_t num_rows, int64_t width, int64_t row_stride,
+                                            segtopk_dtype weight_dtype, const void* weight, const float* mean,
+                                            const float* rstd, void* grad_x, void* grad_weight, void* grad_bias,
+                                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rows in 8 bits (e4m3) with a float scale for each block of 128 values, the
+ * last block of a row in part: with a = max(the block's largest magnitude,
+ * 2^-100),
+ *   values[t, i] = e4m3(x[t, i] * (448 / a)),  scales[t, b] = a / 448,
+ * rounded to nearest, ties to even; 448 is the largest e4m3 number. A block
+ * with a NaN has a scale of NaN, one with an infinity a scale of infinity, and
+ * NaN where those were. values: num_rows x width bytes; scales: num_rows x
+ * ceil(width / 128). width <= 2^20, fewer than 2^31 blocks.
+ */
+SEGTOPK_API int segtopk_quantize_rows(segtopk_dtype dtype, const void* x, int64_t num_rows, int64_t width,
+                                      int64_t row_stride, void* values, float* scales, void* stream);
 
 #ifdef __cplusplus
 }

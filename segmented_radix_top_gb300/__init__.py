@@ -11,9 +11,10 @@ from ._binding import (DETERMINISM, DIRECTION, DTYPE, KEY_BYTES, MAX_K, NOALLOC_
                        batched_topk_host_noalloc, host_workspace_bytes,
                        last_launch_count, library_path, load, load_instrumented, read_device_error,
                        read_stats, set_test_hooks, topk)
-from ._rows import (DEVICE_ERROR_INDEX, MAX_EXPERTS, ROUTE_MAX_K, ExpertGroups, combine,  # noqa: F401
-                    combine_backward, dispatch, dispatch_backward, embedding, embedding_backward,
-                    expert_matmul, expert_matmul_backward, group_by_expert, route, route_backward)
+from ._rows import (DEVICE_ERROR_INDEX, MAX_EXPERTS, MAX_GROUPS, MAX_NORM_WIDTH, ROUTE_MAX_K,  # noqa: F401
+                    ExpertGroups, combine, combine_backward, dispatch, dispatch_backward, embedding,
+                    embedding_backward, expert_matmul, expert_matmul_backward, group_by_expert, layer_norm,
+                    layer_norm_backward, quantize_rows, route, route_backward)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

@@ -34,6 +34,8 @@ from . import _build
 
 MAX_EXPERTS = 1024    # SEGTOPK_MAX_EXPERTS
 ROUTE_MAX_K = 32      # SEGTOPK_ROUTE_MAX_K
+MAX_GROUPS = 32       # SEGTOPK_MAX_GROUPS
+MAX_NORM_WIDTH = 16384  # SEGTOPK_MAX_NORM_WIDTH
 DEVICE_ERROR_INDEX = 4  # SEGTOPK_DEVICE_ERROR_INDEX
 
 
@@ -50,6 +52,7 @@ def _entries():
                               ctypes.c_size_t)
     return {
         "segtopk_route": (i, [i, vp, i64, i32, i64, i32, i, i, f, vp, vp, vp, vp]),
+        "segtopk_route_groups": (i, [i, vp, i64, i32, i64, i32, i32, i32, i, i, i, f, vp, vp, vp, vp]),
         "segtopk_route_backward": (i, [i, vp, vp, i64, i32, i64, i32, vp, i, i, f, vp, vp]),
         "segtopk_group_workspace_bytes": (sz, [i64, i32]),
         "segtopk_group": (i, [vp, i32, i64, i32, vp, vp, vp, vp, sz, vp]),
@@ -62,6 +65,10 @@ def _entries():
         "segtopk_expert_matmul": (i, [i, vp, i64, i64, i64, vp, i32, i64, i64, i64, i64, vp, i, vp, vp]),
         "segtopk_expert_matmul_f8": (i, [vp, i64, i64, i64, vp, i64, vp, i32, i64, i64, i64, vp, vp, i, vp, vp]),
         "segtopk_expert_matmul_weights": (i, [i, vp, i64, i64, vp, i64, i64, i64, i32, vp, i, vp, vp]),
+        "segtopk_layer_norm": (i, [i, vp, i64, i64, i64, i, vp, vp, f, vp, vp, vp, vp]),
+        "segtopk_layer_norm_backward_workspace_bytes": (sz, [i64, i64]),
+        "segtopk_layer_norm_backward": (i, [i, vp, i64, vp, i64, i64, i64, i, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "segtopk_quantize_rows": (i, [i, vp, i64, i64, i64, vp, vp, vp]),
     }
 
 
@@ -116,7 +123,7 @@ def _on_stream(call):
 
 @_on_stream
 def route(logits: torch.Tensor, k: int, *, score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
-          bias=None):
+          bias=None, num_groups: int = 1, groups_kept=None, group_score: str = "best"):
     """The k best experts of each token and their weights (segtopk_route).
 
     logits: [tokens, experts]. score: "softmax" (over all experts) or
@@ -124,8 +131,14 @@ def route(logits: torch.Tensor, k: int, *, score: str = "softmax", renormalize: 
     multiplies. bias: optional float32 [experts], added to the scores for the
     choice only. Experts with a logit or a bias of -inf are never chosen. Returns
     (expert_ids int32 [tokens, k], best first and -1 where none is left,
-    weights float32 [tokens, k])."""
-    return (_native or _load()).route(logits, k, score, renormalize, scale, bias)
+    weights float32 [tokens, k]).
+
+    With num_groups the experts are as many groups of equal size, in order, and
+    the k are chosen from the groups_kept best groups (all unless given;
+    segtopk_route_groups): by group_score "best", a group's best expert, or
+    "best_two", the sum of its two best ones' scores with their biases.
+    route_backward() is the same for both."""
+    return (_native or _load()).route(logits, k, score, renormalize, scale, bias, num_groups, groups_kept, group_score)
 
 
 @_on_stream
@@ -235,3 +248,32 @@ def expert_matmul_backward(grad_out: torch.Tensor, rows: torch.Tensor, weights: 
     given) in the weights' layout, zeros for an expert without rows). width
     and out are multiples of 8."""
     return (_native or _load()).expert_matmul_backward(grad_out, rows, weights, groups, dtype)
+
+
+@_on_stream
+def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias=None, *, eps: float = 1e-5, out=None):
+    """Layer norm of the rows of x [tokens, width] (segtopk_layer_norm):
+    (x - mean) * rstd * weight + bias. weight, and bias where there is one:
+    [width], both of x's type or both float32. Returns (out of x's type, mean
+    and rstd float32 [tokens], for layer_norm_backward). width is at most
+    MAX_NORM_WIDTH."""
+    return (_native or _load()).layer_norm(x, weight, bias, eps, out)
+
+
+@_on_stream
+def layer_norm_backward(grad_out: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor,
+                        rstd: torch.Tensor):
+    """Gradients of layer_norm()'s x, weight and bias
+    (segtopk_layer_norm_backward), the last two of weight's type: (grad_x,
+    grad_weight, grad_bias). mean and rstd are those that layer_norm()
+    returned."""
+    return (_native or _load()).layer_norm_backward(grad_out, x, weight, mean, rstd)
+
+
+@_on_stream
+def quantize_rows(x: torch.Tensor):
+    """The rows of x [tokens, width] in 8 bits with a scale for each block of
+    128 values (segtopk_quantize_rows): (values float8_e4m3fn [tokens, width],
+    scales float32 [tokens, blocks]), x being nearly values * scales. Both can
+    go through dispatch() to expert_matmul()."""
+    return (_native or _load()).quantize_rows(x)

@@ -29,6 +29,7 @@ namespace {
 
 #define SEGTOPK_ENTRIES(X)                                                                                       \
   X(segtopk_route)                                                                                               \
+  X(segtopk_route_groups)                                                                                        \
   X(segtopk_route_backward)                                                                                      \
   X(segtopk_group)                                                                                               \
   X(segtopk_group_workspace_bytes)                                                                               \
@@ -40,7 +41,11 @@ namespace {
   X(segtopk_embedding_backward_workspace_bytes)                                                                  \
   X(segtopk_expert_matmul)                                                                                       \
   X(segtopk_expert_matmul_f8)                                                                                    \
-  X(segtopk_expert_matmul_weights)
+  X(segtopk_expert_matmul_weights)                                                                               \
+  X(segtopk_layer_norm)                                                                                          \
+  X(segtopk_layer_norm_backward)                                                                                 \
+  X(segtopk_layer_norm_backward_workspace_bytes)                                                                 \
+  X(segtopk_quantize_rows)
 
 struct Library {
 #define X(NAME) decltype(&::NAME) NAME = nullptr;
@@ -94,6 +99,16 @@ segtopk_score score_of(PyObject* o)
       return SEGTOPK_SIGMOID;
   }
   TORCH_CHECK_VALUE(false, "score must be one of softmax, sigmoid");
+}
+segtopk_group_score group_score_of(PyObject* o)
+{
+  if (PyUnicode_Check(o)) {
+    if (PyUnicode_CompareWithASCIIString(o, "best") == 0)
+      return SEGTOPK_GROUP_BEST;
+    if (PyUnicode_CompareWithASCIIString(o, "best_two") == 0)
+      return SEGTOPK_GROUP_BEST_TWO;
+  }
+  TORCH_CHECK_VALUE(false, "group_score must be one of best, best_two");
 }
 at::ScalarType dtype_of(PyObject* o)
 {
@@ -233,7 +248,7 @@ PyObject* tuple(T&&... t)
 PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
   HANDLE_TH_ERRORS
-  want_args(n, 6); // logits, k, score, renormalize, scale, bias
+  want_args(n, 9); // logits, k, score, renormalize, scale, bias, num_groups, groups_kept, group_score
   const at::Tensor logits = matrix(tensor(a[0], "logits"), "logits");
   const segtopk_dtype type = float_type(logits.scalar_type(), "logits");
   const int32_t k = integer32(a[1], "k");
@@ -250,9 +265,18 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n)
   }
   const int64_t shape[2] = {tokens, std::max(k, 0)};
   at::Tensor ids = place.empty(shape, at::kInt), weights = place.empty(shape, at::kFloat);
-  check(lib.segtopk_route(type, logits.const_data_ptr(), tokens, (int32_t)experts, logits.stride(0), k, score,
-                          renormalize, scale, bias.defined() ? bias.const_data_ptr<float>() : nullptr,
-                          ids.mutable_data_ptr<int32_t>(), weights.mutable_data_ptr<float>(), place.stream()));
+  const int32_t groups = integer32(a[6], "num_groups");
+  const int32_t kept = a[7] == Py_None ? groups : integer32(a[7], "groups_kept");
+  const segtopk_group_score group_score = group_score_of(a[8]);
+  if (groups != 1 || kept != 1)
+    check(lib.segtopk_route_groups(type, logits.const_data_ptr(), tokens, (int32_t)experts, logits.stride(0), k, groups,
+                                   kept, group_score, score, renormalize, scale,
+                                   bias.defined() ? bias.const_data_ptr<float>() : nullptr,
+                                   ids.mutable_data_ptr<int32_t>(), weights.mutable_data_ptr<float>(), place.stream()));
+  else
+    check(lib.segtopk_route(type, logits.const_data_ptr(), tokens, (int32_t)experts, logits.stride(0), k, score,
+                            renormalize, scale, bias.defined() ? bias.const_data_ptr<float>() : nullptr,
+                            ids.mutable_data_ptr<int32_t>(), weights.mutable_data_ptr<float>(), place.stream()));
   return tuple(std::move(ids), std::move(weights));
   END_HANDLE_TH_ERRORS
 }
@@ -583,6 +607,89 @@ PyObject* expert_matmul_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
   END_HANDLE_TH_ERRORS
 }
 
+// A row of `width` values of x's type or float32: t, or a contiguous copy.
+at::Tensor norm_weight(PyObject* o, const char* name, const at::Tensor& x, const Place& place)
+{
+  const at::Tensor& t = tensor(o, name);
+  TORCH_CHECK_VALUE(t.dim() == 1 && t.size(0) == x.size(1) &&
+                      (t.scalar_type() == x.scalar_type() || t.scalar_type() == at::kFloat),
+                    name, " must be ", x.scalar_type(), " or float32 of [", x.size(1), "]");
+  place.same(t);
+  return values(t).contiguous();
+}
+
+PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+  HANDLE_TH_ERRORS
+  want_args(n, 5); // x, weight, bias or None, eps, out
+  const at::Tensor x = matrix(tensor(a[0], "x"), "x");
+  const segtopk_dtype type = float_type(x.scalar_type(), "x");
+  const Place place(x);
+  const at::Tensor weight = norm_weight(a[1], "weight", x, place);
+  at::Tensor bias;
+  if (a[2] != Py_None) {
+    bias = norm_weight(a[2], "bias", x, place);
+    TORCH_CHECK_VALUE(bias.scalar_type() == weight.scalar_type(), "bias must be ", weight.scalar_type(), ", as weight");
+  }
+  const float eps = real(a[3]);
+  const int64_t rows = x.size(0), width = x.size(1);
+  at::Tensor out = place.result(a[4], "out", {rows, width}, x.scalar_type());
+  at::Tensor mean = place.empty({rows}, at::kFloat), rstd = place.empty({rows}, at::kFloat);
+  check(lib.segtopk_layer_norm(type, x.const_data_ptr(), rows, width, x.stride(0), float_type(weight.scalar_type(), "weight"),
+                               weight.const_data_ptr(), bias.defined() ? bias.const_data_ptr() : nullptr, eps,
+                               out.mutable_data_ptr(), mean.mutable_data_ptr<float>(), rstd.mutable_data_ptr<float>(),
+                               place.stream()));
+  written(a[4], out);
+  return tuple(std::move(out), std::move(mean), std::move(rstd));
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+  HANDLE_TH_ERRORS
+  want_args(n, 5); // grad_out, x, weight, mean, rstd
+  const at::Tensor x = matrix(tensor(a[1], "x"), "x");
+  const segtopk_dtype type = float_type(x.scalar_type(), "x");
+  const at::Tensor grad = matrix(tensor(a[0], "grad_out"), "grad_out");
+  TORCH_CHECK_VALUE(grad.sizes() == x.sizes() && grad.scalar_type() == x.scalar_type(), "grad_out must be ",
+                    x.scalar_type(), " of ", x.sizes());
+  const Place place(x);
+  const at::Tensor weight = norm_weight(a[2], "weight", x, place);
+  const int64_t rows = x.size(0), width = x.size(1);
+  const at::Tensor mean = dense(tensor(a[3], "mean"), "mean", {rows}, at::kFloat);
+  const at::Tensor rstd = dense(tensor(a[4], "rstd"), "rstd", {rows}, at::kFloat);
+  place.same(grad);
+  place.same(mean);
+  place.same(rstd);
+  at::Tensor grad_x = place.empty({rows, width}, x.scalar_type());
+  at::Tensor grad_weight = place.empty({width}, weight.scalar_type()), grad_bias = place.empty({width}, weight.scalar_type());
+  const size_t need = lib.segtopk_layer_norm_backward_workspace_bytes(rows, width);
+  at::Tensor space = place.empty({(int64_t)need}, at::kByte);
+  check(lib.segtopk_layer_norm_backward(type, grad.const_data_ptr(), grad.stride(0), x.const_data_ptr(), rows, width,
+                                        x.stride(0), float_type(weight.scalar_type(), "weight"), weight.const_data_ptr(),
+                                        mean.const_data_ptr<float>(), rstd.const_data_ptr<float>(),
+                                        grad_x.mutable_data_ptr(), grad_weight.mutable_data_ptr(),
+                                        grad_bias.mutable_data_ptr(), space.mutable_data_ptr(), need, place.stream()));
+  return tuple(std::move(grad_x), std::move(grad_weight), std::move(grad_bias));
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+  HANDLE_TH_ERRORS
+  want_args(n, 1); // x
+  const at::Tensor x = matrix(tensor(a[0], "x"), "x");
+  const segtopk_dtype type = float_type(x.scalar_type(), "x");
+  const Place place(x);
+  const int64_t rows = x.size(0), width = x.size(1);
+  at::Tensor out = place.empty({rows, width}, at::kFloat8_e4m3fn);
+  at::Tensor scales = place.empty({rows, (width + 127) / 128}, at::kFloat);
+  check(lib.segtopk_quantize_rows(type, x.const_data_ptr(), rows, width, x.stride(0), out.mutable_data_ptr(),
+                                  scales.mutable_data_ptr<float>(), place.stream()));
+  return tuple(std::move(out), std::move(scales));
+  END_HANDLE_TH_ERRORS
+}
+
 // bind(addresses of the entry points by name, function that raises for a status)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
@@ -613,6 +720,7 @@ PyMethodDef methods[] = {FUNCTION(bind),      FUNCTION(route),    FUNCTION(route
                          FUNCTION(group),     FUNCTION(dispatch), FUNCTION(combine),
                          FUNCTION(combine_backward), FUNCTION(embedding), FUNCTION(embedding_backward),
                          FUNCTION(expert_matmul),    FUNCTION(expert_matmul_backward),
+                         FUNCTION(layer_norm),       FUNCTION(layer_norm_backward), FUNCTION(quantize_rows),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_rows_native", nullptr, -1, methods};
 
