@@ -80,29 +80,63 @@ __device__ __forceinline__ bool in_row(int lane, int lanes, int width, int i, in
   return N > 1 ? at < width : at + j * lanes < width;
 }
 
+// Whether a group loads its next row while it works on one: a block does, since
+// its warps wait for one another at every row; warps on their own do not.
+constexpr bool ahead(int warps) { return warps > 1; }
+
 template <class T, class W, int N, int PARTS, int WARPS>
 __global__ void __launch_bounds__(WARPS == 1 ? kThreads : WARPS * 32)
 norm_kernel(const T* x, int64_t x_stride, uint32_t rows, int width, const W* weight, const W* bias, float eps, T* out,
             float* means, float* rstds)
 {
-  __shared__ Sums<WARPS> sh;
+  __shared__ float2 parts[2][WARPS];
   wait_for_previous();
   allow_next();
   constexpr int kLanes = WARPS * 32;
-  const int lane = threadIdx.x % kLanes;
+  const int lane = threadIdx.x % kLanes, warp = lane / 32;
   const uint32_t step = gridDim.x * (blockDim.x / kLanes);
   int turn = 0;
   const float part_of = 1.0f / (float)width;
-  for (uint32_t r = blockIdx.x * (blockDim.x / kLanes) + threadIdx.x / kLanes; r < rows; r += step) {
+  // values that this warp, and each warp, has
+  auto values_of = [&](int w) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+      if constexpr (N > 1) {
+        n += max(0, min(32 * N, width - (i * kLanes + w * 32) * N));
+      } else {
+#pragma unroll
+        for (int j = 0; j < kLoose; ++j)
+          n += max(0, min(32, width - (i * kLoose + j) * kLanes - w * 32));
+      }
+    }
+    return (float)n;
+  };
+  const float mine = values_of(warp);
+  const float other = WARPS > 1 && (threadIdx.x & 31) < WARPS ? values_of(threadIdx.x & 31) : 0.0f;
+  Share<T, N, PARTS> next;
+  uint32_t r = blockIdx.x * (blockDim.x / kLanes) + threadIdx.x / kLanes;
+  if (ahead(WARPS) && r < rows)
+    load_row(next, x + (int64_t)r * x_stride, lane, kLanes, width);
+  for (; r < rows; r += step) {
     Share<T, N, PARTS> s;
-    load_row(s, x + (int64_t)r * x_stride, lane, kLanes, width);
+    if constexpr (ahead(WARPS)) {
+      s = next;
+      if (step < rows - r)
+        load_row(next, x + (int64_t)(r + step) * x_stride, lane, kLanes, width);
+    } else {
+      load_row(s, x + (int64_t)r * x_stride, lane, kLanes, width);
+    }
+    // the warp's mean and its values' squares about it, then those of the row:
+    // n var = sum over the warps of theirs + n_w (mean_w - mean)^2, which needs
+    // one barrier and does not cancel
     float sum = 0;
 #pragma unroll
     for (int i = 0; i < PARTS; ++i)
 #pragma unroll
       for (int j = 0; j < kPart<N>; ++j)
         sum += s.part[i].f32(j);
-    const float mean = group_sum<WARPS>(make_float2(sum, 0), sh, turn).x * part_of;
+    float mean = mine > 0 ? warp_sum(sum) / mine : 0.0f;
     float square = 0;
 #pragma unroll
     for (int i = 0; i < PARTS; ++i)
@@ -111,8 +145,19 @@ norm_kernel(const T* x, int64_t x_stride, uint32_t rows, int width, const W* wei
         const float d = in_row<N>(lane, kLanes, width, i, j) ? s.part[i].f32(j) - mean : 0.0f;
         square = fmaf(d, d, square);
       }
-    const float var = group_sum<WARPS>(make_float2(square, 0), sh, turn).x * part_of;
-    const float rstd = 1.0f / sqrtf(var + eps);
+    square = warp_sum(square);
+    if constexpr (WARPS > 1) {
+      float2* part = parts[turn];
+      turn ^= 1;
+      if ((threadIdx.x & 31) == 0)
+        part[warp] = make_float2(mean, square);
+      __syncthreads();
+      const float2 p = other > 0 ? part[threadIdx.x & 31] : float2{};
+      mean = warp_sum(p.x * other) * part_of;
+      const float d = p.x - mean;
+      square = warp_sum(fmaf(d * d, other, p.y));
+    }
+    const float rstd = 1.0f / sqrtf(square * part_of + eps);
     if (lane == 0) {
       means[r] = mean;
       rstds[r] = rstd;
@@ -156,11 +201,31 @@ norm_backward_kernel(const T* grad, int64_t grad_stride, const T* x, int64_t x_s
   int turn = 0;
   const float part_of = 1.0f / (float)width;
   float sum_w[PARTS][kPart<N>] = {}, sum_b[PARTS][kPart<N>] = {};
-  for (uint32_t r = blockIdx.x * kGroups + group; r < rows; r += step) {
-    Share<T, N, PARTS> sx, sg;
-    load_row(sg, grad + (int64_t)r * grad_stride, lane, kLanes, width);
-    load_row(sx, x + (int64_t)r * x_stride, lane, kLanes, width);
-    const float mean = means[r], rstd = rstds[r];
+  struct Row {
+    Share<T, N, PARTS> g, x;
+    float mean, rstd;
+  };
+  auto get = [&](Row& row, uint32_t r) {
+    load_row(row.g, grad + (int64_t)r * grad_stride, lane, kLanes, width);
+    load_row(row.x, x + (int64_t)r * x_stride, lane, kLanes, width);
+    row.mean = means[r];
+    row.rstd = rstds[r];
+  };
+  Row next;
+  uint32_t r = blockIdx.x * kGroups + group;
+  if (ahead(WARPS) && r < rows)
+    get(next, r);
+  for (; r < rows; r += step) {
+    Row row;
+    if constexpr (ahead(WARPS)) {
+      row = next;
+      if (step < rows - r)
+        get(next, r + step);
+    } else {
+      get(row, r);
+    }
+    const Share<T, N, PARTS>&sx = row.x, &sg = row.g;
+    const float mean = row.mean, rstd = row.rstd;
     float2 inner = {};
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) {
@@ -309,7 +374,7 @@ quantize_kernel(const T* x, int64_t x_stride, uint32_t blocks, uint32_t per_row,
   for (int i = 0; i < STEPS; ++i) {
     const uint32_t b = first + i * kGroups;
     row[i] = b / per_row;
-    at[i] = (int)(b - row[i] * per_row) * kBlock + lane * 8;
+    at[i] = (int)(b - row[i] * per_row) * kBlock + (VECTOR ? lane * 8 : lane); // then 16 apart, side by side in a warp
     const bool in = b < blocks;
     const T* from = x + (int64_t)row[i] * x_stride + at[i];
     if constexpr (VECTOR) {
@@ -326,7 +391,7 @@ quantize_kernel(const T* x, int64_t x_stride, uint32_t blocks, uint32_t per_row,
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        v[i][j] = in && at[i] + j < width ? to_f32(from[j]) : 0.0f;
+        v[i][j] = in && at[i] + 16 * j < width ? to_f32(from[16 * j]) : 0.0f;
     }
   }
 #pragma unroll
@@ -353,8 +418,8 @@ quantize_kernel(const T* x, int64_t x_stride, uint32_t blocks, uint32_t per_row,
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (at[i] + j < width)
-            to[j] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+          if (at[i] + 16 * j < width)
+            to[16 * j] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
       }
     }
   }
@@ -373,9 +438,9 @@ cudaError_t with_group(int64_t parts, F&& f)
   if (parts <= 64)
     SEGTOPK_GROUP(2, 1);
   if (parts <= 128)
-    SEGTOPK_GROUP(1, 4);
+    SEGTOPK_GROUP(4, 1);
   if (parts <= 256)
-    SEGTOPK_GROUP(1, 8);
+    SEGTOPK_GROUP(2, 4);
   if (parts <= 512)
     SEGTOPK_GROUP(2, 8);
   if (parts <= 1024)
@@ -389,12 +454,15 @@ cudaError_t with_group(int64_t parts, F&& f)
 unsigned threads_of(int warps) { return warps == 1 ? kThreads : warps * 32; }
 int groups_of(int warps) { return warps == 1 ? kThreads / 32 : 1; }
 
-// Blocks of the first backward kernel. Each leaves 2 * width sums.
-constexpr int64_t kMostBlocks = 152 * 8;
-int64_t backward_blocks(int64_t rows, int groups, int warps)
+// Blocks that stay, each with several rows: as many as the SMs hold at once of
+// groups that load ahead (16 warps an SM have 64 KB of rows under way), more of
+// warps on their own. In the backward pass each leaves 2 * width sums.
+constexpr int64_t kSms = 152;
+constexpr int64_t kMostBlocks = kSms * 4;
+int64_t blocks_for(int64_t rows, int warps)
 {
-  const int64_t resident = 152 * std::max(1, 48 / (groups * warps)); // 1536 threads an SM
-  return std::max<int64_t>(1, std::min({(rows + groups - 1) / groups, resident, kMostBlocks}));
+  return std::max<int64_t>(1, std::min<int64_t>((rows + groups_of(warps) - 1) / groups_of(warps),
+                                                kSms * std::max(1, warps == 1 ? 2 : 16 / warps)));
 }
 
 int check(segtopk_dtype dtype, segtopk_dtype weight_dtype, int64_t rows, int64_t width)
@@ -452,8 +520,9 @@ extern "C" int segtopk_layer_norm(segtopk_dtype dtype, const void* x, int64_t nu
       constexpr int V = decltype(n)::value;
       return with_group<V>(parts_of(width, V), [&](auto parts, auto warps) {
         constexpr int G = decltype(warps)::value;
-        const int64_t blocks = (num_rows + groups_of(G) - 1) / groups_of(G);
-        return launch(norm_kernel<T, W, V, decltype(parts)::value, G>, dim3((unsigned)std::min<int64_t>(blocks, 1 << 30)),
+        // warps on their own: the next rows are other blocks'
+        const int64_t blocks = G == 1 ? (num_rows + groups_of(G) - 1) / groups_of(G) : 2 * blocks_for(num_rows, G);
+        return launch(norm_kernel<T, W, V, decltype(parts)::value, G>, dim3((unsigned)blocks),
                       threads_of(G), 0, (cudaStream_t)stream, (const T*)x, row_stride, (uint32_t)num_rows, (int)width,
                       (const W*)weight, (const W*)bias, eps, (T*)out, mean, rstd);
       });
@@ -508,7 +577,7 @@ extern "C" int segtopk_layer_norm_backward(segtopk_dtype dtype, const void* grad
         constexpr int V = decltype(n)::value;
         return with_group<V>(parts_of(width, V), [&](auto parts, auto warps) {
           constexpr int G = decltype(warps)::value;
-          blocks = (int)backward_blocks(num_rows, groups_of(G), G);
+          blocks = (int)blocks_for(num_rows, G);
           return launch(norm_backward_kernel<T, W, V, decltype(parts)::value, G>, dim3((unsigned)blocks), threads_of(G), 0,
                         (cudaStream_t)stream, (const T*)grad_out, grad_stride, (const T*)x, row_stride,
                         (uint32_t)num_rows, (int)width, (const W*)weight, mean, rstd, (T*)grad_x, (float*)workspace);

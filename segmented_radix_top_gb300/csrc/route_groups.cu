@@ -16,7 +16,11 @@ extern "C" int segtopk_route_groups(segtopk_dtype dtype, const void* logits, int
     return SEGTOPK_ERROR_INVALID_VALUE;
   if (num_groups > SEGTOPK_MAX_GROUPS)
     return SEGTOPK_ERROR_NOT_SUPPORTED;
-  const GroupRule rule = {num_groups, experts / num_groups, groups_kept, group_score == SEGTOPK_GROUP_BEST_TWO};
+  int log_lanes = 5;
+  while (num_groups << log_lanes > 32)
+    --log_lanes;
+  const int size = experts / num_groups;
+  const GroupRule rule = {num_groups, size, groups_kept, group_score == SEGTOPK_GROUP_BEST_TWO, log_lanes, 1.0f / size};
   return route<true>(dtype, logits, tokens, experts, row_stride, k, rule, score, renormalize, scale, bias, expert_ids,
                      weights, stream);
 }
