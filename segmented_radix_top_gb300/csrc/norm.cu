@@ -19,7 +19,10 @@ namespace segtopk {
 namespace {
 using namespace rows;
 
-constexpr int kThreads = 256;         // where a warp serves a row
+constexpr int kThreads = 256; // of a block where a warp serves a row
+constexpr int kSmWarps = 16;  // of the blocks that an SM holds at once, backward pass
+constexpr int threads_of(int warps) { return warps == 1 ? kThreads : warps * 32; }
+constexpr int groups_of(int warps) { return warps == 1 ? kThreads / 32 : 1; }
 constexpr int kMaxNormWidth = SEGTOPK_MAX_NORM_WIDTH;
 
 __device__ __forceinline__ float warp_sum(float x)
@@ -80,22 +83,21 @@ __device__ __forceinline__ bool in_row(int lane, int lanes, int width, int i, in
   return N > 1 ? at < width : at + j * lanes < width;
 }
 
-// Whether a group loads its next row while it works on one: a block does, since
-// its warps wait for one another at every row; warps on their own do not.
-constexpr bool ahead(int warps) { return warps > 1; }
-
+// Parts of a row a thread has against warps that wait for one another: rows of
+// 4096 in bf16 (65536 of them) took 205 us with 2 parts and 8 warps, 172 with 4
+// and 4, 178 with 8 and 2, 200 with 16 and one; of 2048 199, 170 (4 and 2) and
+// 158 (8 and one). A row read ahead into registers, or several into shared
+// memory, cost more warps than it hid latency.
 template <class T, class W, int N, int PARTS, int WARPS>
-__global__ void __launch_bounds__(WARPS == 1 ? kThreads : WARPS * 32)
+__global__ void __launch_bounds__(threads_of(WARPS), std::max(1, (WARPS == 1 ? 768 : PARTS == 4 ? 1024 : 768) / threads_of(WARPS)))
 norm_kernel(const T* x, int64_t x_stride, uint32_t rows, int width, const W* weight, const W* bias, float eps, T* out,
             float* means, float* rstds)
 {
-  __shared__ float2 parts[2][WARPS];
+  __shared__ float2 part[WARPS];
   wait_for_previous();
   allow_next();
   constexpr int kLanes = WARPS * 32;
   const int lane = threadIdx.x % kLanes, warp = lane / 32;
-  const uint32_t step = gridDim.x * (blockDim.x / kLanes);
-  int turn = 0;
   const float part_of = 1.0f / (float)width;
   // values that this warp, and each warp, has
   auto values_of = [&](int w) {
@@ -114,19 +116,10 @@ norm_kernel(const T* x, int64_t x_stride, uint32_t rows, int width, const W* wei
   };
   const float mine = values_of(warp);
   const float other = WARPS > 1 && (threadIdx.x & 31) < WARPS ? values_of(threadIdx.x & 31) : 0.0f;
-  Share<T, N, PARTS> next;
-  uint32_t r = blockIdx.x * (blockDim.x / kLanes) + threadIdx.x / kLanes;
-  if (ahead(WARPS) && r < rows)
-    load_row(next, x + (int64_t)r * x_stride, lane, kLanes, width);
-  for (; r < rows; r += step) {
+  const uint32_t r = blockIdx.x * (blockDim.x / kLanes) + threadIdx.x / kLanes;
+  if (r < rows) { // the same for all of a group
     Share<T, N, PARTS> s;
-    if constexpr (ahead(WARPS)) {
-      s = next;
-      if (step < rows - r)
-        load_row(next, x + (int64_t)(r + step) * x_stride, lane, kLanes, width);
-    } else {
-      load_row(s, x + (int64_t)r * x_stride, lane, kLanes, width);
-    }
+    load_row(s, x + (int64_t)r * x_stride, lane, kLanes, width);
     // the warp's mean and its values' squares about it, then those of the row:
     // n var = sum over the warps of theirs + n_w (mean_w - mean)^2, which needs
     // one barrier and does not cancel
@@ -147,8 +140,6 @@ norm_kernel(const T* x, int64_t x_stride, uint32_t rows, int width, const W* wei
       }
     square = warp_sum(square);
     if constexpr (WARPS > 1) {
-      float2* part = parts[turn];
-      turn ^= 1;
       if ((threadIdx.x & 31) == 0)
         part[warp] = make_float2(mean, square);
       __syncthreads();
@@ -186,8 +177,15 @@ norm_kernel(const T* x, int64_t x_stride, uint32_t rows, int width, const W* wei
 }
 
 // Rows' gradients, and a row of the sums of g h and of g for each block.
+//
+// Where a group is a large block, whose warps wait for one another at every
+// row, it loads its next row while it works on one: 65536 rows of 4096 in
+// bf16 283 us, 315 without; with 4 parts and 4 warps 294. Groups of two warps
+// and single ones do not: rows of 2048 278 us, 354 with a row ahead.
+constexpr bool ahead(int warps) { return warps >= 8; }
+
 template <class T, class W, int N, int PARTS, int WARPS>
-__global__ void __launch_bounds__(WARPS == 1 ? kThreads : WARPS * 32)
+__global__ void __launch_bounds__(threads_of(WARPS), std::max(1, kSmWarps / (threads_of(WARPS) / 32)))
 norm_backward_kernel(const T* grad, int64_t grad_stride, const T* x, int64_t x_stride, uint32_t rows, int width,
                      const W* weight, const float* means, const float* rstds, T* grad_x, float* sums)
 {
@@ -215,7 +213,7 @@ norm_backward_kernel(const T* grad, int64_t grad_stride, const T* x, int64_t x_s
   uint32_t r = blockIdx.x * kGroups + group;
   if (ahead(WARPS) && r < rows)
     get(next, r);
-  for (; r < rows; r += step) {
+  for (; r < rows; r += step) { // rows + step is below 2^32
     Row row;
     if constexpr (ahead(WARPS)) {
       row = next;
@@ -317,7 +315,7 @@ norm_join_kernel(const float* sums, int blocks, int width, W* grad_weight, W* gr
     const float* at = sums + c;
     const int each = (blocks + kJoinWarps - 1) / kJoinWarps;
     const int end = min(blocks, (warp + 1) * each);
-#pragma unroll 8
+#pragma unroll 16
     for (int b = warp * each; b < end; ++b)
       sum += at[(int64_t)b * 2 * width];
   }
@@ -428,19 +426,35 @@ quantize_kernel(const T* x, int64_t x_stride, uint32_t blocks, uint32_t per_row,
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-// Calls f with the parts that a thread holds of a row and the warps of a group:
-// a warp for up to 64 parts, else a block.
-template <int N, class F>
+// Calls f with the parts that a thread holds of a row and the warps of a group
+// (measured at the kernels).
+#define SEGTOPK_GROUP(P, WARPS) return f(std::integral_constant<int, P>{}, std::integral_constant<int, WARPS>{})
+template <class F>
 cudaError_t with_group(int64_t parts, F&& f)
 {
-  using std::integral_constant;
-#define SEGTOPK_GROUP(P, WARPS) return f(integral_constant<int, P>{}, integral_constant<int, WARPS>{})
   if (parts <= 64)
     SEGTOPK_GROUP(2, 1);
   if (parts <= 128)
     SEGTOPK_GROUP(4, 1);
   if (parts <= 256)
-    SEGTOPK_GROUP(2, 4);
+    SEGTOPK_GROUP(8, 1);
+  if (parts <= 512)
+    SEGTOPK_GROUP(4, 4);
+  if (parts <= 1024)
+    SEGTOPK_GROUP(8, 4);
+  if (parts <= 2048)
+    SEGTOPK_GROUP(8, 8);
+  SEGTOPK_GROUP(8, 16);
+}
+template <int N, class F>
+cudaError_t with_backward_group(int64_t parts, F&& f)
+{
+  if (parts <= 64)
+    SEGTOPK_GROUP(2, 1);
+  if (parts <= 128)
+    SEGTOPK_GROUP(4, 1);
+  if (parts <= 256)
+    SEGTOPK_GROUP(4, 2);
   if (parts <= 512)
     SEGTOPK_GROUP(2, 8);
   if (parts <= 1024)
@@ -449,20 +463,19 @@ cudaError_t with_group(int64_t parts, F&& f)
     if (parts > 2048)
       SEGTOPK_GROUP(4, 32);
   SEGTOPK_GROUP(2, 32);
-#undef SEGTOPK_GROUP
 }
-unsigned threads_of(int warps) { return warps == 1 ? kThreads : warps * 32; }
-int groups_of(int warps) { return warps == 1 ? kThreads / 32 : 1; }
+#undef SEGTOPK_GROUP
 
-// Blocks that stay, each with several rows: as many as the SMs hold at once of
-// groups that load ahead (16 warps an SM have 64 KB of rows under way), more of
-// warps on their own. In the backward pass each leaves 2 * width sums.
+// Blocks of the backward pass stay and take row after row; each leaves 2 *
+// width sums, so a group has four rows at least where that leaves no SM idle
+// (1237 rows of 1001 in f32: 14.1 us with one row each, 1216 blocks).
 constexpr int64_t kSms = 152;
-constexpr int64_t kMostBlocks = kSms * 4;
+constexpr int64_t kMostBlocks = kSms * (kSmWarps / 2);
 int64_t blocks_for(int64_t rows, int warps)
 {
-  return std::max<int64_t>(1, std::min<int64_t>((rows + groups_of(warps) - 1) / groups_of(warps),
-                                                kSms * std::max(1, warps == 1 ? 2 : 16 / warps)));
+  const int64_t resident = kSms * std::max(1, kSmWarps / (threads_of(warps) / 32));
+  const int64_t each = groups_of(warps), most = (rows + each - 1) / each;
+  return std::max<int64_t>(1, std::min({most, std::max(kSms, most / 4), resident}));
 }
 
 int check(segtopk_dtype dtype, segtopk_dtype weight_dtype, int64_t rows, int64_t width)
@@ -518,10 +531,9 @@ extern "C" int segtopk_layer_norm(segtopk_dtype dtype, const void* x, int64_t nu
                         rows_fit(weight, width, width, sizeof(W), N) && rows_fit(bias, width, width, sizeof(W), N);
     auto go = [&](auto n) {
       constexpr int V = decltype(n)::value;
-      return with_group<V>(parts_of(width, V), [&](auto parts, auto warps) {
+      return with_group(parts_of(width, V), [&](auto parts, auto warps) {
         constexpr int G = decltype(warps)::value;
-        // warps on their own: the next rows are other blocks'
-        const int64_t blocks = G == 1 ? (num_rows + groups_of(G) - 1) / groups_of(G) : 2 * blocks_for(num_rows, G);
+        const int64_t blocks = (num_rows + groups_of(G) - 1) / groups_of(G);
         return launch(norm_kernel<T, W, V, decltype(parts)::value, G>, dim3((unsigned)blocks),
                       threads_of(G), 0, (cudaStream_t)stream, (const T*)x, row_stride, (uint32_t)num_rows, (int)width,
                       (const W*)weight, (const W*)bias, eps, (T*)out, mean, rstd);
@@ -575,7 +587,7 @@ extern "C" int segtopk_layer_norm_backward(segtopk_dtype dtype, const void* grad
                           rows_fit(grad_x, width, width, sizeof(T), N) && rows_fit(weight, width, width, sizeof(W), N);
       auto go = [&](auto n) {
         constexpr int V = decltype(n)::value;
-        return with_group<V>(parts_of(width, V), [&](auto parts, auto warps) {
+        return with_backward_group<V>(parts_of(width, V), [&](auto parts, auto warps) {
           constexpr int G = decltype(warps)::value;
           blocks = (int)blocks_for(num_rows, G);
           return launch(norm_backward_kernel<T, W, V, decltype(parts)::value, G>, dim3((unsigned)blocks), threads_of(G), 0,
