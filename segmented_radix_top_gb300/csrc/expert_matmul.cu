@@ -39,7 +39,7 @@ constexpr int kSumWarps = 8;     // of them the last
 constexpr int kTileP = 128;      // of a block: the lanes of TMEM
 constexpr int kTileQ = 256;      // half of its columns
 constexpr int kOperandBytes = 192 << 10;
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 4;
 constexpr int kBytesP = kTileP * 128;
 constexpr int kBox = 32;         // rows of one copy of few of an expert's rows
 constexpr int kDepth = 64;       // rows of one copy where c runs over rows
@@ -56,9 +56,13 @@ constexpr bool p_by_rows(Kind k) { return eight(k) || k == kForward; } // rows o
 constexpr bool q_by_rows(Kind k) { return k != kWeights; }
 constexpr int tile_p(Kind k) { return kTileP * blocks_of(k); }
 constexpr int bytes_q(Kind k) { return kTileQ / blocks_of(k) * 128; }
-constexpr int stage_bytes(Kind k) { return kBytesP + bytes_q(k); }
+// Blocks of c that are copied and waited for at a time: issuing the products of
+// one takes 200 cycles, the waits around them as many again.
+constexpr int run_of(Kind k) { return pair(k) ? 2 : 1; }
+constexpr int block_bytes(Kind k) { return kBytesP + bytes_q(k); }
+constexpr int stage_bytes(Kind k) { return block_bytes(k) * run_of(k); }
 constexpr int stages_of(Kind k) { return kOperandBytes / stage_bytes(k); }
-static_assert(stages_of(kForward) <= kMaxStages);
+static_assert(stages_of(kForward) <= kMaxStages && stages_of(kForward8) <= kMaxStages);
 
 struct Control {
   uint64_t full[kMaxStages], empty[kMaxStages]; // copies (a pair's: at its first block) have landed; products have read them
@@ -151,17 +155,14 @@ __device__ __forceinline__ void commit(uint64_t* bar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
                  : "memory");
 }
-// At a barrier of either block of a pair. What the other block has to see of
-// this one's memory goes with the second form only: it waits until all of it
-// is visible there, and once every block of 8-bit operands that doubled the
-// time of a product.
+// At a barrier of either block of a pair. Without a release at cluster scope,
+// which waits until all of the block's writes are visible everywhere: once
+// every block of 8-bit operands that doubled the time of a product. What the
+// other block is told here is that it may write, or what a fence has already
+// made visible to the tensor cores.
 __device__ __forceinline__ void arrive(uint32_t bar)
 {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void release(uint32_t bar)
-{
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // The address of the first block's `bar`.
 template <Kind K>
@@ -415,34 +416,38 @@ __device__ void copy_operands(bool is_p, const CUtensorMap& map, const CUtensorM
     const bool by_rows = is_p == eight(K) && K != kWeights; // these are the expert's rows
     const CUtensorMap& from = by_rows && lines == kTileP ? large : map;
     const int box = K == kWeights || (is_p && K == kForwardTurned) ? 64 : by_rows && lines < kTileP ? kBox : kTileP;
-    for (int b = 0; b < tile.blocks; ++b) {
+    for (int b = 0; b < tile.blocks; b += run_of(K)) {
       if (!ready)
         ok = wait(&sh.empty[s.at], s.parity ^ 1, sh);
       if (!ok)
         break;
+      const int n = min(run_of(K), tile.blocks - b);
       char* const to = stages + s.at * stage_bytes(K) + (is_p ? 0 : kBytesP);
       uint32_t bar = at_first<K>(&sh.full[s.at]);
-      if (K == kWeights && (b + 1) * kDepth > tile.rows) {
+      if (K == kWeights && (b + n) * kDepth > tile.rows) {
         // an expert's last rows: each block of the pair first takes out those of others
         if (is_p && me == 0)
           arrive(bar);
         bar = smem_addr(&sh.end_full[s.at]);
         if (is_p)
-          mbar_arrive_expect_tx(&sh.end_full[s.at], (lines_p + lines_q) * 128);
+          mbar_arrive_expect_tx(&sh.end_full[s.at], (lines_p + lines_q) * 128 * n);
       } else if (is_p && me == 0) {
-        mbar_arrive_expect_tx(&sh.full[s.at], expected * 128);
+        mbar_arrive_expect_tx(&sh.full[s.at], expected * 128 * n);
       }
       used = min(used + 1, kStages);
       s.next();
       ready = over(&sh.empty[s.at], s.parity ^ 1);
-      for (int i = 0; i < lines; i += box) {
-        if constexpr (K == kWeights)
-          tile_load<true>(to + i * 128, &from, first + i, tile.row + b * kDepth, 0, bar);
-        else if (K == kForwardTurned && is_p)
-          tile_load<true>(to + i * 128, &from, first + i, b * kDepth, tile.expert, bar);
-        else
-          tile_load<pair(K)>(to + i * 128, &from, b * (eight(K) ? 128 : 64), (by_rows ? tile.row : 0) + first + i,
-                             by_rows ? 0 : tile.expert, bar);
+      for (int j = 0; j < n; ++j) {
+        char* const block = to + j * block_bytes(K);
+        for (int i = 0; i < lines; i += box) {
+          if constexpr (K == kWeights)
+            tile_load<true>(block + i * 128, &from, first + i, tile.row + (b + j) * kDepth, 0, bar);
+          else if (K == kForwardTurned && is_p)
+            tile_load<true>(block + i * 128, &from, first + i, (b + j) * kDepth, tile.expert, bar);
+          else
+            tile_load<pair(K)>(block + i * 128, &from, (b + j) * (eight(K) ? 128 : 64), (by_rows ? tile.row : 0) + first + i,
+                               by_rows ? 0 : tile.expert, bar);
+        }
       }
     }
   }
@@ -461,24 +466,27 @@ __device__ void copy_operands(bool is_p, const CUtensorMap& map, const CUtensorM
 // products read them.
 __device__ void clear_ends(const Sizes& z, char* stages, Control& sh)
 {
+  constexpr Kind K = kWeights;
   const int lane = threadIdx.x & 31, tiles = sh.tile_start[z.experts];
-  Ring<stages_of(kWeights)> s;
+  Ring<stages_of(K)> s;
   uint32_t before = 0; // a bit for each stage: the parity of its last blocks of rows
   for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2) {
-    const Tile tile = tile_at<kWeights>(t, z, sh);
+    const Tile tile = tile_at<K>(t, z, sh);
     const int copies = 2 + pieces(pieces(tile.width, kStepQ) * kStepQ / 2, 64), left = tile.rows % kDepth;
-    for (int b = 0; b < tile.blocks; ++b) {
-      if (left != 0 && b == tile.blocks - 1) {
+    for (int b = 0; b < tile.blocks; b += run_of(K)) {
+      const int n = min(run_of(K), tile.blocks - b);
+      if (left != 0 && b + n == tile.blocks) {
         if (!__all_sync(kAll, wait(&sh.end_full[s.at], before >> s.at & 1, sh)))
           return;
         before ^= 1u << s.at;
+        char* const block = stages + s.at * stage_bytes(K) + (n - 1) * block_bytes(K);
         for (int i = 0; i < copies; ++i)
           for (int at = left * 128 + lane * 16; at < kDepth * 128; at += 512)
-            *reinterpret_cast<uint4*>(stages + s.at * stage_bytes(kWeights) + i * kDepth * 128 + at) = uint4{};
+            *reinterpret_cast<uint4*>(block + i * kDepth * 128 + at) = uint4{};
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0)
-          release(at_first<kWeights>(&sh.end_ready[s.at]));
+          arrive(at_first<K>(&sh.end_ready[s.at]));
       }
       s.next();
     }
@@ -491,6 +499,7 @@ __device__ void clear_ends(const Sizes& z, char* stages, Control& sh)
 template <Kind K>
 __device__ void issue_products(const Sizes& z, char* stages, Control& sh)
 {
+  constexpr int kRun = run_of(K);
   const int tiles = sh.tile_start[z.experts];
   const uint32_t tmem = sh.tmem;
   const uint64_t p0 = operand<p_by_rows(K)>(smem_addr(stages)), q0 = operand<q_by_rows(K)>(smem_addr(stages) + kBytesP);
@@ -501,35 +510,51 @@ __device__ void issue_products(const Sizes& z, char* stages, Control& sh)
   for (int t = blockIdx.x / blocks_of(K); ok && t < tiles; t += gridDim.x / blocks_of(K)) {
     const Tile tile = tile_at<K>(t, z, sh);
     const uint32_t instruction = z.instruction | (uint32_t)(pieces(tile.width, kStepQ) * kStepQ / 8) << 17;
-    for (int b = 0; b < tile.blocks; ++b) {
-      // the sums of one block, or of all
-      const bool first = eight(K) || b == 0, last = eight(K) || b == tile.blocks - 1;
-      ok = (!first || sums_ready || wait(&sh.sums_empty[d.at], d.parity ^ 1, sh)) &&
-           (ready || wait(&sh.full[s.at], s.parity, sh));
-      if (K == kWeights && ok && last && tile.rows % kDepth != 0) {
+    if (!eight(K) && tile.blocks > 0)
+      ok = sums_ready || wait(&sh.sums_empty[d.at], d.parity ^ 1, sh);
+    for (int b = 0; ok && b < tile.blocks; b += kRun) {
+      const int n = min(kRun, tile.blocks - b);
+      if (!ready)
+        ok = wait(&sh.full[s.at], s.parity, sh);
+      if (K == kWeights && ok && b + n == tile.blocks && tile.rows % kDepth != 0) {
         ok = wait(&sh.end_ready[s.at], ends_before >> s.at & 1, sh);
         ends_before ^= 1u << s.at;
       }
       if (!ok)
         break;
       fence_after_sync();
-      const uint64_t p = p0 + s.at * (stage_bytes(K) / 16), q = q0 + s.at * (stage_bytes(K) / 16);
-      const uint32_t sums = tmem + d.at * kTileQ;
-      uint64_t *const empty = &sh.empty[s.at], *const sums_full = &sh.sums_full[d.at];
+      const uint32_t stage = s.at * (stage_bytes(K) / 16);
+      uint64_t* const empty = &sh.empty[s.at];
       s.next();
       ready = over(&sh.full[s.at], s.parity);
-      if (last) {
-        d.next();
-        sums_ready = over(&sh.sums_empty[d.at], d.parity ^ 1);
-      }
-      // four products: 32 bytes of c on, or 16 rows of 128 bytes
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        multiply<K>(sums, p + i * (p_by_rows(K) ? 2 : 128), q + i * (q_by_rows(K) ? 2 : 128),
-                    instruction, !first || i > 0);
+      for (int j = 0; j < kRun; ++j) {
+        if (j > 0 && j >= n)
+          break;
+        if constexpr (eight(K)) { // each block has sums of its own
+          ok = sums_ready || wait(&sh.sums_empty[d.at], d.parity ^ 1, sh);
+          if (!ok)
+            break;
+          fence_after_sync();
+        }
+        const uint64_t p = p0 + stage + j * (block_bytes(K) / 16), q = q0 + stage + j * (block_bytes(K) / 16);
+        // four products: 32 bytes of c on, or 16 rows of 128 bytes
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          multiply<K>(tmem + d.at * kTileQ, p + i * (p_by_rows(K) ? 2 : 128), q + i * (q_by_rows(K) ? 2 : 128), instruction,
+                      eight(K) ? i > 0 : b > 0 || j > 0 || i > 0);
+        if constexpr (eight(K)) {
+          commit<pair(K)>(&sh.sums_full[d.at]);
+          d.next();
+          sums_ready = over(&sh.sums_empty[d.at], d.parity ^ 1);
+        }
+      }
       commit<pair(K)>(empty);
-      if (last)
-        commit<pair(K)>(sums_full);
+    }
+    if (!eight(K) && ok && tile.blocks > 0) {
+      commit<pair(K)>(&sh.sums_full[d.at]);
+      d.next();
+      sums_ready = over(&sh.sums_empty[d.at], d.parity ^ 1);
     }
   }
   if (!ok) {
