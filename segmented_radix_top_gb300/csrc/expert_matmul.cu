@@ -39,7 +39,7 @@ constexpr int kSumWarps = 8;     // of them the last
 constexpr int kTileP = 128;      // of a block: the lanes of TMEM
 constexpr int kTileQ = 256;      // half of its columns
 constexpr int kOperandBytes = 192 << 10;
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 6;
 constexpr int kBytesP = kTileP * 128;
 constexpr int kBox = 32;         // rows of one copy of few of an expert's rows
 constexpr int kDepth = 64;       // rows of one copy where c runs over rows
@@ -56,11 +56,7 @@ constexpr bool p_by_rows(Kind k) { return eight(k) || k == kForward; } // rows o
 constexpr bool q_by_rows(Kind k) { return k != kWeights; }
 constexpr int tile_p(Kind k) { return kTileP * blocks_of(k); }
 constexpr int bytes_q(Kind k) { return kTileQ / blocks_of(k) * 128; }
-// Blocks of c that are copied and waited for at a time: issuing the products of
-// one takes 200 cycles, the waits around them as many again.
-constexpr int run_of(Kind k) { return pair(k) ? 2 : 1; }
-constexpr int block_bytes(Kind k) { return kBytesP + bytes_q(k); }
-constexpr int stage_bytes(Kind k) { return block_bytes(k) * run_of(k); }
+constexpr int stage_bytes(Kind k) { return kBytesP + bytes_q(k); }
 constexpr int stages_of(Kind k) { return kOperandBytes / stage_bytes(k); }
 static_assert(stages_of(kForward) <= kMaxStages && stages_of(kForward8) <= kMaxStages);
 
@@ -98,21 +94,32 @@ struct Sizes {
 __device__ __forceinline__ void fence_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// What follows is issued by one lane (`on`) of a warp whose lanes all get here:
+// their operands then stay in the warp's uniform registers. In a branch that
+// one lane takes alone each product cost 48 cycles and each copy 165.
+__device__ __forceinline__ uint32_t elected()
+{
+  uint32_t on;
+  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}" : "=r"(on));
+  return on;
+}
+
 // A copy that counts at `bar`: an address in the cluster's shared memory, of
 // either block of a pair.
 template <bool PAIR>
-__device__ __forceinline__ void tile_load(void* to, const CUtensorMap* map, int x, int y, int z, uint32_t bar)
+__device__ __forceinline__ void tile_load(uint32_t on, uint32_t to, const CUtensorMap* map, int x, int y, int z, uint32_t bar)
 {
+#define SEGTOPK_COPY(GROUP)                                                                                      \
+  asm volatile("{\n .reg .pred e;\n setp.ne.b32 e, %6, 0;\n"                                                    \
+               " @e cp.async.bulk.tensor.3d" GROUP ".shared::cluster.global.tile.mbarrier::complete_tx::bytes "  \
+               "[%0], [%1, {%2, %3, %4}], [%5];\n}" ::"r"(to),                                                   \
+               "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(on)                                               \
+               : "memory")
   if constexpr (PAIR)
-    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(to)),
-                 "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-                 : "memory");
+    SEGTOPK_COPY(".cta_group::2");
   else
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(to)),
-                 "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-                 : "memory");
+    SEGTOPK_COPY("");
+#undef SEGTOPK_COPY
 }
 
 // Shared-memory operand of 128-byte rows, swizzled over eight of them. Rows
@@ -126,12 +133,12 @@ __device__ __forceinline__ uint64_t operand(uint32_t address)
 }
 
 template <Kind K>
-__device__ __forceinline__ void multiply(uint32_t sums, uint64_t p, uint64_t q, uint32_t instruction, bool add)
+__device__ __forceinline__ void multiply(uint32_t on, uint32_t sums, uint64_t p, uint64_t q, uint32_t instruction, bool add)
 {
 #define SEGTOPK_MULTIPLY(GROUP, TYPE)                                                                            \
-  asm volatile("{\n .reg .pred a;\n setp.ne.b32 a, %4, 0;\n"                                                    \
-               " tcgen05.mma.cta_group::" GROUP ".kind::" TYPE " [%0], %1, %2, %3, a;\n}" ::"r"(sums),           \
-               "l"(p), "l"(q), "r"(instruction), "r"((uint32_t)add)                                              \
+  asm volatile("{\n .reg .pred a, e;\n setp.ne.b32 a, %4, 0;\n setp.ne.b32 e, %5, 0;\n"                         \
+               " @e tcgen05.mma.cta_group::" GROUP ".kind::" TYPE " [%0], %1, %2, %3, a;\n}" ::"r"(sums),        \
+               "l"(p), "l"(q), "r"(instruction), "r"((uint32_t)add), "r"(on)                                     \
                : "memory")
   if constexpr (eight(K) && pair(K))
     SEGTOPK_MULTIPLY("2", "f8f6f4");
@@ -144,16 +151,24 @@ __device__ __forceinline__ void multiply(uint32_t sums, uint64_t p, uint64_t q, 
 // Arrives at `bar`, a pair's at both blocks', once the products issued so far
 // are done.
 template <bool PAIR>
-__device__ __forceinline__ void commit(uint64_t* bar)
+__device__ __forceinline__ void commit(uint32_t on, uint32_t bar)
 {
   if constexpr (PAIR)
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                   smem_addr(bar)),
-                 "h"((uint16_t)3)
+    asm volatile("{\n .reg .pred e;\n setp.ne.b32 e, %2, 0;\n @e tcgen05.commit.cta_group::2.mbarrier::arrive::one"
+                 ".shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::"r"(bar),
+                 "h"((uint16_t)3), "r"(on)
                  : "memory");
   else
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+    asm volatile("{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n @e tcgen05.commit.cta_group::1.mbarrier::arrive::one"
+                 ".shared::cluster.b64 [%0];\n}" ::"r"(bar),
+                 "r"(on)
                  : "memory");
+}
+__device__ __forceinline__ void expect(uint32_t on, uint32_t bar, int bytes)
+{
+  asm volatile("{\n .reg .pred e;\n setp.ne.b32 e, %2, 0;\n @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}" ::"r"(bar),
+               "r"(bytes), "r"(on)
+               : "memory");
 }
 // At a barrier of either block of a pair. Without a release at cluster scope,
 // which waits until all of the block's writes are visible everywhere: once
@@ -210,38 +225,52 @@ __device__ __forceinline__ void sums_load(uint32_t (&v)[64], uint32_t at)
                : "memory");
 }
 
-// Waits for the phase of `bar` with this parity; false, for good, after about
-// a second, or once another wait of the block has run out.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Control& sh)
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
 {
-  if (mbar_try_wait(bar, parity))
+  uint32_t ok;
+  asm volatile(
+    "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+    : "=r"(ok)
+    : "r"(bar), "r"(parity)
+    : "memory");
+  return ok != 0;
+}
+// One warp: waits for the phase of `bar` with this parity; false, for good,
+// after about a second, or once another wait of the block has run out.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Control& sh)
+{
+  if (__all_sync(kAll, try_wait(bar, parity)))
     return true;
   const long long start = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (*(volatile int*)&sh.failed)
-      return false;
+  bool failed = false;
+  while (!__all_sync(kAll, try_wait(bar, parity))) {
     if (clock64() - start > kWaitLimitCycles) {
       *(volatile int*)&sh.failed = 1;
       raise_error(kErrCopyTimeout);
-      return false;
     }
+    failed = *(volatile int*)&sh.failed;
+    if (__any_sync(kAll, failed))
+      return false;
   }
   return true;
 }
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Control& sh) { return wait(smem_addr(bar), parity, sh); }
 
 // Whether that phase is over already; does not wait. Asked a step ahead, so
-// that the answer is there when the step comes: a wait alone takes a hundred
-// cycles or two even where there is nothing to wait for.
-__device__ __forceinline__ bool over(uint64_t* bar, uint32_t parity)
+// that the answer is there when the step comes.
+__device__ __forceinline__ bool over(uint32_t bar, uint32_t parity)
 {
   uint32_t ok;
   asm volatile(
     "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
     : "=r"(ok)
-    : "r"(smem_addr(bar)), "r"(parity)
+    : "r"(bar), "r"(parity)
     : "memory");
   return ok != 0;
 }
+
+// The same value in all lanes, known to be so.
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(kAll, x); }
 
 // A place in a ring of N and the parity of the passes over it.
 template <int N>
@@ -381,26 +410,27 @@ __device__ void find_tiles(const int64_t* offsets, const Sizes& z, Control& sh)
 // ---------------------------------------------------------------------------
 // Kernel
 // ---------------------------------------------------------------------------
-// One thread each for p and q: copies of this block's operands, as stages get
-// free. A pair's count at the first block, whose thread for p expects those of
+// A warp each for p and q: copies of this block's operands, as stages get
+// free. A pair's count at the first block, whose warp for p expects those of
 // both; they may land before it says so, since the phase waits for that too.
 // An expert's rows come in boxes of kTileP, or of kBox where that is less; all
 // boxes are copied whole, whatever of them there is.
 __device__ __forceinline__ int boxed(int rows) { return rows > kTileP / 2 ? kTileP : pieces(max(rows, 0), kBox) * kBox; }
 
-template <Kind K>
-__device__ void copy_operands(bool is_p, const CUtensorMap& map, const CUtensorMap& large, const Sizes& z, char* stages,
-                              Control& sh)
+template <Kind K, bool IS_P>
+__device__ void copy_operands(const CUtensorMap& map, const CUtensorMap& large, const Sizes& z, char* stages, Control& sh)
 {
   constexpr int kStages = stages_of(K);
-  const int tiles = sh.tile_start[z.experts], me = rank<K>();
+  constexpr bool kByRows = IS_P == eight(K) && K != kWeights; // these are the expert's rows
+  const int tiles = uniform(sh.tile_start[z.experts]), me = rank<K>();
+  const uint32_t on = elected(), to = smem_addr(stages) + (IS_P ? 0 : kBytesP);
+  const uint32_t full = at_first<K>(&sh.full[0]), empty = smem_addr(&sh.empty[0]);
   Ring<kStages> s;
   int used = 0; // stages whose copies are under way or have landed
   bool ok = true, ready = false;
   for (int t = blockIdx.x / blocks_of(K); ok && t < tiles; t += gridDim.x / blocks_of(K)) {
     const Tile tile = tile_at<K>(t, z, sh);
     const int width = pieces(tile.width, kStepQ) * kStepQ / blocks_of(K); // of q in this block
-    const int first = is_p ? tile.p + me * kTileP : tile.q + me * width;
     // rows of 128 bytes that land
     int lines_p = kTileP, lines_q;
     if constexpr (eight(K)) {
@@ -409,49 +439,54 @@ __device__ void copy_operands(bool is_p, const CUtensorMap& map, const CUtensorM
     } else {
       lines_q = K == kWeights ? pieces(width, 64) * 64 : boxed(width);
     }
-    int expected = lines_p + lines_q;
+    const int landing = uniform((lines_p + lines_q) * 128);
+    int expected = landing;
     if constexpr (pair(K))
-      expected += eight(K) ? boxed(tile.rows - tile.p - kTileP) + lines_q : expected;
-    const int lines = is_p ? lines_p : lines_q;
-    const bool by_rows = is_p == eight(K) && K != kWeights; // these are the expert's rows
-    const CUtensorMap& from = by_rows && lines == kTileP ? large : map;
-    const int box = K == kWeights || (is_p && K == kForwardTurned) ? 64 : by_rows && lines < kTileP ? kBox : kTileP;
-    for (int b = 0; b < tile.blocks; b += run_of(K)) {
-      if (!ready)
-        ok = wait(&sh.empty[s.at], s.parity ^ 1, sh);
+      expected += eight(K) ? (boxed(tile.rows - tile.p - kTileP) + lines_q) * 128 : landing;
+    expected = uniform(expected);
+    const int lines = uniform(IS_P ? lines_p : lines_q);
+    const bool whole = kByRows && lines == kTileP;
+    const int box = K == kWeights || (IS_P && K == kForwardTurned) ? 64 : kByRows && !whole ? kBox : kTileP;
+    const int first = uniform((IS_P ? tile.p + me * kTileP : tile.q + me * width) + (kByRows ? tile.row : 0));
+    const int row = uniform(tile.row), expert = uniform(kByRows ? 0 : tile.expert), blocks = uniform(tile.blocks);
+    const int end = K == kWeights && tile.rows % kDepth != 0 ? blocks - 1 : blocks; // kWeights: the block with last rows
+    for (int b = 0; b < blocks; ++b) {
+      if (!__all_sync(kAll, ready))
+        ok = wait(empty + s.at * 8, s.parity ^ 1, sh);
       if (!ok)
         break;
-      const int n = min(run_of(K), tile.blocks - b);
-      char* const to = stages + s.at * stage_bytes(K) + (is_p ? 0 : kBytesP);
-      uint32_t bar = at_first<K>(&sh.full[s.at]);
-      if (K == kWeights && (b + n) * kDepth > tile.rows) {
-        // an expert's last rows: each block of the pair first takes out those of others
-        if (is_p && me == 0)
-          arrive(bar);
-        bar = smem_addr(&sh.end_full[s.at]);
-        if (is_p)
-          mbar_arrive_expect_tx(&sh.end_full[s.at], (lines_p + lines_q) * 128 * n);
-      } else if (is_p && me == 0) {
-        mbar_arrive_expect_tx(&sh.full[s.at], expected * 128 * n);
+      uint32_t bar = full + s.at * 8;
+      const uint32_t at = to + s.at * stage_bytes(K);
+      if (K == kWeights && b == end) {
+        // each block of the pair first takes out the rows of others
+        if (IS_P) {
+          if (me == 0 && on)
+            arrive(bar);
+          expect(on, smem_addr(&sh.end_full[0]) + s.at * 8, landing);
+        }
+        bar = smem_addr(&sh.end_full[0]) + s.at * 8;
+      } else if (IS_P && me == 0) {
+        expect(on, bar, expected);
       }
       used = min(used + 1, kStages);
       s.next();
-      ready = over(&sh.empty[s.at], s.parity ^ 1);
-      for (int j = 0; j < n; ++j) {
-        char* const block = to + j * block_bytes(K);
-        for (int i = 0; i < lines; i += box) {
-          if constexpr (K == kWeights)
-            tile_load<true>(block + i * 128, &from, first + i, tile.row + (b + j) * kDepth, 0, bar);
-          else if (K == kForwardTurned && is_p)
-            tile_load<true>(block + i * 128, &from, first + i, (b + j) * kDepth, tile.expert, bar);
-          else
-            tile_load<pair(K)>(block + i * 128, &from, (b + j) * (eight(K) ? 128 : 64), (by_rows ? tile.row : 0) + first + i,
-                               by_rows ? 0 : tile.expert, bar);
-        }
+      ready = over(empty + s.at * 8, s.parity ^ 1);
+      if constexpr (K == kWeights) {
+        for (int i = 0; i < lines; i += 64)
+          tile_load<true>(on, at + i * 128, &map, first + i, row + b * kDepth, 0, bar);
+      } else if constexpr (K == kForwardTurned && IS_P) {
+#pragma unroll
+        for (int i = 0; i < kTileP; i += 64)
+          tile_load<true>(on, at + i * 128, &map, first + i, b * kDepth, expert, bar);
+      } else if (whole) {
+        tile_load<pair(K)>(on, at, &large, b * (eight(K) ? 128 : 64), first, 0, bar);
+      } else {
+        for (int i = 0; i < lines; i += box)
+          tile_load<pair(K)>(on, at + i * 128, &map, b * (eight(K) ? 128 : 64), first + i, expert, bar);
       }
     }
   }
-  if (!ok && is_p && me == 0) {
+  if (!ok && IS_P && me == 0) {
     // what is under way lands before the blocks end (a second each at most)
     for (int i = 0; i < used; ++i) {
       s.at = s.at == 0 ? kStages - 1 : s.at - 1;
@@ -468,99 +503,85 @@ __device__ void clear_ends(const Sizes& z, char* stages, Control& sh)
 {
   constexpr Kind K = kWeights;
   const int lane = threadIdx.x & 31, tiles = sh.tile_start[z.experts];
-  Ring<stages_of(K)> s;
+  int stage = 0;
   uint32_t before = 0; // a bit for each stage: the parity of its last blocks of rows
   for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2) {
     const Tile tile = tile_at<K>(t, z, sh);
     const int copies = 2 + pieces(pieces(tile.width, kStepQ) * kStepQ / 2, 64), left = tile.rows % kDepth;
-    for (int b = 0; b < tile.blocks; b += run_of(K)) {
-      const int n = min(run_of(K), tile.blocks - b);
-      if (left != 0 && b + n == tile.blocks) {
-        if (!__all_sync(kAll, wait(&sh.end_full[s.at], before >> s.at & 1, sh)))
-          return;
-        before ^= 1u << s.at;
-        char* const block = stages + s.at * stage_bytes(K) + (n - 1) * block_bytes(K);
-        for (int i = 0; i < copies; ++i)
-          for (int at = left * 128 + lane * 16; at < kDepth * 128; at += 512)
-            *reinterpret_cast<uint4*>(block + i * kDepth * 128 + at) = uint4{};
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0)
-          arrive(at_first<K>(&sh.end_ready[s.at]));
-      }
-      s.next();
-    }
+    stage += tile.blocks;
+    if (left == 0)
+      continue;
+    const int at = (stage - 1) % stages_of(K);
+    if (!wait(&sh.end_full[at], before >> at & 1, sh))
+      return;
+    before ^= 1u << at;
+    for (int i = 0; i < copies; ++i)
+      for (int byte = left * 128 + lane * 16; byte < kDepth * 128; byte += 512)
+        *reinterpret_cast<uint4*>(stages + at * stage_bytes(K) + i * kDepth * 128 + byte) = uint4{};
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0)
+      arrive(at_first<K>(&sh.end_ready[at]));
   }
 }
 
-// One thread, of a pair's first block: the products of the blocks that have
-// landed. It alone, since the tensor cores are as fast as it can issue: with a
-// warp that agrees on every wait it took 730 cycles for a block of 512.
+// One warp, of a pair's first block: the products of the blocks that have
+// landed.
 template <Kind K>
 __device__ void issue_products(const Sizes& z, char* stages, Control& sh)
 {
-  constexpr int kRun = run_of(K);
-  const int tiles = sh.tile_start[z.experts];
-  const uint32_t tmem = sh.tmem;
+  const int tiles = uniform(sh.tile_start[z.experts]);
+  const uint32_t on = elected(), tmem = uniform(sh.tmem);
   const uint64_t p0 = operand<p_by_rows(K)>(smem_addr(stages)), q0 = operand<q_by_rows(K)>(smem_addr(stages) + kBytesP);
+  const uint32_t full = smem_addr(&sh.full[0]), empty = smem_addr(&sh.empty[0]), sums_full = smem_addr(&sh.sums_full[0]),
+                 sums_empty = smem_addr(&sh.sums_empty[0]);
   Ring<stages_of(K)> s;
   Ring<2> d;
   uint32_t ends_before = 0;
   bool ok = true, ready = false, sums_ready = false;
   for (int t = blockIdx.x / blocks_of(K); ok && t < tiles; t += gridDim.x / blocks_of(K)) {
     const Tile tile = tile_at<K>(t, z, sh);
-    const uint32_t instruction = z.instruction | (uint32_t)(pieces(tile.width, kStepQ) * kStepQ / 8) << 17;
-    if (!eight(K) && tile.blocks > 0)
-      ok = sums_ready || wait(&sh.sums_empty[d.at], d.parity ^ 1, sh);
-    for (int b = 0; ok && b < tile.blocks; b += kRun) {
-      const int n = min(kRun, tile.blocks - b);
-      if (!ready)
-        ok = wait(&sh.full[s.at], s.parity, sh);
-      if (K == kWeights && ok && b + n == tile.blocks && tile.rows % kDepth != 0) {
-        ok = wait(&sh.end_ready[s.at], ends_before >> s.at & 1, sh);
+    const uint32_t instruction = uniform((int)(z.instruction | (uint32_t)(pieces(tile.width, kStepQ) * kStepQ / 8) << 17));
+    const int blocks = uniform(tile.blocks);
+    const int end = uniform(K == kWeights && tile.rows % kDepth != 0 ? blocks - 1 : blocks);
+    for (int b = 0; b < blocks; ++b) {
+      // the sums of one block, or of all
+      const bool first = eight(K) || b == 0, last = eight(K) || b == blocks - 1;
+      if (first && !__all_sync(kAll, sums_ready))
+        ok = wait(sums_empty + d.at * 8, d.parity ^ 1, sh);
+      if (ok && !__all_sync(kAll, ready))
+        ok = wait(full + s.at * 8, s.parity, sh);
+      if (K == kWeights && ok && b == end) {
+        ok = wait(smem_addr(&sh.end_ready[0]) + s.at * 8, ends_before >> s.at & 1, sh);
         ends_before ^= 1u << s.at;
       }
       if (!ok)
         break;
       fence_after_sync();
-      const uint32_t stage = s.at * (stage_bytes(K) / 16);
-      uint64_t* const empty = &sh.empty[s.at];
+      const uint64_t p = p0 + s.at * (stage_bytes(K) / 16), q = q0 + s.at * (stage_bytes(K) / 16);
+      const uint32_t sums = tmem + d.at * kTileQ, free = empty + s.at * 8, done = sums_full + d.at * 8;
       s.next();
-      ready = over(&sh.full[s.at], s.parity);
-#pragma unroll
-      for (int j = 0; j < kRun; ++j) {
-        if (j > 0 && j >= n)
-          break;
-        if constexpr (eight(K)) { // each block has sums of its own
-          ok = sums_ready || wait(&sh.sums_empty[d.at], d.parity ^ 1, sh);
-          if (!ok)
-            break;
-          fence_after_sync();
-        }
-        const uint64_t p = p0 + stage + j * (block_bytes(K) / 16), q = q0 + stage + j * (block_bytes(K) / 16);
-        // four products: 32 bytes of c on, or 16 rows of 128 bytes
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          multiply<K>(tmem + d.at * kTileQ, p + i * (p_by_rows(K) ? 2 : 128), q + i * (q_by_rows(K) ? 2 : 128), instruction,
-                      eight(K) ? i > 0 : b > 0 || j > 0 || i > 0);
-        if constexpr (eight(K)) {
-          commit<pair(K)>(&sh.sums_full[d.at]);
-          d.next();
-          sums_ready = over(&sh.sums_empty[d.at], d.parity ^ 1);
-        }
+      ready = over(full + s.at * 8, s.parity);
+      if (last) {
+        d.next();
+        sums_ready = over(sums_empty + d.at * 8, d.parity ^ 1);
       }
-      commit<pair(K)>(empty);
-    }
-    if (!eight(K) && ok && tile.blocks > 0) {
-      commit<pair(K)>(&sh.sums_full[d.at]);
-      d.next();
-      sums_ready = over(&sh.sums_empty[d.at], d.parity ^ 1);
+      // four products: 32 bytes of c on, or 16 rows of 128 bytes
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        multiply<K>(on, sums, p + i * (p_by_rows(K) ? 2 : 128), q + i * (q_by_rows(K) ? 2 : 128), instruction,
+                    !first || i > 0);
+      commit<pair(K)>(on, free);
+      if (last)
+        commit<pair(K)>(on, done);
     }
   }
   if (!ok) {
-    commit<pair(K)>(&sh.drained); // what is under way ends before the blocks do
-    mbar_wait(&sh.drained, 0);
+    commit<pair(K)>(on, smem_addr(&sh.drained)); // what is under way ends before the blocks do
+    if (on)
+      mbar_wait(&sh.drained, 0);
   }
+  __syncwarp();
 }
 
 // kSumWarps warps, 8-bit operands: each block's sums times their scales. A
@@ -588,7 +609,7 @@ __device__ void add_scaled(const Sizes& z, O* out, Control& sh)
       const float2 f = make_float2(scale, scale);
       if (on && b + 1 < tile.blocks)
         scale = by_row[b + 1] * by_weight[b + 1];
-      if (!__all_sync(kAll, wait(&sh.sums_full[d.at], d.parity, sh)))
+      if (!wait(&sh.sums_full[d.at], d.parity, sh))
         return;
       fence_after_sync();
       const uint32_t from = lanes + d.at * kTileQ + start;
@@ -654,7 +675,7 @@ __device__ void write_sums(const Sizes& z, O* out, Control& sh)
     O* at = out + (row + start) * z.out_stride + p;
     const bool any = tile.blocks > 0; // none: an expert without rows has a gradient of zeros
     if (any) {
-      if (!__all_sync(kAll, wait(&sh.sums_full[d.at], d.parity, sh)))
+      if (!wait(&sh.sums_full[d.at], d.parity, sh))
         return;
       fence_after_sync();
     }
@@ -728,11 +749,12 @@ product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant_
   if (warp < kThreads / 32 - kSumWarps) {
     if constexpr (eight(K))
       asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 0 || warp == 3) {
-      if (lane == 0)
-        copy_operands<K>(warp == 0, warp == 0 ? p_map : q_map, large, z, stages, sh);
+    if (warp == 0) {
+      copy_operands<K, true>(p_map, large, z, stages, sh);
+    } else if (warp == 3) {
+      copy_operands<K, false>(q_map, large, z, stages, sh);
     } else if (warp == 1) {
-      if (lane == 0 && rank<K>() == 0)
+      if (rank<K>() == 0)
         issue_products<K>(z, stages, sh);
     } else if (K == kWeights && warp == 2) {
       clear_ends(z, stages, sh);
