@@ -815,7 +815,8 @@ Encode encoder()
 }
 
 // Matrices of `rows` rows of `width` elements of `size` bytes, `count` of
-// them, in boxes of 128 bytes by `box` rows; zeros are read past the ends.
+// them, in boxes of 128 bytes by `box` rows; zeros are read past the ends. The
+// distance of a single one says nothing, but is described too.
 cudaError_t describe(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base, int64_t width, int64_t rows,
                      int64_t count, int64_t row_stride, int64_t stride, int box)
 {
@@ -926,11 +927,14 @@ extern "C" int segtopk_expert_matmul(segtopk_dtype dtype, const void* rows, int6
   int rc = check_sizes(num_rows, width, out_width, experts);
   if (rc == SEGTOPK_ERROR_INVALID_VALUE || dtype < SEGTOPK_F16 || dtype > SEGTOPK_I32 || out_dtype < SEGTOPK_F16 ||
       out_dtype > SEGTOPK_I32 || (in_stride != 1 && out_stride != 1) || row_stride < width ||
-      (in_stride == 1 && out_width > 1 ? out_stride < width : false) ||
-      (in_stride != 1 && in_stride < out_width) || expert_stride < 0)
+      (in_stride == 1 ? out_width > 1 && out_stride < width : in_stride < out_width) ||
+      (rc == SEGTOPK_SUCCESS && experts > 1 && expert_stride < width * out_width))
     return SEGTOPK_ERROR_INVALID_VALUE;
   const bool turned = in_stride != 1;
-  const int64_t line = turned ? in_stride : out_stride; // between rows of the weights in memory
+  // between rows of the weights in memory, and matrices; those of one say nothing
+  const int64_t line = turned ? in_stride : out_width > 1 ? out_stride : width;
+  if (experts == 1)
+    expert_stride = line;
   if (rc != SEGTOPK_SUCCESS || (dtype != SEGTOPK_F16 && dtype != SEGTOPK_BF16) || !float_type_of(out_dtype) ||
       width % 8 != 0 || (turned && out_width % 8 != 0) || row_stride > kMaxStride || line > kMaxStride ||
       expert_stride > kMaxStride || forward_tiles(num_rows, kTileQ, out_width, kTileP, experts) > kMaxTiles)
@@ -949,9 +953,9 @@ extern "C" int segtopk_expert_matmul(segtopk_dtype dtype, const void* rows, int6
   cudaError_t e = turned ? describe(&p, map_type(dtype), 2, weights, out_width, width, experts, line, expert_stride, kDepth)
                          : describe(&p, map_type(dtype), 2, weights, width, out_width, experts, line, expert_stride, kTileP);
   if (e == cudaSuccess)
-    e = describe(&q, map_type(dtype), 2, rows, width, num_rows, 1, row_stride, num_rows * row_stride, kBox);
+    e = describe(&q, map_type(dtype), 2, rows, width, num_rows, 1, row_stride, row_stride, kBox);
   if (e == cudaSuccess)
-    e = describe(&large, map_type(dtype), 2, rows, width, num_rows, 1, row_stride, num_rows * row_stride, kTileP);
+    e = describe(&large, map_type(dtype), 2, rows, width, num_rows, 1, row_stride, row_stride, kTileP);
   if (e != cudaSuccess)
     return record_cuda_error(e);
   Sizes z = {};
@@ -978,16 +982,19 @@ extern "C" int segtopk_expert_matmul_f8(const void* rows, int64_t num_rows, int6
   record_launch_count(0);
   int rc = check_sizes(num_rows, width, out_width, experts);
   if (rc == SEGTOPK_ERROR_INVALID_VALUE || out_dtype < SEGTOPK_F16 || out_dtype > SEGTOPK_I32 || row_stride < width ||
-      (out_width > 1 && out_stride < width) || expert_stride < 0 || scale_stride < 0)
+      (out_width > 1 && out_stride < width) || (rc == SEGTOPK_SUCCESS && experts > 1 && expert_stride < width * out_width) || scale_stride < 0)
     return SEGTOPK_ERROR_INVALID_VALUE;
+  const int64_t line = out_width > 1 ? out_stride : width;
+  if (experts == 1)
+    expert_stride = line;
   if (rc != SEGTOPK_SUCCESS || !float_type_of(out_dtype) || width % 16 != 0 || row_stride > kMaxStride ||
-      out_stride > kMaxStride || expert_stride > kMaxStride || forward_tiles(num_rows, kTileP, out_width, kTileP, experts) > kMaxTiles)
+      line > kMaxStride || expert_stride > kMaxStride || forward_tiles(num_rows, kTileP, out_width, kTileP, experts) > kMaxTiles)
     return SEGTOPK_ERROR_NOT_SUPPORTED;
   if (num_rows == 0)
     return SEGTOPK_SUCCESS;
   if (!rows || !row_scales || !weights || !weight_scales || !offsets || !out)
     return SEGTOPK_ERROR_INVALID_VALUE;
-  if (!tma_fits(rows, row_stride, 1) || !tma_fits(weights, out_stride, 1) || expert_stride % 16 != 0 ||
+  if (!tma_fits(rows, row_stride, 1) || !tma_fits(weights, line, 1) || expert_stride % 16 != 0 ||
       !aligned(offsets, 8) || !aligned(row_scales, 4) || !aligned(weight_scales, 4) ||
       !aligned(out, out_dtype == SEGTOPK_F32 ? 4 : 2))
     return SEGTOPK_ERROR_MISALIGNED;
@@ -996,12 +1003,12 @@ extern "C" int segtopk_expert_matmul_f8(const void* rows, int64_t num_rows, int6
     return rc;
   CUtensorMap p, q, large = {};
   cudaError_t e = describe(&p, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, width, num_rows, 1, row_stride,
-                           num_rows * row_stride, kBox);
+                           row_stride, kBox);
   if (e == cudaSuccess)
-    e = describe(&large, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, width, num_rows, 1, row_stride, num_rows * row_stride,
+    e = describe(&large, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, width, num_rows, 1, row_stride, row_stride,
                  kTileP);
   if (e == cudaSuccess)
-    e = describe(&q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, weights, width, out_width, experts, out_stride, expert_stride,
+    e = describe(&q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, weights, width, out_width, experts, line, expert_stride,
                  kTileP);
   if (e != cudaSuccess)
     return record_cuda_error(e);
@@ -1057,9 +1064,9 @@ extern "C" int segtopk_expert_matmul_weights(segtopk_dtype dtype, const void* a_
     return e == cudaSuccess ? SEGTOPK_SUCCESS : record_cuda_error(e);
   }
   CUtensorMap p, q, large = {};
-  cudaError_t e = describe(&p, map_type(dtype), 2, b_rows, b_width, num_rows, 1, b_stride, num_rows * b_stride, kDepth);
+  cudaError_t e = describe(&p, map_type(dtype), 2, b_rows, b_width, num_rows, 1, b_stride, b_stride, kDepth);
   if (e == cudaSuccess)
-    e = describe(&q, map_type(dtype), 2, a_rows, a_width, num_rows, 1, a_stride, num_rows * a_stride, kDepth);
+    e = describe(&q, map_type(dtype), 2, a_rows, a_width, num_rows, 1, a_stride, a_stride, kDepth);
   if (e != cudaSuccess)
     return record_cuda_error(e);
   Sizes z = {};

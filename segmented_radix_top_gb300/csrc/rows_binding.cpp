@@ -507,7 +507,7 @@ Matrices matrices(const at::Tensor& given)
   const int64_t line = m.turned() ? m.in_stride : m.out_stride;
   const bool fits = (m.in_stride == 1 ? m.out_stride >= k : m.out_stride == 1 && m.in_stride >= n) &&
                     reinterpret_cast<uintptr_t>(t.const_data_ptr()) % 16 == 0 && line * size % 16 == 0 &&
-                    m.expert_stride * size % 16 == 0;
+                    m.expert_stride * size % 16 == 0 && m.expert_stride >= n * k;
   return fits ? m : view(t.clone(at::MemoryFormat::Contiguous));
 }
 
