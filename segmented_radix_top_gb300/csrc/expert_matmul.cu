@@ -71,6 +71,7 @@ struct Control {
   int part[kThreads / 32];
   int tile_start[kMaxExperts + 1];              // experts' first tiles
   int row_start[kMaxExperts + 1];               // and rows
+  uint4 staging[kSumWarps][32 * 4];             // 8 bits: 64 bytes of a warp's rows on their way to memory
 };
 constexpr size_t kShared = 1024 + (size_t)kOperandBytes + sizeof(Control);
 static_assert(kShared <= 227 * 1024, "shared memory of a block");
@@ -82,7 +83,7 @@ struct Sizes {
   int step;             // kForward8: the tiles' q
   uint32_t instruction; // types and majors of the operands
   int64_t out_stride;   // between rows of the result, which are dense
-  int out_bytes;        // of a row of the result that can be written at a time
+  bool out_vectors;     // 8 bits: its rows can be written 16 bytes at a time
   const float* row_scales;
   int64_t scale_stride;
   const float* weight_scales;
@@ -300,35 +301,49 @@ __device__ __forceinline__ int parts_q(int rows, const Sizes& z)
   return eight(K) ? pieces(z.q, z.step) : pieces(K == kWeights ? z.q : rows, kTileQ);
 }
 
+// a / b, rounded down, for a >= 0 and b > 0: by a product in 32 bits, which is
+// at most one off where the quotient is below 2^22, and a step.
+__device__ __forceinline__ int divide(int a, int b)
+{
+  if (a >= 1 << 22)
+    return a / b;
+  int q = (int)((float)a * __frcp_rn((float)b));
+  const int rest = a - q * b;
+  q += rest >= b ? 1 : rest < 0 ? -1 : 0;
+  return q;
+}
+__device__ __forceinline__ int divide_up(int a, int b) { return divide(a + b - 1, b); }
+
+// Tile t, by a whole warp, which finds its expert in two looks: among every
+// 32nd, then the 32 after that.
 template <Kind K>
 __device__ __forceinline__ Tile tile_at(int t, const Sizes& z, const Control& sh)
 {
-  int low = 0, high = z.experts; // tile_start[low] <= t < tile_start[high]
-  while (high - low > 1) {
-    const int mid = (low + high) / 2;
-    if (sh.tile_start[mid] <= t)
-      low = mid;
-    else
-      high = mid;
-  }
+  static_assert(kMaxExperts <= 32 * 32);
+  const int lane = threadIdx.x & 31;
+  const int far = (lane + 1) * 32;
+  const int base = 32 * __popc(__ballot_sync(kAll, far < z.experts && sh.tile_start[min(far, kMaxExperts)] <= t));
+  const int near = base + lane;
+  const int low = base + __popc(__ballot_sync(kAll, near < z.experts && sh.tile_start[min(near + 1, kMaxExperts)] <= t));
   Tile r;
   r.expert = low;
   r.row = sh.row_start[low];
   r.rows = sh.row_start[low + 1] - r.row;
   const int i = t - sh.tile_start[low];
   if constexpr (eight(K)) {
-    const int parts = parts_p<K>(r.rows, z);
-    r.p = i % parts * tile_p(K);
-    r.q = i / parts * z.step;
+    const int parts = parts_p<K>(r.rows, z), q = divide(i, parts);
+    r.p = (i - q * parts) * tile_p(K);
+    r.q = q * z.step;
     r.width = min(z.step, z.q - r.q);
     r.blocks = pieces(z.c, 128);
   } else {
     const int q = K == kWeights ? z.q : r.rows;
     const int parts = parts_q<K>(r.rows, z);
-    const int step = pieces(pieces(q, parts), kStepQ) * kStepQ;
-    r.q = i % parts * step;
+    const int step = pieces(divide_up(q, parts), kStepQ) * kStepQ;
+    const int p = divide(i, parts);
+    r.q = (i - p * parts) * step;
     r.width = min(step, q - r.q);
-    r.p = i / parts * tile_p(K);
+    r.p = p * tile_p(K);
     r.blocks = K == kWeights ? pieces(r.rows, kDepth) : pieces(z.c, 64);
   }
   return r;
@@ -351,8 +366,11 @@ __device__ int before_this_thread(int value, Control& sh, F&& join)
   const int previous = __shfl_up_sync(kAll, all, 1);
   __syncthreads();
   int before = lane > 0 ? previous : 0;
-  for (int w = 0; w < threadIdx.x / 32; ++w)
-    before = join(before, sh.part[w]);
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) { // all are read at once
+    const int part = sh.part[w];
+    before = w < threadIdx.x / 32 ? join(before, part) : before;
+  }
   __syncthreads();
   return before;
 }
@@ -438,7 +456,7 @@ __device__ void copy_operands(const CUtensorMap& map, const CUtensorMap& large, 
     const bool whole = kByRows && lines == kTileP;
     const int box = K == kWeights || (IS_P && K == kForwardTurned) ? 64 : kByRows && !whole ? kBox : kTileP;
     const int first = uniform((IS_P ? tile.p + me * kTileP : tile.q + me * width) + (kByRows ? tile.row : 0));
-    const int row = uniform(tile.row), expert = uniform(kByRows ? 0 : tile.expert), blocks = uniform(tile.blocks);
+    const int row = uniform(tile.row), matrix = uniform(kByRows ? 0 : tile.expert), blocks = uniform(tile.blocks);
     const int end = K == kWeights && tile.rows % kDepth != 0 ? blocks - 1 : blocks; // kWeights: the block with last rows
     for (int b = 0; b < blocks; ++b) {
       if (!__all_sync(kAll, ready))
@@ -467,12 +485,12 @@ __device__ void copy_operands(const CUtensorMap& map, const CUtensorMap& large, 
       } else if constexpr (K == kForwardTurned && IS_P) {
 #pragma unroll
         for (int i = 0; i < kTileP; i += 64)
-          tile_load<true>(on, at + i * 128, &map, first + i, b * kDepth, expert, bar);
+          tile_load<true>(on, at + i * 128, &map, first + i, b * kDepth, matrix, bar);
       } else if (whole) {
         tile_load<pair(K)>(on, at, &large, b * (eight(K) ? 128 : 64), first, 0, bar);
       } else {
         for (int i = 0; i < lines; i += box)
-          tile_load<pair(K)>(on, at + i * 128, &map, b * (eight(K) ? 128 : 64), first + i, expert, bar);
+          tile_load<pair(K)>(on, at + i * 128, &map, b * (eight(K) ? 128 : 64), first + i, matrix, bar);
       }
     }
   }
@@ -574,37 +592,50 @@ __device__ void issue_products(const Sizes& z, char* stages, Control& sh)
   __syncwarp();
 }
 
-// A lane's `columns` of N values, neighbours in memory, from `to` on: `bytes`
-// (32, a whole sector of the memory, 16, or those of one value) at a time,
-// which `to` and the columns are multiples of.
+// A warp's 32 rows, one a lane, of `columns` values to memory, `stride` apart
+// from `to` on; the first `rows` of them. With rows on 16-byte boundaries they
+// pass through shared memory 64 bytes at a time, so that four lanes write them
+// together: a store whose lanes write to a row each takes 32 cycles of an SM's
+// memory pipe, and with 16 bytes a lane a tile's took longer than four of its
+// blocks' products.
 template <class O, int N, class F>
-__device__ __forceinline__ void write_row(O* to, int columns, int bytes, F&& sum)
+__device__ __forceinline__ void write_rows(O* to, int64_t stride, int rows, int columns, bool vectors, uint4* staging, F&& sum)
 {
-  auto by = [&](auto size) {
-    constexpr int V = decltype(size)::value / (int)sizeof(O);
+  const int lane = threadIdx.x & 31;
+  if (vectors) { // columns is a multiple of V
+    constexpr int V = 16 / (int)sizeof(O);
+    const int unit = lane & 3;
+    auto place = [](int row, int u) { return row * 4 + (u ^ (row >> 1 & 3)); }; // eight lanes in different banks
 #pragma unroll
-    for (int c = 0; c < N; c += V)
-      if (c < columns) {
+    for (int c = 0; c < N; c += 4 * V) {
+      if (c >= columns)
+        break;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
         float x[V];
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          x[i] = sum(c + i);
+          x[i] = sum(c + u * V + i);
         Vec<O, V> v;
         v.set(x);
-        if constexpr (V * sizeof(O) == 32)
-          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + c), "r"(v.w[0]),
-                       "r"(v.w[1]), "r"(v.w[2]), "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]), "r"(v.w[7])
-                       : "memory");
-        else
-          store<O, V>(to + c, v);
+        staging[place(lane, u)] = *reinterpret_cast<const uint4*>(&v);
       }
-  };
-  if (bytes == 32)
-    by(std::integral_constant<int, 32>{});
-  else if (bytes == 16)
-    by(std::integral_constant<int, 16>{});
-  else
-    by(std::integral_constant<int, (int)sizeof(O)>{});
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = j * 8 + lane / 4;
+        const uint4 v = staging[place(row, unit)];
+        if (row < rows && c + unit * V < columns)
+          *reinterpret_cast<uint4*>(to + row * stride + c + unit * V) = v;
+      }
+      __syncwarp();
+    }
+  } else if (lane < rows) {
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+      if (c < columns)
+        to[lane * stride + c] = from_f32<O>(sum(c));
+  }
 }
 
 // kSumWarps warps, 8-bit operands: each block's sums times their scales. A
@@ -647,16 +678,19 @@ __device__ void add_scaled(const Sizes& z, O* out, Control& sh)
           sum[c * 32 + i] =
             __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f, sum[c * 32 + i]);
       }
+      // (said right after the second load, before its products, this took 9 %
+      // more: registers were spilled)
       fence_before_sync();
       __syncwarp();
       if (lane == 0)
         arrive(at_first<K>(&sh.sums_empty[d.at]));
       d.next();
     }
-    if (on) {
-      O* const to = out + (int64_t)(tile.row + row) * z.out_stride + tile.q + start;
-      write_row<O, 128>(to, min(128, columns), z.out_bytes, [&](int i) { return i & 1 ? sum[i / 2].y : sum[i / 2].x; });
-    }
+    const int first = row - lane; // of the warp
+    if (columns > 0 && first < tile.rows)
+      write_rows<O, 128>(out + (int64_t)(tile.row + first) * z.out_stride + tile.q + start, z.out_stride, tile.rows - first,
+                         min(128, columns), z.out_vectors, sh.staging[warp],
+                         [&](int i) { return i & 1 ? sum[i / 2].y : sum[i / 2].x; });
   }
 }
 
@@ -720,6 +754,9 @@ product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant_
   Control& sh = *reinterpret_cast<Control*>(stages + kOperandBytes);
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
 
+  if (threadIdx.x == 32)
+    for (const CUtensorMap* map : {&p_map, &q_map, &large})
+      asm volatile("prefetch.tensormap [%0];" ::"l"(map));
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&sh.full[i], 1);
@@ -882,14 +919,6 @@ CUtensorMapDataType map_type(int dtype)
   return dtype == SEGTOPK_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 
-int bytes_at_a_time(const void* out, int64_t width, size_t size)
-{
-  for (int bytes : {32, 16})
-    if (aligned(out, bytes) && width * size % bytes == 0)
-      return bytes;
-  return (int)size;
-}
-
 int check_sizes(int64_t num_rows, int64_t width, int64_t out_width, int32_t experts)
 {
   if (num_rows < 0 || width < 1 || out_width < 1 || experts < 1)
@@ -1030,7 +1059,7 @@ extern "C" int segtopk_expert_matmul_f8(const void* rows, int64_t num_rows, int6
   z.step = step;
   return with_float_type(out_dtype, [&](auto zero) {
     using O = decltype(zero);
-    z.out_bytes = bytes_at_a_time(out, out_width, sizeof(O));
+    z.out_vectors = rows_fit(out, out_width, out_width, sizeof(O), 16 / (int)sizeof(O));
     return by_pairs ? run<kForward8Pair, O>(p, q, large, offsets, z, out, sms, tiles, stream)
                     : run<kForward8, O>(p, q, large, offsets, z, out, sms, tiles, stream);
   });
