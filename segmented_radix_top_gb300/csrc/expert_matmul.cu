@@ -71,7 +71,7 @@ struct Control {
   int part[kThreads / 32];
   int tile_start[kMaxExperts + 1];              // experts' first tiles
   int row_start[kMaxExperts + 1];               // and rows
-  uint4 staging[kSumWarps][32 * 4];             // 8 bits: 64 bytes of a warp's rows on their way to memory
+  uint4 staging[kSumWarps][32 * 4];             // 64 bytes of 32 rows on their way to memory
 };
 constexpr size_t kShared = 1024 + (size_t)kOperandBytes + sizeof(Control);
 static_assert(kShared <= 227 * 1024, "shared memory of a block");
@@ -83,7 +83,7 @@ struct Sizes {
   int step;             // kForward8: the tiles' q
   uint32_t instruction; // types and majors of the operands
   int64_t out_stride;   // between rows of the result, which are dense
-  bool out_vectors;     // 8 bits: its rows can be written 16 bytes at a time
+  bool out_vectors;     // its rows can be written 16 bytes at a time
   const float* row_scales;
   int64_t scale_stride;
   const float* weight_scales;
@@ -694,10 +694,48 @@ __device__ void add_scaled(const Sizes& z, O* out, Control& sh)
   }
 }
 
+// A warp's 32 columns of a 16-bit result, of which a lane has 32 rows' values,
+// to memory, `stride` between rows: the first `rows` rows, `lanes` columns.
+// Pairs of rows pass through shared memory, so that four lanes write 64 bytes
+// of a row. Written by a store a row, two bytes a lane, a tile of 256 by 256
+// took 5400 cycles, as long as ten blocks' products.
+template <class O, class F>
+__device__ __forceinline__ void write_columns(O* to, int64_t stride, int rows, int lanes, uint4* staging, F&& sum)
+{
+  const int lane = threadIdx.x & 31, unit = lane & 3;
+  uint32_t* const words = reinterpret_cast<uint32_t*>(staging); // [pair of rows][column]: the values of both
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    Vec<O, 2> v;
+    v.set({sum(2 * k), sum(2 * k + 1)});
+    words[k * 32 + lane] = v.w[0];
+  }
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int k = j * 8 + lane / 4;
+    // eight columns' pairs, in an order that takes eight lanes to different banks
+    const uint4* const from = staging + k * 8 + unit * 2;
+    const uint4 x = from[k & 1], y = from[~k & 1];
+    const uint4 a = k & 1 ? y : x, b = k & 1 ? x : y;
+    if (unit * 8 < lanes) {
+      O* const at = to + 2 * k * stride + unit * 8;
+      if (2 * k < rows)
+        *reinterpret_cast<uint4*>(at) = {__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
+                                         __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410)};
+      if (2 * k + 1 < rows)
+        *reinterpret_cast<uint4*>(at + stride) = {__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
+                                                  __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632)};
+    }
+  }
+  __syncwarp();
+}
+
 // kSumWarps warps, 16-bit operands: sums to memory, where the neighbours of a
 // lane's value are the other lanes'. The weights' gradient with the operands
 // exchanged, so that a lane stores 16 bytes of a row of its own, took 302 us
-// instead of 237 (65536 rows of 128 experts, 2048x1024).
+// where a store of two bytes a lane took 237 (65536 rows of 128 experts,
+// 2048x1024).
 template <Kind K, class O>
 __device__ void write_sums(const Sizes& z, O* out, Control& sh)
 {
@@ -727,11 +765,17 @@ __device__ void write_sums(const Sizes& z, O* out, Control& sh)
       uint32_t v[64] = {};
       if (any)
         sums_load(v, from + c);
+      if (sizeof(O) == 2 && z.out_vectors) {
+        if constexpr (sizeof(O) == 2)
 #pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        if (c + i < left)
-          *at = from_f32<O>(__uint_as_float(v[i]));
-        at += z.out_stride;
+          for (int i = 0; i < 64; i += 32)
+            write_columns(at - lane + (c + i) * z.out_stride, z.out_stride, columns - c - i, z.p - (p - lane), sh.staging[warp],
+                          [&](int k) { return __uint_as_float(v[i + k]); });
+      } else {
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (c + i < left)
+            at[(c + i) * z.out_stride] = from_f32<O>(__uint_as_float(v[i]));
       }
     }
     if (any) {
@@ -997,6 +1041,7 @@ extern "C" int segtopk_expert_matmul(segtopk_dtype dtype, const void* rows, int6
   const int64_t tiles = forward_tiles(num_rows, kTileQ, out_width, kTileP, experts);
   return with_float_type(out_dtype, [&](auto zero) {
     using O = decltype(zero);
+    z.out_vectors = rows_fit(out, out_width, out_width, sizeof(O), 16 / (int)sizeof(O));
     return turned ? run<kForwardTurned, O>(p, q, large, offsets, z, out, sms, tiles, stream)
                   : run<kForward, O>(p, q, large, offsets, z, out, sms, tiles, stream);
   });
@@ -1106,6 +1151,8 @@ extern "C" int segtopk_expert_matmul_weights(segtopk_dtype dtype, const void* a_
   z.instruction = instruction(kWeights, dtype == SEGTOPK_BF16);
   z.out_stride = b_width;
   return with_float_type(out_dtype, [&](auto zero) {
-    return run<kWeights, decltype(zero)>(p, q, large, offsets, z, out, sms, tiles, stream);
+    using O = decltype(zero);
+    z.out_vectors = rows_fit(out, b_width, b_width, sizeof(O), 16 / (int)sizeof(O));
+    return run<kWeights, O>(p, q, large, offsets, z, out, sms, tiles, stream);
   });
 }
