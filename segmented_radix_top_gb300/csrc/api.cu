@@ -458,6 +458,12 @@ int record_cuda_error(cudaError_t e) { return cuda_fail(e); }
 // The rest of what an entry point of another translation unit shares (entry.h).
 void record_launch_count(int launches) { t_last_launch_count = launches; }
 
+void test_hooks(long long* wait_limit, uint32_t* extra_bytes)
+{
+  *wait_limit = g_wait_limit;
+  *extra_bytes = g_test_extra_tx;
+}
+
 int check_device(int* sms)
 {
   DeviceInfo dev;

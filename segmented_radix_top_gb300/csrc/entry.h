@@ -17,6 +17,11 @@ void record_launch_count(int launches);
 // GPU, else the status to return.
 int check_device(int* sms);
 
+// The bound of a wait in SM clock cycles, and the bytes that a test adds to
+// what the first copies are expected to bring (segtopk_set_test_hooks; 0 in
+// the ordinary build).
+void test_hooks(long long* wait_limit, uint32_t* extra_bytes);
+
 // Read and clear the device error words of the units that can set one
 // (synchronous).
 cudaError_t read_group_error(uint32_t* word);

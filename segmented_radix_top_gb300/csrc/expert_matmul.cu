@@ -68,6 +68,7 @@ struct Control {
   uint64_t drained;                             // products behind a wait that ran out
   uint32_t tmem;
   int failed;                                   // a wait ran out: everybody leaves
+  long long wait_limit;                         // cycles
   int part[kThreads / 32];
   int tile_start[kMaxExperts + 1];              // experts' first tiles
   int row_start[kMaxExperts + 1];               // and rows
@@ -87,6 +88,8 @@ struct Sizes {
   const float* row_scales;
   int64_t scale_stride;
   const float* weight_scales;
+  long long wait_limit; // of a wait, in cycles
+  int test_extra_bytes; // builds with test hooks: added to what a block's first copies are expected to bring
 };
 
 // ---------------------------------------------------------------------------
@@ -235,7 +238,7 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Control& sh)
   const long long start = clock64();
   bool failed = false;
   while (!__all_sync(kAll, try_wait(bar, parity))) {
-    if (clock64() - start > kWaitLimitCycles) {
+    if (clock64() - start > sh.wait_limit) {
       *(volatile int*)&sh.failed = 1;
       raise_error(kErrCopyTimeout);
     }
@@ -463,6 +466,11 @@ __device__ void copy_operands(const CUtensorMap& map, const CUtensorMap& large, 
         ok = wait(empty + s.at * 8, s.parity ^ 1, sh);
       if (!ok)
         break;
+#ifdef SEGTOPK_TEST_HOOKS
+      const int extra = used == 0 ? z.test_extra_bytes : 0;
+#else
+      constexpr int extra = 0;
+#endif
       uint32_t bar = full + s.at * 8;
       const uint32_t at = to + s.at * stage_bytes(K);
       if (K == kWeights && b == end) {
@@ -470,11 +478,11 @@ __device__ void copy_operands(const CUtensorMap& map, const CUtensorMap& large, 
         if (IS_P) {
           if (me == 0 && on)
             arrive(bar);
-          expect(on, smem_addr(&sh.end_full[0]) + s.at * 8, landing);
+          expect(on, smem_addr(&sh.end_full[0]) + s.at * 8, landing + extra);
         }
         bar = smem_addr(&sh.end_full[0]) + s.at * 8;
       } else if (IS_P && me == 0) {
-        expect(on, bar, expected);
+        expect(on, bar, expected + extra);
       }
       used = min(used + 1, kStages);
       s.next();
@@ -499,7 +507,7 @@ __device__ void copy_operands(const CUtensorMap& map, const CUtensorMap& large, 
     for (int i = 0; i < used; ++i) {
       s.at = s.at == 0 ? kStages - 1 : s.at - 1;
       s.parity ^= s.at == kStages - 1;
-      mbar_wait(&sh.full[s.at], s.parity);
+      mbar_wait(&sh.full[s.at], s.parity, sh.wait_limit);
     }
   }
 }
@@ -587,7 +595,7 @@ __device__ void issue_products(const Sizes& z, char* stages, Control& sh)
   if (!ok) {
     commit<pair(K)>(on, smem_addr(&sh.drained)); // what is under way ends before the blocks do
     if (on)
-      mbar_wait(&sh.drained, 0);
+      mbar_wait(&sh.drained, 0, sh.wait_limit);
   }
   __syncwarp();
 }
@@ -815,6 +823,7 @@ product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant_
     mbar_init(&sh.drained, 1);
     fence_mbar_init();
     sh.failed = 0;
+    sh.wait_limit = z.wait_limit;
   }
   if (warp == 2) {
     if constexpr (pair(K)) {
@@ -933,9 +942,12 @@ cudaError_t allow_shared()
 }
 
 template <Kind K, class O>
-int run(const CUtensorMap& p, const CUtensorMap& q, const CUtensorMap& large, const int64_t* offsets, const Sizes& z, void* out, int sms,
+int run(const CUtensorMap& p, const CUtensorMap& q, const CUtensorMap& large, const int64_t* offsets, Sizes z, void* out, int sms,
         int64_t most_tiles, void* stream)
 {
+  uint32_t extra;
+  test_hooks(&z.wait_limit, &extra);
+  z.test_extra_bytes = (int)extra;
   const cudaError_t e = allow_shared<K, O>();
   if (e != cudaSuccess)
     return record_cuda_error(e);
