@@ -2,28 +2,48 @@
 // (segtopk_expert_matmul, segtopk_expert_matmul_f8 and
 // segtopk_expert_matmul_weights in include/segtopk.h).
 //
-// All are products of tiles D[p, q] = sum_c P[p, c] Q[q, c], 128 values of p
-// by up to 256 of q, on the tensor cores (tcgen05, sums in TMEM in 32 bits):
+// All are products of tiles D[p, q] = sum_c P[p, c] Q[q, c] on the tensor cores
+// (tcgen05), whose sums are held in 32 bits in tensor memory (TMEM): a lane for
+// each p, a column for each q.
 //   forward         p an expert's outputs, q its rows, c the width
 //   rows' gradient  p an expert's inputs, q its rows, c the outputs: the
 //                   forward product with the weights read the other way round
 //   weights'        p and q an expert's inputs and outputs (the dense one of
 //                   the weights as p), c its rows
-// The weights are p even where there are few rows: a tile is as wide as the
-// expert's rows, in steps of 16, so one kernel serves 1 row and 10 000, and a
-// lane of the sums is a column of the result, whose 32 neighbours lie side by
-// side in memory.
+//   8 bits          p an expert's rows, q its outputs, c the width
+// In 16 bits the rows are q, since a tile may be any multiple of 32 of q wide:
+// experts have as many rows as the router gives them, and a tile no more than
+// that. In 8 bits the sum over one block of 128 values of c has one scale for
+// each row and one for the weights' tile, so each block's sums are taken out
+// of TMEM, multiplied and added up in registers in 32 bits; there the rows are
+// p, which gives a lane one factor for all its columns (the other way round,
+// with a factor a column from shared memory, a prefill took 3076 us instead of
+// 1222).
 //
-// Operands come by TMA in blocks of 128 bytes of c, a ring of four stages of
-// 48 KB. Warps have one part each: 0 copies, 1 issues products, 2 and 3 fetch
-// scales, 4 to 11 take the sums out of TMEM, which holds two sets of them, so
-// that they work while the next set is computed. Blocks stay on their SM and
-// take tile after tile; each finds the tiles from the experts' offsets, which
-// the host never reads.
+// Two blocks on neighbouring SMs share a tile of 256 p by up to 256 q (pair()):
+// each has half of p in its TMEM and copies half of q for both, which is what
+// the way from L2 to an SM carries in the time of the products (64 bytes a
+// cycle); one block alone on 128 p by 256 q needs half as much again. 8-bit
+// rows of which an expert has few go to single blocks.
 //
-// 8-bit operands: the sum over one block of 128 values of c has one scale for
-// each row and one for the weights' tile, so every block's sums are taken out
-// of TMEM, multiplied and added up in registers in 32 bits.
+// Operands come by TMA in blocks of 128 bytes of c, six of them under way (192
+// KB). Of a block's twelve warps one copies p, one q, one issues products and
+// eight take sums out of TMEM, which holds two sets of them, so that one is
+// taken out while the next is computed. Blocks stay on their SM and take tile
+// after tile; each finds its tiles from the experts' offsets, which the host
+// never reads.
+//
+// Measured on GB300 (through the Python API, results of the type of the rows):
+//   16 bits, 8192^3, one expert                604 us, 1820 TFLOP/s (cuBLAS 545)
+//   16 bits, 65536 rows of 128 experts, 2048x1024   190 us forward, 193 the
+//     rows' gradient, 222 the weights'
+//   8 bits, 131072 rows of 128 experts, 4096x2048   975 us, 2257 TFLOP/s
+//   8 bits, 64 rows of 64 experts, 2048x1024         17 us (decode)
+// A block of the main loop takes 518 cycles of the tensor cores' 512 in the
+// first; the clock is then at 1.45 GHz of 2.07 by the GPU's power limit. In 8
+// bits it takes 920: the sums' way from TMEM to registers, a wait of some
+// hundred cycles for every load of it, is what bounds it. With few rows the
+// weights' bytes do.
 #include <atomic>
 #include <cuda.h>
 
@@ -43,7 +63,7 @@ constexpr int kMaxStages = 6;
 constexpr int kBytesP = kTileP * 128;
 constexpr int kBox = 32;         // rows of one copy of few of an expert's rows
 constexpr int kDepth = 64;       // rows of one copy where c runs over rows
-constexpr int kStepQ = 32;       // 16 for each block of a pair
+constexpr int kStepQ = 32;       // of a tile's width: 16 for each block of a pair
 constexpr int kMaxExperts = SEGTOPK_MAX_EXPERTS;
 
 enum Kind { kForward8, kForward8Pair, kForward, kForwardTurned, kWeights };
@@ -81,7 +101,7 @@ struct Sizes {
   int64_t num_rows;     // slots; those from the last offset on have no expert
   int experts;
   int p, q, c;          // sizes; an expert's rows take the place of one
-  int step;             // kForward8: the tiles' q
+  int step;             // 8 bits: the tiles' q
   uint32_t instruction; // types and majors of the operands
   int64_t out_stride;   // between rows of the result, which are dense
   bool out_vectors;     // its rows can be written 16 bytes at a time

@@ -354,57 +354,67 @@ __device__ __forceinline__ float max_nan(float x, float y)
   return m;
 }
 
-// Eight values a thread, 16 threads a block of values. STEPS blocks, kThreads
-// * 8 values apart in the list of all rows' blocks, are under way at once.
+// Eight values a thread, 16 threads a block of values. STEPS of them are read
+// before the first is used and stay in the type they came in until then.
+// 131072 rows of 4096 in bf16: 260 us, 240 at the copy rate; 282 when all were
+// widened to 32 bits at once.
 template <class T, bool VECTOR, int STEPS>
 __global__ void __launch_bounds__(kThreads)
-quantize_kernel(const T* x, int64_t x_stride, uint32_t blocks, uint32_t per_row, int width, uint8_t* values, float* scales)
+quantize_kernel(const T* x, int64_t x_stride, uint32_t blocks, uint32_t per_row, float per_row_inverse, int width,
+                uint8_t* values, float* scales)
 {
   wait_for_previous();
   allow_next();
   constexpr int kGroups = kThreads / 16;
   const int lane = threadIdx.x & 15;
   const uint32_t first = blockIdx.x * (kGroups * STEPS) + threadIdx.x / 16;
-  float v[STEPS][8];
+  struct Eight {
+    T v[8];
+  };
+  std::conditional_t<VECTOR, Vec<T, 8>, Eight> got[STEPS];
   uint32_t row[STEPS];
   int at[STEPS];
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
     const uint32_t b = first + i * kGroups;
-    row[i] = b / per_row;
-    at[i] = (int)(b - row[i] * per_row) * kBlock + (VECTOR ? lane * 8 : lane); // then 16 apart, side by side in a warp
+    // b / per_row: by a product, at most one off below 2^22, and a step
+    uint32_t r = b >> 22 ? b / per_row : (uint32_t)((float)b * per_row_inverse);
+    const int32_t rest = (int32_t)(b - r * per_row);
+    r += rest < 0 ? -1 : rest >= (int32_t)per_row ? 1 : 0;
+    row[i] = r;
+    at[i] = (int)(b - r * per_row) * kBlock + (VECTOR ? lane * 8 : lane); // then 16 apart, side by side in a warp
     const bool in = b < blocks;
-    const T* from = x + (int64_t)row[i] * x_stride + at[i];
+    const T* from = x + (int64_t)r * x_stride + at[i];
     if constexpr (VECTOR) {
-      if (in && at[i] < width) { // width is a multiple of 8
-        const Vec<T, 8> got = load<T, 8>(from);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          v[i][j] = got.f32(j);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          v[i][j] = 0;
-      }
+      got[i] = {};
+      if (in && at[i] < width) // width is a multiple of 8
+        got[i] = load<T, 8>(from);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        v[i][j] = in && at[i] + 16 * j < width ? to_f32(from[16 * j]) : 0.0f;
+        got[i].v[j] = in && at[i] + 16 * j < width ? from[16 * j] : from_f32<T>(0.0f);
     }
   }
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
-    float most = fabsf(v[i][0]);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (VECTOR)
+        v[j] = got[i].f32(j);
+      else
+        v[j] = to_f32(got[i].v[j]);
+    }
+    float most = fabsf(v[0]);
 #pragma unroll
     for (int j = 1; j < 8; ++j)
-      most = max_nan(most, fabsf(v[i][j]));
+      most = max_nan(most, fabsf(v[j]));
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1)
       most = max_nan(most, __shfl_xor_sync(kAll, most, o));
     most = max_nan(most, kSmallest);
     const float by = kLargest / most;
-    const uint2 q = {to_e4m3(v[i][0] * by, v[i][1] * by, v[i][2] * by, v[i][3] * by),
-                     to_e4m3(v[i][4] * by, v[i][5] * by, v[i][6] * by, v[i][7] * by)};
+    const uint2 q = {to_e4m3(v[0] * by, v[1] * by, v[2] * by, v[3] * by), to_e4m3(v[4] * by, v[5] * by, v[6] * by, v[7] * by)};
     const uint32_t b = first + i * kGroups;
     if (b < blocks) {
       if (lane == 0)
@@ -635,7 +645,7 @@ extern "C" int segtopk_quantize_rows(segtopk_dtype dtype, const void* x, int64_t
       constexpr int S = decltype(steps)::value;
       const int64_t each = kThreads / 16 * S;
       return launch(quantize_kernel<T, decltype(vec)::value, S>, dim3((unsigned)((blocks + each - 1) / each)), kThreads, 0,
-                    (cudaStream_t)stream, (const T*)x, row_stride, (uint32_t)blocks, per_row, (int)width, (uint8_t*)values, scales);
+                    (cudaStream_t)stream, (const T*)x, row_stride, (uint32_t)blocks, per_row, 1.0f / (float)per_row, (int)width, (uint8_t*)values, scales);
     };
     auto by = [&](auto vec) {
       return few ? go(vec, std::integral_constant<int, 1>{}) : go(vec, std::integral_constant<int, 4>{});

@@ -259,10 +259,11 @@ template <int NV>
 __device__ __forceinline__ void keep_groups(float (&key)[NV], const GroupRule& rule, float* row)
 {
   const int lane = threadIdx.x & 31, first = lane * NV;
-  auto place = [](int e) { return e + e / 32; }; // lanes' shares in different banks
+  auto place = [](int e) { return e + (e >> 5); }; // lanes' shares in different banks
+  float* const share = row + place(first);         // all in the same 32
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    row[place(first + i)] = key[i];
+    share[i] = key[i];
   __syncwarp();
   const int each = 1 << rule.log_lanes; // lanes of a group
   const int group = lane >> rule.log_lanes, sub = lane & (each - 1);
@@ -300,16 +301,17 @@ __device__ __forceinline__ void keep_groups(float (&key)[NV], const GroupRule& r
     ahead += __shfl_xor_sync(kAll, ahead, o);
   const uint32_t kept = __ballot_sync(kAll, end > 0 && ahead < rule.kept);
   int g = (int)(((float)first + 0.5f) * rule.per_expert); // first / size: both are below 1025
-  if (rule.size % NV == 0) {
-    const bool on = g < rule.count && kept >> (g << rule.log_lanes) & 1;
+  int left = rule.size - (first - g * rule.size); // keys up to the next group
+  auto on = [&](int group) { return group < rule.count && kept >> ((group << rule.log_lanes) & 31) & 1; };
+  if (rule.size >= NV) { // no more than one border within
+    const bool on0 = on(g), on1 = on(g + 1);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      key[i] = on ? key[i] : -INFINITY;
+      key[i] = (i < left ? on0 : on1) ? key[i] : -INFINITY;
   } else {
-    int left = rule.size - (first - g * rule.size);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (g >= rule.count || !(kept >> (g << rule.log_lanes) & 1))
+      if (!on(g))
         key[i] = -INFINITY;
       if (--left == 0) {
         ++g;

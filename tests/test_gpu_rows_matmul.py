@@ -126,6 +126,21 @@ def test_products_and_gradients(tokens, k, experts, width, out, dropped, dtype):
     assert abs(float((grad_rows.double() * dx).sum() - ahead)) <= float((bound * dx.abs()).sum()) * 1.01
 
 
+@pytest.mark.parametrize("out", [1, 7, 129, 1001])
+def test_any_number_of_outputs(out):
+    groups = groups_of(150, 2, 5, 0.1)
+    rows, weights = whole(300, 136, seed=1, dtype=torch.bfloat16), whole(5, out, 136, seed=2, dtype=torch.bfloat16)
+    want = product(rows.double(), weights.double(), groups)[0]
+    for type in (torch.float32, torch.bfloat16, torch.float16):
+        assert torch.equal(st.expert_matmul(rows, weights, groups, out_dtype=type), want.to(type))
+    # a result that does not start on 16 bytes, and what lies around it
+    around = torch.full((300 * 64 + 2,), 7.0, device="cuda", dtype=torch.bfloat16)
+    weights = whole(5, 64, 136, seed=3, dtype=torch.bfloat16)
+    st.expert_matmul(rows, weights, groups, out=around[1:-1].view(300, 64))
+    assert torch.equal(around[1:-1].view(300, 64), product(rows.double(), weights.double(), groups)[0].bfloat16())
+    assert around[0] == around[-1] == 7
+
+
 F8_SHAPES = [  # tokens, k, experts, width, out, dropped
     (1, 1, 1, 16, 1, 0), (1, 8, 64, 128, 128, 0), (3, 2, 4, 128, 129, 0), (7, 3, 5, 144, 40, 0.3), (100, 6, 60, 1040, 1000, 0.1),
     (300, 2, 3, 256, 1001, 0), (1500, 1, 1, 640, 520, 0), (9000, 1, 3, 272, 392, 0.1), (50, 2, 8, 128, 128, 1.0),
