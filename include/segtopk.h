@@ -398,7 +398,8 @@ SEGTOPK_API int segtopk_test_device_prep(int n, const int* devices, const uint32
  * The selection's neighbours in a model (the source pages have no counterpart):
  * the k best experts of every token with their weights; the tokens' rows in
  * the order of their experts and, weighted, back; the rows of a token
- * embedding; and the gradients of all three. Sorting is stable and there are
+ * embedding; and the gradients of all three (the experts' products, layer norm
+ * and rows in 8 bits follow below). Sorting is stable and there are
  * no atomics on results, so every result is the same from run to run.
  *
  * Common to all: device pointers unless stated; float types are F16, BF16 and

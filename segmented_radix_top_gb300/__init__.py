@@ -2,9 +2,9 @@
 
 The compute runs in hand-written sm_103a CUDA kernels behind the C ABI of
 include/segtopk.h (libsegtopk.so); this package only marshals tensors into
-that ABI (_binding.py: the selection; _rows.py: expert routing, tokens sorted
-by expert and back, token embedding, and their gradients) and provides the
-seeded synthetic workloads (workloads.py).
+that ABI (_binding.py: the selection; _rows.py: layer norm, expert routing,
+tokens sorted by expert and back, the experts' products, token embedding, and
+their gradients) and provides the seeded synthetic workloads (workloads.py).
 """
 from ._binding import (DETERMINISM, DIRECTION, DTYPE, KEY_BYTES, MAX_K, NOALLOC_STAGING_BYTES,  # noqa: F401
                        ORDERING, TIE_BREAK, SegTopKError, batched_topk, batched_topk_host,

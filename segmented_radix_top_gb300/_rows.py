@@ -1,6 +1,7 @@
-"""The row operators of libsegtopk.so: expert routing, tokens sorted by expert
-and back, token embedding, and their gradients (include/segtopk.h has each
-operator's contract).
+"""The row operators of libsegtopk.so: layer norm, expert routing, tokens sorted
+by expert and back, the experts' matrix products, rows in 8 bits, token
+embedding, and their gradients (include/segtopk.h has each operator's
+contract).
 
 Inputs are CUDA tensors on one device. Rows may lie any distance apart (a
 part of a wider tensor's columns, one row expanded to many); tensors whose

@@ -1,6 +1,7 @@
 // Python binding of the row operators (include/segtopk.h: routing, tokens
-// sorted by expert and back, embedding): checks tensors, makes the results
-// and calls the C entry points on the current stream. _rows.py holds the
+// sorted by expert and back, the experts' products, layer norm, embedding):
+// checks tensors, makes the results and calls the C entry points on the
+// current stream. _rows.py holds the
 // public functions and their documentation.
 //
 // It is compiled, unlike the ctypes binding of the selection, because these
