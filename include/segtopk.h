@@ -646,7 +646,7 @@ SEGTOPK_API int segtopk_layer_norm(segtopk_dtype dtype, const void* x, int64_t n
  * of bias (of weight_dtype; sums over the rows in an order that depends on the
  * sizes alone; zeros where there are no rows). mean and rstd are what the
  * forward call wrote. workspace: at least
- * segtopk_layer_norm_backward_workspace_bytes(...) bytes, 4-byte aligned
+ * segtopk_layer_norm_backward_workspace_bytes(...) bytes, 16-byte aligned
  * (host-only arithmetic; 0 for no rows and for sizes out of range).
  */
 SEGTOPK_API size_t segtopk_layer_norm_backward_workspace_bytes(int64_t num_rows, int64_t width);

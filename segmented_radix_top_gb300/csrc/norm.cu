@@ -287,13 +287,8 @@ norm_backward_kernel(const T* grad, int64_t grad_stride, const T* x, int64_t x_s
               v[j] += joined[(group * kPart<N> + j) * 32 + lane];
         }
       }
-      if (group == 0)
-#pragma unroll
-        for (int j = 0; j < kPart<N>; ++j) {
-          const int c = N > 1 ? at + j : at + j * kLanes;
-          if (c < width)
-            to[which * width + c] = v[j];
-        }
+      if (group == 0 && at < width)
+        store_part<float, N>(to + which * width + at, v, kLanes, width - at);
     }
   }
 }
@@ -457,14 +452,19 @@ cudaError_t with_group(int64_t parts, F&& f)
   SEGTOPK_GROUP(8, 16);
 }
 template <int N, class F>
-cudaError_t with_backward_group(int64_t parts, F&& f)
+cudaError_t with_backward_group(int64_t parts, int64_t rows, F&& f)
 {
   if (parts <= 64)
     SEGTOPK_GROUP(2, 1);
-  if (parts <= 128)
+  // with few rows more warps for each: 1237 of 1001 in f32 9.5 us, 13.0 by (4, 2)
+  const bool few = rows <= 152 * 16;
+  if (parts <= 128 && !few)
     SEGTOPK_GROUP(4, 1);
-  if (parts <= 256)
+  if (parts <= 256) {
+    if (few)
+      SEGTOPK_GROUP(1, 8);
     SEGTOPK_GROUP(4, 2);
+  }
   if (parts <= 512)
     SEGTOPK_GROUP(2, 8);
   if (parts <= 1024)
@@ -579,7 +579,7 @@ extern "C" int segtopk_layer_norm_backward(segtopk_dtype dtype, const void* grad
         workspace_bytes < segtopk_layer_norm_backward_workspace_bytes(num_rows, width))
       return SEGTOPK_ERROR_INVALID_VALUE;
     if (!aligned(x, size_of(dtype)) || !aligned(grad_out, size_of(dtype)) || !aligned(grad_x, size_of(dtype)) ||
-        !aligned(weight, size_of(weight_dtype)) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(workspace, 4))
+        !aligned(weight, size_of(weight_dtype)) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(workspace, 16))
       return SEGTOPK_ERROR_MISALIGNED;
   }
   int sms;
@@ -597,7 +597,7 @@ extern "C" int segtopk_layer_norm_backward(segtopk_dtype dtype, const void* grad
                           rows_fit(grad_x, width, width, sizeof(T), N) && rows_fit(weight, width, width, sizeof(W), N);
       auto go = [&](auto n) {
         constexpr int V = decltype(n)::value;
-        return with_backward_group<V>(parts_of(width, V), [&](auto parts, auto warps) {
+        return with_backward_group<V>(parts_of(width, V), num_rows, [&](auto parts, auto warps) {
           constexpr int G = decltype(warps)::value;
           blocks = (int)blocks_for(num_rows, G);
           return launch(norm_backward_kernel<T, W, V, decltype(parts)::value, G>, dim3((unsigned)blocks), threads_of(G), 0,
