@@ -247,50 +247,78 @@ __device__ __forceinline__ int choose(const float (&key)[NV], float largest, flo
 struct GroupRule {
   int count, size, kept;
   bool two;         // a group's score is the sum of its two best
-  int log_lanes;    // lanes that share a group: as many as there are, a power of two
+  int log_lanes;    // lanes that serve a group: as many as there are, a power of two
+  int share;        // of a group for each of them
   float per_expert; // 1 / size
 };
 
-// Keys of the experts outside the best groups become -inf. The row passes
-// through shared memory, so that as many lanes as there are for each group
-// share its keys whatever its size: 65536 rows of 160 in 8 groups took 72 us
-// with the lanes' own keys compared group by group.
+// Where a lane's keys are of: its NV consecutive experts, or `share` of those
+// of the group that it serves with the lanes beside it. In both, places
+// lane * NV + i follow the experts' order.
+struct Places {
+  int share; // 0: NV consecutive experts
+  int size, log_lanes;
+  template <int NV>
+  __device__ __forceinline__ int expert(int place) const
+  {
+    const int lane = place / NV, group = lane >> log_lanes, sub = lane - (group << log_lanes);
+    return share == 0 ? place : group * size + sub * share + place % NV;
+  }
+};
+
+// The keys of the best groups; -inf in the other places. Each group is served
+// by as many lanes as there are for it, a power of two. Where a lane's share of
+// a group is at most NV keys it takes them over, from shared memory, so that
+// the group is the lanes' and whole lanes are kept or not. 65536 rows of 160, 3
+// of 8 groups: 37 us, 72 with the lanes' own keys compared group by group, 40
+// with the shares only looked at and left where they were, as they are where
+// groups are few, uneven and large.
 template <int NV>
-__device__ __forceinline__ void keep_groups(float (&key)[NV], const GroupRule& rule, float* row)
+__device__ __forceinline__ Places keep_groups(float (&key)[NV], const GroupRule& rule, float* row)
 {
   const int lane = threadIdx.x & 31, first = lane * NV;
-  auto place = [](int e) { return e + (e >> 5); }; // lanes' shares in different banks
-  float* const share = row + place(first);         // all in the same 32
+  auto gapped = [](int e) { return e + (e >> 5); }; // lanes' shares in different banks
+  float* const own = row + gapped(first);           // all in the same 32
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    share[i] = key[i];
+    own[i] = key[i];
   __syncwarp();
   const int each = 1 << rule.log_lanes; // lanes of a group
   const int group = lane >> rule.log_lanes, sub = lane & (each - 1);
-  const int end = group < rule.count ? rule.size : 0;
-  float a = -INFINITY; // the best key
-  if (!rule.two) {
-    for (int j = sub; j < end; j += each)
-      a = max_nan(a, row[place(group * rule.size + j)]);
-    for (int o = each / 2; o > 0; o /= 2)
-      a = max_nan(a, __shfl_xor_sync(kAll, a, o));
-  } else {
-    float b = -INFINITY; // the second best
-    for (int j = sub; j < end; j += each) {
-      const float x = row[place(group * rule.size + j)];
+  const bool serves = group < rule.count;
+  const bool taken = rule.share <= NV;
+  float a = -INFINITY, b = -INFINITY; // the best keys
+  auto look = [&](float x) {
+    if (rule.two)
       b = max_nan(b, fminf(a, x));
-      a = max_nan(a, x);
+    a = max_nan(a, x);
+  };
+  if (taken) {
+    const int begin = group * rule.size + sub * rule.share;
+    const int count = serves ? min(rule.share, rule.size - sub * rule.share) : 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      key[i] = -INFINITY;
+      if (i < rule.share) { // the same for all
+        if (i < count)
+          key[i] = row[gapped(begin + i)];
+        look(key[i]);
+      }
     }
-    for (int o = each / 2; o > 0; o /= 2) {
-      const float other_a = __shfl_xor_sync(kAll, a, o), other_b = __shfl_xor_sync(kAll, b, o);
-      b = max_nan(max_nan(b, other_b), fminf(a, other_a));
-      a = max_nan(a, other_a);
-    }
-    if (a != -INFINITY && b != -INFINITY)
-      a += b;
+  } else if (serves) {
+    for (int j = sub; j < rule.size; j += each)
+      look(row[gapped(group * rule.size + j)]);
   }
+  for (int o = each / 2; o > 0; o /= 2) {
+    const float other_a = __shfl_xor_sync(kAll, a, o);
+    if (rule.two)
+      b = max_nan(max_nan(b, __shfl_xor_sync(kAll, b, o)), fminf(a, other_a));
+    a = max_nan(a, other_a);
+  }
+  if (rule.two && a != -INFINITY && b != -INFINITY)
+    a += b;
   // a group's lanes share the others that may be ahead of it
-  const uint32_t code = end > 0 ? code_of(a) : 0;
+  const uint32_t code = serves ? code_of(a) : 0;
   int ahead = 0;
   for (int g = 0; g < rule.count; g += each) { // the same steps for all
     const int other_group = g + sub;
@@ -299,26 +327,26 @@ __device__ __forceinline__ void keep_groups(float (&key)[NV], const GroupRule& r
   }
   for (int o = each / 2; o > 0; o /= 2)
     ahead += __shfl_xor_sync(kAll, ahead, o);
-  const uint32_t kept = __ballot_sync(kAll, end > 0 && ahead < rule.kept);
-  int g = (int)(((float)first + 0.5f) * rule.per_expert); // first / size: both are below 1025
-  int left = rule.size - (first - g * rule.size); // keys up to the next group
-  auto on = [&](int group) { return group < rule.count && kept >> ((group << rule.log_lanes) & 31) & 1; };
-  if (rule.size >= NV) { // no more than one border within
-    const bool on0 = on(g), on1 = on(g + 1);
+  const bool keep = serves && ahead < rule.kept;
+  if (taken) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      key[i] = (i < left ? on0 : on1) ? key[i] : -INFINITY;
-  } else {
+      key[i] = keep ? key[i] : -INFINITY;
+    return {rule.share, rule.size, rule.log_lanes};
+  }
+  const uint32_t kept = __ballot_sync(kAll, keep);
+  int g = (int)(((float)first + 0.5f) * rule.per_expert); // first / size: both are below 1025
+  int left = rule.size - (first - g * rule.size);         // keys up to the next group
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (!on(g))
-        key[i] = -INFINITY;
-      if (--left == 0) {
-        ++g;
-        left = rule.size;
-      }
+  for (int i = 0; i < NV; ++i) {
+    if (g >= rule.count || !(kept >> ((g << rule.log_lanes) & 31) & 1))
+      key[i] = -INFINITY;
+    if (--left == 0) {
+      ++g;
+      left = rule.size;
     }
   }
+  return {0, rule.size, rule.log_lanes};
 }
 
 template <class T, int NV, bool VECTOR, bool SIGMOID, bool GROUPS>
@@ -356,21 +384,30 @@ route_kernel(const T* logits, uint32_t tokens, int experts, int64_t stride, int 
     for (int i = 0; i < NV; ++i)
       if (x[i] != -INFINITY) // which those past the row's end are
         x[i] = key_at(first + i, x[i]);
+    Places places = {};
     if constexpr (GROUPS)
-      keep_groups(x, rule, group_rows[warp]);
+      places = keep_groups(x, rule, group_rows[warp]);
     largest = max_of(x);
-    id = choose<NV>(x, largest, warp_max_nan(largest), k, choices[warp],
-                    [&](int e) { return key_at(e, to_f32(row[e])); });
+    id = choose<NV>(x, largest, warp_max_nan(largest), k, choices[warp], [&](int place) {
+      const int e = GROUPS ? places.expert<NV>(place) : place;
+      return key_at(e, to_f32(row[e]));
+    });
+    if (GROUPS && id >= 0)
+      id = places.expert<NV>(id);
   } else {
     if (!SIGMOID && !renormalize)
       sum = softmax_sum<true>(x, top);
     float best = top;
+    Places places = {};
     if constexpr (GROUPS) {
-      keep_groups(x, rule, group_rows[warp]);
+      places = keep_groups(x, rule, group_rows[warp]);
       largest = max_of(x);
       best = warp_max_nan(largest);
     }
-    id = choose<NV>(x, largest, best, k, choices[warp], [&](int e) { return to_f32(row[e]); });
+    id = choose<NV>(x, largest, best, k, choices[warp],
+                    [&](int place) { return to_f32(row[GROUPS ? places.expert<NV>(place) : place]); });
+    if (GROUPS && id >= 0)
+      id = places.expert<NV>(id);
   }
   const bool on = id >= 0;
   const float w = chosen_weight<SIGMOID>(on ? to_f32(row[id]) : 0.0f, on, renormalize, top, sum);

@@ -20,7 +20,8 @@ extern "C" int segtopk_route_groups(segtopk_dtype dtype, const void* logits, int
   while (num_groups << log_lanes > 32)
     --log_lanes;
   const int size = experts / num_groups;
-  const GroupRule rule = {num_groups, size, groups_kept, group_score == SEGTOPK_GROUP_BEST_TWO, log_lanes, 1.0f / size};
+  const GroupRule rule = {num_groups, size, groups_kept, group_score == SEGTOPK_GROUP_BEST_TWO, log_lanes,
+                          (size + (1 << log_lanes) - 1) >> log_lanes, 1.0f / size};
   return route<true>(dtype, logits, tokens, experts, row_stride, k, rule, score, renormalize, scale, bias, expert_ids,
                      weights, stream);
 }
