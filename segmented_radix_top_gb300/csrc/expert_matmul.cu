@@ -41,9 +41,9 @@
 //   8 bits, 64 rows of 64 experts, 2048x1024         17 us (decode)
 // A block of the main loop takes 518 cycles of the tensor cores' 512 in the
 // first; the clock is then at 1.45 GHz of 2.07 by the GPU's power limit. In 8
-// bits it takes 920: the sums' way from TMEM to registers, a wait of some
-// hundred cycles for every load of it, is what bounds it. With few rows the
-// weights' bytes do.
+// bits it takes 920: products that are issued back to back end that far apart
+// while sums are loaded from TMEM, 530 while none are, and each block's 128 KB
+// of sums have to be loaded. With few rows the weights' bytes bound it.
 #include <atomic>
 #include <cuda.h>
 
