@@ -458,6 +458,7 @@ __device__ void copy_operands(const CUtensorMap& map, const CUtensorMap& large, 
   const uint32_t full = at_first<K>(&sh.full[0]), empty = smem_addr(&sh.empty[0]);
   Ring<kStages> s;
   int used = 0; // stages whose copies are under way or have landed
+  uint32_t end_parity = 0, end_last = 0; // kWeights, a bit for each stage: its last rows' next phase; they are its last copies
   bool ok = true, ready = false;
   for (int t = blockIdx.x / blocks_of(K); ok && t < tiles; t += gridDim.x / blocks_of(K)) {
     const Tile tile = tile_at<K>(t, z, sh);
@@ -501,8 +502,12 @@ __device__ void copy_operands(const CUtensorMap& map, const CUtensorMap& large, 
           expect(on, smem_addr(&sh.end_full[0]) + s.at * 8, landing + extra);
         }
         bar = smem_addr(&sh.end_full[0]) + s.at * 8;
-      } else if (IS_P && me == 0) {
-        expect(on, bar, expected + extra);
+        end_parity ^= 1u << s.at;
+        end_last |= 1u << s.at;
+      } else {
+        if (IS_P && me == 0)
+          expect(on, bar, expected + extra);
+        end_last &= ~(1u << s.at);
       }
       used = min(used + 1, kStages);
       s.next();
@@ -522,12 +527,15 @@ __device__ void copy_operands(const CUtensorMap& map, const CUtensorMap& large, 
       }
     }
   }
-  if (!ok && IS_P && me == 0) {
+  if (!ok && IS_P) {
     // what is under way lands before the blocks end (a second each at most)
     for (int i = 0; i < used; ++i) {
       s.at = s.at == 0 ? kStages - 1 : s.at - 1;
       s.parity ^= s.at == kStages - 1;
-      mbar_wait(&sh.full[s.at], s.parity, sh.wait_limit);
+      if (end_last >> s.at & 1)
+        mbar_wait(&sh.end_full[s.at], ~end_parity >> s.at & 1, sh.wait_limit);
+      else if (me == 0)
+        mbar_wait(&sh.full[s.at], s.parity, sh.wait_limit);
     }
   }
 }
@@ -539,15 +547,15 @@ __device__ void clear_ends(const Sizes& z, char* stages, Control& sh)
 {
   constexpr Kind K = kWeights;
   const int lane = threadIdx.x & 31, tiles = sh.tile_start[z.experts];
-  int stage = 0;
+  int next = 0;        // stage
   uint32_t before = 0; // a bit for each stage: the parity of its last blocks of rows
   for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2) {
     const Tile tile = tile_at<K>(t, z, sh);
     const int copies = 2 + pieces(pieces(tile.width, kStepQ) * kStepQ / 2, 64), left = tile.rows % kDepth;
-    stage += tile.blocks;
+    const int at = (next + tile.blocks - 1) % stages_of(K);
+    next = (next + tile.blocks) % stages_of(K);
     if (left == 0)
       continue;
-    const int at = (stage - 1) % stages_of(K);
     if (!wait(&sh.end_full[at], before >> at & 1, sh))
       return;
     before ^= 1u << at;
