@@ -629,19 +629,20 @@ __device__ void issue_products(const Sizes& z, char* stages, Control& sh)
 }
 
 // A warp's 32 rows, one a lane, of `columns` values to memory, `stride` apart
-// from `to` on; the first `rows` of them. With rows on 16-byte boundaries they
-// pass through shared memory 64 bytes at a time, so that four lanes write them
-// together: a store whose lanes write to a row each takes 32 cycles of an SM's
-// memory pipe, and with 16 bytes a lane a tile's took longer than four of its
-// blocks' products.
+// from `to` on; the first `rows` of them. They pass through shared memory 64
+// bytes at a time, so that lanes write a row together: four of them 16 bytes
+// each with rows on 16-byte boundaries, else one for each value. A store whose
+// lanes write to a row each takes 32 cycles of an SM's memory pipe; with 16
+// bytes a lane a tile's took longer than four of its blocks' products, with a
+// value a lane the whole product four times as long.
 template <class O, int N, class F>
 __device__ __forceinline__ void write_rows(O* to, int64_t stride, int rows, int columns, bool vectors, uint4* staging, F&& sum)
 {
+  constexpr int V = 16 / (int)sizeof(O);
   const int lane = threadIdx.x & 31;
+  auto place = [](int row, int u) { return row * 4 + (u ^ (row >> 1 & 3)); }; // eight lanes in different banks
   if (vectors) { // columns is a multiple of V
-    constexpr int V = 16 / (int)sizeof(O);
     const int unit = lane & 3;
-    auto place = [](int row, int u) { return row * 4 + (u ^ (row >> 1 & 3)); }; // eight lanes in different banks
 #pragma unroll
     for (int c = 0; c < N; c += 4 * V) {
       if (c >= columns)
@@ -666,11 +667,22 @@ __device__ __forceinline__ void write_rows(O* to, int64_t stride, int rows, int 
       }
       __syncwarp();
     }
-  } else if (lane < rows) {
+  } else {
+    O* const values = reinterpret_cast<O*>(staging);
+    const int i = lane % (4 * V);
 #pragma unroll
-    for (int c = 0; c < N; ++c)
-      if (c < columns)
-        to[lane * stride + c] = from_f32<O>(sum(c));
+    for (int c = 0; c < N; c += 4 * V) {
+      if (c >= columns)
+        break;
+#pragma unroll
+      for (int k = 0; k < 4 * V; ++k)
+        values[lane * 4 * V + (k ^ (lane & (4 * V - 1)))] = from_f32<O>(sum(c + k));
+      __syncwarp();
+      for (int row = lane / (4 * V); row < min(rows, 32); row += 32 / (4 * V))
+        if (c + i < columns)
+          to[row * stride + c + i] = values[row * 4 * V + (i ^ (row & (4 * V - 1)))];
+      __syncwarp();
+    }
   }
 }
 
