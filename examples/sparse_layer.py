@@ -3,11 +3,12 @@ with this package's operators:
 
     tokens -> embedding -> router -> tokens sorted by expert -> experts -> back, weighted -> logits -> top-k
 
-    python examples/sparse_layer.py [--steps 60]
+    python examples/sparse_layer.py [--steps 60] [--dtype bfloat16]
 
 The data is synthetic (each token is followed by a fixed other one most of the
-time), so the loss has a known floor. The experts' products and the logits are
-torch matrix products; everything around them runs in libsegtopk.so. The four
+time), so the loss has a known floor. In 16 bits the experts' products run in
+libsegtopk.so too, from the experts' offsets on the device; in 32 bits they are
+torch matrix products, expert by expert. The logits are torch's. The five
 autograd functions below are all that is needed to use the operators in a
 model that torch differentiates.
 """
@@ -72,13 +73,25 @@ class Combine(torch.autograd.Function):
         return *st.combine_backward(grad, rows, ctx.groups, weights), None
 
 
+class Product(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, weights, groups):
+        ctx.save_for_backward(rows, weights)
+        ctx.groups = groups
+        return st.expert_matmul(rows, weights, groups)
+
+    @staticmethod
+    def backward(ctx, grad):
+        return *st.expert_matmul_backward(grad, *ctx.saved_tensors, ctx.groups), None
+
+
 class SparseModel(torch.nn.Module):
-    def __init__(self, vocab, width, hidden, experts, k, device="cuda", seed=0):
+    def __init__(self, vocab, width, hidden, experts, k, device="cuda", seed=0, dtype=torch.float32):
         super().__init__()
         g = torch.Generator().manual_seed(seed)
 
         def weight(*shape, scale):
-            return torch.nn.Parameter((scale * torch.randn(*shape, generator=g)).to(device))
+            return torch.nn.Parameter((scale * torch.randn(*shape, generator=g)).to(device, dtype))
 
         self.k = k
         self.table = weight(vocab, width, scale=width ** -0.5)
@@ -89,6 +102,9 @@ class SparseModel(torch.nn.Module):
 
     def experts(self, rows, groups):
         """Each expert's two products on its rows; rows of no expert stay zero."""
+        if rows.dtype != torch.float32:
+            hidden = Product.apply(rows, self.up.transpose(1, 2), groups)
+            return Product.apply(torch.nn.functional.gelu(hidden), self.down.transpose(1, 2), groups)
         bounds = groups.offsets.tolist()
         done = [torch.nn.functional.gelu(rows[a:b] @ self.up[e]) @ self.down[e]
                 for e, (a, b) in enumerate(zip(bounds, bounds[1:]))]
@@ -109,7 +125,7 @@ def sample(model, tokens, k, generator):
     offsets = torch.arange(0, (rows + 1) * vocab, vocab, device=logits.device)
     ids = torch.arange(vocab, dtype=torch.int32, device=logits.device).repeat(rows)
     best, which = st.batched_topk(logits.reshape(-1), offsets, k, values=ids, max_segment_len=vocab)
-    p = torch.softmax(best.reshape(rows, k), 1)
+    p = torch.softmax(best.reshape(rows, k).float(), 1)
     return which.reshape(rows, k).gather(1, torch.multinomial(p, 1, generator=generator)).squeeze(1)
 
 
@@ -121,14 +137,14 @@ def text(n, vocab, generator, device="cuda"):
     return tokens, torch.where(rule, (7 * tokens + 3) % vocab, other)
 
 
-def train(steps=60, vocab=512, width=128, hidden=256, experts=16, k=2, batch=4096, rate=2e-3):
+def train(steps=60, vocab=512, width=128, hidden=256, experts=16, k=2, batch=4096, rate=2e-3, dtype=torch.float32):
     g = torch.Generator(device="cuda").manual_seed(1)
-    model = SparseModel(vocab, width, hidden, experts, k)
+    model = SparseModel(vocab, width, hidden, experts, k, dtype=dtype)
     optimizer = torch.optim.Adam(model.parameters(), lr=rate)
     losses = []
     for _ in range(steps):
         tokens, following = text(batch, vocab, g)
-        loss = torch.nn.functional.cross_entropy(model(tokens), following)
+        loss = torch.nn.functional.cross_entropy(model(tokens).float(), following)
         optimizer.zero_grad()
         loss.backward()
         optimizer.step()
@@ -142,7 +158,10 @@ def train(steps=60, vocab=512, width=128, hidden=256, experts=16, k=2, batch=409
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=60)
-    losses, right = train(ap.parse_args().steps)
+    # float16 would want a loss scale and an optimizer in 32 bits: Adam's 1e-8 is 0 there
+    ap.add_argument("--dtype", choices=["float32", "bfloat16"], default="float32")
+    args = ap.parse_args()
+    losses, right = train(args.steps, dtype=getattr(torch, args.dtype))
     print("loss %.3f -> %.3f; %.0f %% of the sampled tokens follow the rule" % (losses[0], losses[-1], 100 * right))
 
 
