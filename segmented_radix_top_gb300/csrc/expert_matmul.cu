@@ -1189,7 +1189,7 @@ extern "C" int segtopk_expert_matmul_weights(segtopk_dtype dtype, const void* a_
     const cudaError_t e = cudaMemsetAsync(out, 0, bytes, (cudaStream_t)stream);
     return e == cudaSuccess ? SEGTOPK_SUCCESS : record_cuda_error(e);
   }
-  CUtensorMap p, q, large = {};
+  CUtensorMap p, q;
   cudaError_t e = describe(&p, map_type(dtype), 2, b_rows, b_width, num_rows, 1, b_stride, b_stride, kDepth);
   if (e == cudaSuccess)
     e = describe(&q, map_type(dtype), 2, a_rows, a_width, num_rows, 1, a_stride, a_stride, kDepth);
@@ -1205,6 +1205,7 @@ extern "C" int segtopk_expert_matmul_weights(segtopk_dtype dtype, const void* a_
   return with_float_type(out_dtype, [&](auto zero) {
     using O = decltype(zero);
     z.out_vectors = rows_fit(out, b_width, b_width, sizeof(O), 16 / (int)sizeof(O));
-    return run<kWeights, O>(p, q, large, offsets, z, out, sms, tiles, stream);
+    // The kernel fetches three descriptors ahead and copies with two: the third is a valid one too.
+    return run<kWeights, O>(p, q, p, offsets, z, out, sms, tiles, stream);
   });
 }
