@@ -622,6 +622,16 @@ SEGTOPK_API int segtopk_expert_matmul_weights(segtopk_dtype dtype, const void* a
                                               const int64_t* offsets, segtopk_dtype out_dtype, void* out,
                                               void* stream);
 
+/*
+ * segtopk_test_expert_tile (instrumented build; host only, no CUDA call): the
+ * rows of an expert that its tile `index` of segtopk_expert_matmul has, by the
+ * arithmetic of the kernel: `width` of the expert's `rows` rows from `first`
+ * on. An expert has ceil(rows / 256) tiles of them (for each 256 outputs).
+ * Errors: SEGTOPK_ERROR_INVALID_VALUE for a number of rows or an index out of
+ * range.
+ */
+SEGTOPK_API int segtopk_test_expert_tile(int32_t rows, int32_t index, int32_t* first, int32_t* width);
+
 /* ---------------------------------------------------------------------------
  * Layer norm, and rows in 8 bits
  * ---------------------------------------------------------------------------

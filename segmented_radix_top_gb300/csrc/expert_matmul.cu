@@ -48,6 +48,7 @@
 #include <cuda.h>
 
 #include "common.cuh"
+#include "expert_tiles.h"
 #include "rows.cuh"
 
 namespace segtopk {
@@ -57,13 +58,11 @@ using namespace rows;
 constexpr int kThreads = 384;
 constexpr int kSumWarps = 8;     // of them the last
 constexpr int kTileP = 128;      // of a block: the lanes of TMEM
-constexpr int kTileQ = 256;      // half of its columns
 constexpr int kOperandBytes = 192 << 10;
 constexpr int kMaxStages = 6;
 constexpr int kBytesP = kTileP * 128;
 constexpr int kBox = 32;         // rows of one copy of few of an expert's rows
 constexpr int kDepth = 64;       // rows of one copy where c runs over rows
-constexpr int kStepQ = 32;       // of a tile's width: 16 for each block of a pair
 constexpr int kMaxExperts = SEGTOPK_MAX_EXPERTS;
 
 enum Kind { kForward8, kForward8Pair, kForward, kForwardTurned, kWeights };
@@ -303,8 +302,6 @@ struct Ring {
 // ---------------------------------------------------------------------------
 // Tiles
 // ---------------------------------------------------------------------------
-__host__ __device__ __forceinline__ int pieces(int n, int size) { return (n + size - 1) / size; }
-
 struct Tile {
   int expert;
   int p;          // first
@@ -314,8 +311,7 @@ struct Tile {
 };
 
 // Tiles of an expert with this many rows. Where q are its rows, or its inputs
-// or outputs, it goes to as few tiles as hold it, of even widths in steps of
-// kStepQ; none is empty, since all but the last are no wider than kTileQ.
+// or outputs, it goes to as few tiles as hold it (even_part()).
 template <Kind K>
 __device__ __forceinline__ int parts_p(int rows, const Sizes& z) { return pieces(eight(K) ? rows : z.p, tile_p(K)); }
 template <Kind K>
@@ -323,19 +319,6 @@ __device__ __forceinline__ int parts_q(int rows, const Sizes& z)
 {
   return eight(K) ? pieces(z.q, z.step) : pieces(K == kWeights ? z.q : rows, kTileQ);
 }
-
-// a / b, rounded down, for a >= 0 and b > 0: by a product in 32 bits, which is
-// at most one off where the quotient is below 2^22, and a step.
-__device__ __forceinline__ int divide(int a, int b)
-{
-  if (a >= 1 << 22)
-    return a / b;
-  int q = (int)((float)a * __frcp_rn((float)b));
-  const int rest = a - q * b;
-  q += rest >= b ? 1 : rest < 0 ? -1 : 0;
-  return q;
-}
-__device__ __forceinline__ int divide_up(int a, int b) { return divide(a + b - 1, b); }
 
 // Tile t, by a whole warp, which finds its expert in two looks: among every
 // 32nd, then the 32 after that.
@@ -362,10 +345,10 @@ __device__ __forceinline__ Tile tile_at(int t, const Sizes& z, const Control& sh
   } else {
     const int q = K == kWeights ? z.q : r.rows;
     const int parts = parts_q<K>(r.rows, z);
-    const int step = pieces(divide_up(q, parts), kStepQ) * kStepQ;
     const int p = divide(i, parts);
-    r.q = (i - p * parts) * step;
-    r.width = min(step, q - r.q);
+    const TilePart part = even_part(q, parts, i - p * parts);
+    r.q = part.first;
+    r.width = part.width;
     r.p = p * tile_p(K);
     r.blocks = K == kWeights ? pieces(r.rows, kDepth) : pieces(z.c, 64);
   }
@@ -1208,4 +1191,22 @@ extern "C" int segtopk_expert_matmul_weights(segtopk_dtype dtype, const void* a_
     // The kernel fetches three descriptors ahead and copies with two: the third is a valid one too.
     return run<kWeights, O>(p, q, p, offsets, z, out, sms, tiles, stream);
   });
+}
+
+extern "C" int segtopk_test_expert_tile(int32_t rows, int32_t index, int32_t* first, int32_t* width)
+{
+#ifndef SEGTOPK_TEST_HOOKS
+  (void)rows;
+  (void)index;
+  (void)first;
+  (void)width;
+  return SEGTOPK_ERROR_NOT_SUPPORTED;
+#else
+  if (rows < 1 || rows > 2147483647 - kTileQ || index < 0 || index >= pieces(rows, kTileQ) || !first || !width)
+    return SEGTOPK_ERROR_INVALID_VALUE;
+  const TilePart part = even_part(rows, pieces(rows, kTileQ), index);
+  *first = part.first;
+  *width = part.width;
+  return SEGTOPK_SUCCESS;
+#endif
 }
