@@ -632,6 +632,14 @@ SEGTOPK_API int segtopk_expert_matmul_weights(segtopk_dtype dtype, const void* a
  */
 SEGTOPK_API int segtopk_test_expert_tile(int32_t rows, int32_t index, int32_t* first, int32_t* width);
 
+/*
+ * segtopk_test_free_row (instrumented build; host only, no CUDA call): the row
+ * of the result that the kernels take as number `index` of those that no
+ * expert has, where the experts' rows begin at `first` and end at `end`.
+ * Errors: SEGTOPK_ERROR_INVALID_VALUE.
+ */
+SEGTOPK_API int segtopk_test_free_row(int32_t first, int32_t end, int32_t index, int64_t* row);
+
 /* ---------------------------------------------------------------------------
  * Layer norm, and rows in 8 bits
  * ---------------------------------------------------------------------------

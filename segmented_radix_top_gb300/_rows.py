@@ -67,6 +67,7 @@ def _entries():
         "segtopk_expert_matmul_f8": (i, [vp, i64, i64, i64, vp, i64, vp, i32, i64, i64, i64, vp, vp, i, vp, vp]),
         "segtopk_expert_matmul_weights": (i, [i, vp, i64, i64, vp, i64, i64, i64, i32, vp, i, vp, vp]),
         "segtopk_test_expert_tile": (i, [i32, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]),
+        "segtopk_test_free_row": (i, [i32, i32, i32, ctypes.POINTER(i64)]),
         "segtopk_layer_norm": (i, [i, vp, i64, i64, i64, i, vp, vp, f, vp, vp, vp, vp]),
         "segtopk_layer_norm_backward_workspace_bytes": (sz, [i64, i64]),
         "segtopk_layer_norm_backward": (i, [i, vp, i64, vp, i64, i64, i64, i, vp, vp, vp, vp, vp, vp, vp, sz, vp]),

@@ -891,10 +891,12 @@ product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant_
     if constexpr (K != kWeights) {
       // rows that no expert has
       const int all = (int)gridDim.x * kSumWarps;
-      const int first = (int)blockIdx.x * kSumWarps + warp - (kThreads / 32 - kSumWarps);
-      for (int64_t r = sh.row_start[z.experts] + first; r < z.num_rows; r += all)
-        for (int i = lane; i < z.out_stride; i += 32)
-          out[r * z.out_stride + i] = from_f32<O>(0.0f);
+      const int end = sh.row_start[z.experts];
+      for (int64_t i = (int)blockIdx.x * kSumWarps + warp - (kThreads / 32 - kSumWarps); i < z.num_rows - end; i += all) {
+        O* const to = out + free_row(0, end, i) * z.out_stride;
+        for (int c = lane; c < z.out_stride; c += 32)
+          to[c] = from_f32<O>(0.0f);
+      }
     }
     fence_before_sync();
   }
@@ -1207,6 +1209,22 @@ extern "C" int segtopk_test_expert_tile(int32_t rows, int32_t index, int32_t* fi
   const TilePart part = even_part(rows, pieces(rows, kTileQ), index);
   *first = part.first;
   *width = part.width;
+  return SEGTOPK_SUCCESS;
+#endif
+}
+
+extern "C" int segtopk_test_free_row(int32_t first, int32_t end, int32_t index, int64_t* row)
+{
+#ifndef SEGTOPK_TEST_HOOKS
+  (void)first;
+  (void)end;
+  (void)index;
+  (void)row;
+  return SEGTOPK_ERROR_NOT_SUPPORTED;
+#else
+  if (first < 0 || end < first || index < 0 || !row)
+    return SEGTOPK_ERROR_INVALID_VALUE;
+  *row = free_row(first, end, index);
   return SEGTOPK_SUCCESS;
 #endif
 }

@@ -5,6 +5,7 @@
 // still is a 32-bit number; nothing larger is added to them in 32 bits.
 #pragma once
 
+#include <cstdint>
 #include <cuda_runtime.h>
 
 namespace segtopk {
@@ -44,6 +45,14 @@ __host__ __device__ __forceinline__ TilePart even_part(int n, int parts, int at)
   const int step = pieces(divide_up(n, parts), kStepQ) * kStepQ;
   const int first = at * step;
   return {first, step < n - first ? step : n - first};
+}
+
+// Row i of those that no expert has: the ones before `first`, then those from
+// `end` on. In 64 bits: the GPU's warps take a number each to begin with, there
+// being that many such rows or not, so end + i may pass 2^31.
+__host__ __device__ __forceinline__ int64_t free_row(int first, int end, int64_t i)
+{
+  return i < first ? i : end + (i - first);
 }
 
 } // namespace segtopk
