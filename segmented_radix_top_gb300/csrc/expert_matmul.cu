@@ -87,6 +87,7 @@ struct Control {
   uint64_t drained;                             // products behind a wait that ran out
   uint32_t tmem;
   int failed;                                   // a wait ran out: everybody leaves
+  uint32_t progress;                            // kWeights: blocks of rows that this block has begun to copy
   long long wait_limit;                         // cycles
   int part[kThreads / 32];
   int tile_start[kMaxExperts + 1];              // experts' first tiles
@@ -249,17 +250,27 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
   return ok != 0;
 }
 // One warp: waits for the phase of `bar` with this parity; false, for good,
-// after about a second, or once another wait of the block has run out.
+// after about a second, or once another wait of the block has run out. A LONG
+// wait lasts as long as an expert has rows: its second begins anew as long as
+// the block goes on to copy.
+template <bool LONG = false>
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Control& sh)
 {
   if (__all_sync(kAll, try_wait(bar, parity)))
     return true;
-  const long long start = clock64();
+  long long start = clock64();
+  uint32_t seen = LONG ? *(volatile uint32_t*)&sh.progress : 0;
   bool failed = false;
   while (!__all_sync(kAll, try_wait(bar, parity))) {
     if (clock64() - start > sh.wait_limit) {
-      *(volatile int*)&sh.failed = 1;
-      raise_error(kErrCopyTimeout);
+      const uint32_t now = LONG ? *(volatile uint32_t*)&sh.progress : 0;
+      if (now != seen) {
+        seen = now;
+        start = clock64();
+      } else {
+        *(volatile int*)&sh.failed = 1;
+        raise_error(kErrCopyTimeout);
+      }
     }
     failed = *(volatile int*)&sh.failed;
     if (__any_sync(kAll, failed))
@@ -267,7 +278,11 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Control& sh)
   }
   return true;
 }
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Control& sh) { return wait(smem_addr(bar), parity, sh); }
+template <bool LONG = false>
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Control& sh)
+{
+  return wait<LONG>(smem_addr(bar), parity, sh);
+}
 
 // Whether that phase is over already; does not wait. Asked a step ahead, so
 // that the answer is there when the step comes.
@@ -442,6 +457,7 @@ __device__ void copy_operands(const CUtensorMap& map, const CUtensorMap& large, 
   Ring<kStages> s;
   int used = 0; // stages whose copies are under way or have landed
   uint32_t end_parity = 0, end_last = 0; // kWeights, a bit for each stage: its last rows' next phase; they are its last copies
+  uint32_t begun = 0;                    // kWeights: blocks of rows
   bool ok = true, ready = false;
   for (int t = blockIdx.x / blocks_of(K); ok && t < tiles; t += gridDim.x / blocks_of(K)) {
     const Tile tile = tile_at<K>(t, z, sh);
@@ -470,6 +486,8 @@ __device__ void copy_operands(const CUtensorMap& map, const CUtensorMap& large, 
         ok = wait(empty + s.at * 8, s.parity ^ 1, sh);
       if (!ok)
         break;
+      if (K == kWeights && IS_P)
+        *(volatile uint32_t*)&sh.progress = ++begun; // by all lanes, the same
 #ifdef SEGTOPK_TEST_HOOKS
       const int extra = used == 0 ? z.test_extra_bytes : 0;
 #else
@@ -539,7 +557,7 @@ __device__ void clear_ends(const Sizes& z, char* stages, Control& sh)
     next = (next + tile.blocks) % stages_of(K);
     if (left == 0)
       continue;
-    if (!wait(&sh.end_full[at], before >> at & 1, sh))
+    if (!wait<true>(&sh.end_full[at], before >> at & 1, sh))
       return;
     before ^= 1u << at;
     for (int i = 0; i < copies; ++i)
@@ -784,7 +802,7 @@ __device__ void write_sums(const Sizes& z, O* out, Control& sh)
     const int p = tile.p + rank<K>() * kTileP + quarter * 32 + lane;
     const bool any = tile.blocks > 0; // none: an expert without rows has a gradient of zeros
     if (any) {
-      if (!wait(&sh.sums_full[d.at], d.parity, sh))
+      if (!wait<K == kWeights>(&sh.sums_full[d.at], d.parity, sh))
         return;
       fence_after_sync();
     }
@@ -846,6 +864,7 @@ product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant_
     mbar_init(&sh.drained, 1);
     fence_mbar_init();
     sh.failed = 0;
+    sh.progress = 0;
     sh.wait_limit = z.wait_limit;
   }
   if (warp == 2) {
