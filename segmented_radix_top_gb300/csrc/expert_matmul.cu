@@ -197,11 +197,16 @@ __device__ __forceinline__ void expect(uint32_t on, uint32_t bar, int bytes)
 // At a barrier of either block of a pair. Without a release at cluster scope,
 // which waits until all of the block's writes are visible everywhere: once
 // every block of 8-bit operands that doubled the time of a product. What the
-// other block is told here is that it may write, or what a fence has already
-// made visible to the tensor cores.
+// other block is told here is that it may write, or has to wait for more.
 __device__ __forceinline__ void arrive(uint32_t bar)
 {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same for a block that has written to its own shared memory what products
+// of the other one read: with that release, once a tile.
+__device__ __forceinline__ void arrive_after_writes(uint32_t bar)
+{
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // The address of the first block's `bar`.
 template <Kind K>
@@ -249,21 +254,34 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
     : "memory");
   return ok != 0;
 }
+// As try_wait, for what the arrivals' blocks wrote (arrive_after_writes).
+__device__ __forceinline__ bool try_wait_for_writes(uint32_t bar, uint32_t parity)
+{
+  uint32_t ok;
+  asm volatile(
+    "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+    : "=r"(ok)
+    : "r"(bar), "r"(parity)
+    : "memory");
+  return ok != 0;
+}
 // One warp: waits for the phase of `bar` with this parity; false, for good,
-// after about a second, or once another wait of the block has run out. A LONG
-// wait lasts as long as an expert has rows: its second begins anew as long as
-// the block goes on to copy.
-template <bool LONG = false>
+// after about a second, or once another wait of the block has run out. A
+// kLongWait lasts as long as an expert has rows: its second begins anew as
+// long as the block goes on to copy.
+enum Wait { kWait, kLongWait, kWaitForWrites };
+template <Wait W = kWait>
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Control& sh)
 {
-  if (__all_sync(kAll, try_wait(bar, parity)))
+  auto over = [&] { return __all_sync(kAll, W == kWaitForWrites ? try_wait_for_writes(bar, parity) : try_wait(bar, parity)); };
+  if (over())
     return true;
   long long start = clock64();
-  uint32_t seen = LONG ? *(volatile uint32_t*)&sh.progress : 0;
+  uint32_t seen = W == kLongWait ? *(volatile uint32_t*)&sh.progress : 0;
   bool failed = false;
-  while (!__all_sync(kAll, try_wait(bar, parity))) {
+  while (!over()) {
     if (clock64() - start > sh.wait_limit) {
-      const uint32_t now = LONG ? *(volatile uint32_t*)&sh.progress : 0;
+      const uint32_t now = W == kLongWait ? *(volatile uint32_t*)&sh.progress : 0;
       if (now != seen) {
         seen = now;
         start = clock64();
@@ -278,10 +296,10 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Control& sh)
   }
   return true;
 }
-template <bool LONG = false>
+template <Wait W = kWait>
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Control& sh)
 {
-  return wait<LONG>(smem_addr(bar), parity, sh);
+  return wait<W>(smem_addr(bar), parity, sh);
 }
 
 // Whether that phase is over already; does not wait. Asked a step ahead, so
@@ -557,7 +575,7 @@ __device__ void clear_ends(const Sizes& z, char* stages, Control& sh)
     next = (next + tile.blocks) % stages_of(K);
     if (left == 0)
       continue;
-    if (!wait<true>(&sh.end_full[at], before >> at & 1, sh))
+    if (!wait<kLongWait>(&sh.end_full[at], before >> at & 1, sh))
       return;
     before ^= 1u << at;
     for (int i = 0; i < copies; ++i)
@@ -566,7 +584,7 @@ __device__ void clear_ends(const Sizes& z, char* stages, Control& sh)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0)
-      arrive(at_first<K>(&sh.end_ready[at]));
+      arrive_after_writes(at_first<K>(&sh.end_ready[at]));
   }
 }
 
@@ -597,7 +615,7 @@ __device__ void issue_products(const Sizes& z, char* stages, Control& sh)
       if (ok && !__all_sync(kAll, ready))
         ok = wait(full + s.at * 8, s.parity, sh);
       if (K == kWeights && ok && b == end) {
-        ok = wait(smem_addr(&sh.end_ready[0]) + s.at * 8, ends_before >> s.at & 1, sh);
+        ok = wait<kWaitForWrites>(smem_addr(&sh.end_ready[0]) + s.at * 8, ends_before >> s.at & 1, sh);
         ends_before ^= 1u << s.at;
       }
       if (!ok)
@@ -802,7 +820,7 @@ __device__ void write_sums(const Sizes& z, O* out, Control& sh)
     const int p = tile.p + rank<K>() * kTileP + quarter * 32 + lane;
     const bool any = tile.blocks > 0; // none: an expert without rows has a gradient of zeros
     if (any) {
-      if (!wait<K == kWeights>(&sh.sums_full[d.at], d.parity, sh))
+      if (!wait<K == kWeights ? kLongWait : kWait>(&sh.sums_full[d.at], d.parity, sh))
         return;
       fence_after_sync();
     }
