@@ -567,8 +567,10 @@ SEGTOPK_API int segtopk_embedding_backward(segtopk_dtype dtype, const void* grad
  * Between segtopk_dispatch and segtopk_combine: expert e's matrix product of
  * its rows [offsets[e], offsets[e + 1]), as segtopk_group sorted them
  * (offsets: experts + 1 int64 on the device, which the host does not read).
- * Rows of `rows` from offsets[experts] on belong to no expert: they are not
- * read into any result, and their rows of `out` are zeros.
+ * Rows of `rows` from offsets[experts] on, and before offsets[0] where that is
+ * not 0, belong to no expert: they are not read into any result, and their rows
+ * of `out` are zeros. An offset that is negative, past the rows or below an
+ * earlier one counts as the nearest that is not.
  *
  * On the tensor cores: sums are held in 32 bits there, in an order that
  * depends on the sizes alone, and rounded once, to out_dtype (F16, BF16 or

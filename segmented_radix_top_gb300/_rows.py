@@ -219,8 +219,9 @@ def embedding_backward(grad_out: torch.Tensor, tokens: torch.Tensor, num_rows: i
 def expert_matmul(rows: torch.Tensor, weights: torch.Tensor, groups: ExpertGroups, *, row_scales=None,
                   weight_scales=None, out_dtype=None, out=None):
     """Each expert's matrix product of its rows (segtopk_expert_matmul):
-    out[r] = weights[e] @ rows[r] for the rows r of expert e; zeros from row
-    groups.offsets[-1] on. The offsets stay on the device.
+    out[r] = weights[e] @ rows[r] for the rows r of expert e; zeros for rows
+    that no expert has (from groups.offsets[-1] on, and before groups.offsets[0]
+    should that not be 0). The offsets stay on the device.
 
     rows: [tokens * k, width], in the order of dispatch(); weights: [experts,
     out, width] of the same type, float16 or bfloat16, either of the last two

@@ -98,7 +98,7 @@ constexpr size_t kShared = 1024 + (size_t)kOperandBytes + sizeof(Control);
 static_assert(kShared <= 227 * 1024, "shared memory of a block");
 
 struct Sizes {
-  int64_t num_rows;     // slots; those from the last offset on have no expert
+  int64_t num_rows;     // slots; those before the first offset and from the last one on have no expert
   int experts;
   int p, q, c;          // sizes; an expert's rows take the place of one
   int step;             // 8 bits: the tiles' q
@@ -928,9 +928,10 @@ product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant_
     if constexpr (K != kWeights) {
       // rows that no expert has
       const int all = (int)gridDim.x * kSumWarps;
-      const int end = sh.row_start[z.experts];
-      for (int64_t i = (int)blockIdx.x * kSumWarps + warp - (kThreads / 32 - kSumWarps); i < z.num_rows - end; i += all) {
-        O* const to = out + free_row(0, end, i) * z.out_stride;
+      const int begin = sh.row_start[0], end = sh.row_start[z.experts];
+      const int64_t rows = begin + (z.num_rows - end);
+      for (int64_t i = (int)blockIdx.x * kSumWarps + warp - (kThreads / 32 - kSumWarps); i < rows; i += all) {
+        O* const to = out + free_row(begin, end, i) * z.out_stride;
         for (int c = lane; c < z.out_stride; c += 32)
           to[c] = from_f32<O>(0.0f);
       }
