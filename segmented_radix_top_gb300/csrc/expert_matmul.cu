@@ -63,6 +63,7 @@ constexpr int kMaxStages = 6;
 constexpr int kBytesP = kTileP * 128;
 constexpr int kBox = 32;         // rows of one copy of few of an expert's rows
 constexpr int kDepth = 64;       // rows of one copy where c runs over rows
+constexpr int kProduct = 16;     // of them in one product
 constexpr int kMaxExperts = SEGTOPK_MAX_EXPERTS;
 
 enum Kind { kForward8, kForward8Pair, kForward, kForwardTurned, kWeights };
@@ -82,8 +83,6 @@ static_assert(stages_of(kForward) <= kMaxStages && stages_of(kForward8) <= kMaxS
 struct Control {
   uint64_t full[kMaxStages], empty[kMaxStages]; // copies (a pair's: at its first block) have landed; products have read them
   uint64_t sums_full[2], sums_empty[2];         // TMEM's halves (empty: at the first block)
-  uint64_t end_full[kMaxStages];                // kWeights: an expert's last rows have landed,
-  uint64_t end_ready[kMaxStages];               // and in both blocks those of others are gone
   uint64_t drained;                             // products behind a wait that ran out
   uint32_t tmem;
   int failed;                                   // a wait ran out: everybody leaves
@@ -96,6 +95,19 @@ struct Control {
 };
 constexpr size_t kShared = 1024 + (size_t)kOperandBytes + sizeof(Control);
 static_assert(kShared <= 227 * 1024, "shared memory of a block");
+
+// Descriptors of the operands. kWeights: in boxes of kDepth rows, and for an
+// expert's last rows of 8, 4, 2 and 1. Others: `large`, an expert's rows in
+// boxes of kTileP, beside p or q in boxes of kBox.
+constexpr int kEndBoxes = 4;
+struct Maps {
+  CUtensorMap p, q, large;
+};
+struct WeightsMaps {
+  CUtensorMap p, q, p_end[kEndBoxes], q_end[kEndBoxes]; // of 8 >> i rows
+};
+template <Kind K>
+using MapsOf = std::conditional_t<K == kWeights, WeightsMaps, Maps>;
 
 struct Sizes {
   int64_t num_rows;     // slots; those before the first offset and from the last one on have no expert
@@ -197,16 +209,10 @@ __device__ __forceinline__ void expect(uint32_t on, uint32_t bar, int bytes)
 // At a barrier of either block of a pair. Without a release at cluster scope,
 // which waits until all of the block's writes are visible everywhere: once
 // every block of 8-bit operands that doubled the time of a product. What the
-// other block is told here is that it may write, or has to wait for more.
+// other block is told here is that it may write.
 __device__ __forceinline__ void arrive(uint32_t bar)
 {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// The same for a block that has written to its own shared memory what products
-// of the other one read: with that release, once a tile.
-__device__ __forceinline__ void arrive_after_writes(uint32_t bar)
-{
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // The address of the first block's `bar`.
 template <Kind K>
@@ -254,34 +260,21 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
     : "memory");
   return ok != 0;
 }
-// As try_wait, for what the arrivals' blocks wrote (arrive_after_writes).
-__device__ __forceinline__ bool try_wait_for_writes(uint32_t bar, uint32_t parity)
-{
-  uint32_t ok;
-  asm volatile(
-    "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-    : "=r"(ok)
-    : "r"(bar), "r"(parity)
-    : "memory");
-  return ok != 0;
-}
 // One warp: waits for the phase of `bar` with this parity; false, for good,
 // after about a second, or once another wait of the block has run out. A
-// kLongWait lasts as long as an expert has rows: its second begins anew as
+// LONG wait lasts as long as an expert has rows: its second begins anew as
 // long as the block goes on to copy.
-enum Wait { kWait, kLongWait, kWaitForWrites };
-template <Wait W = kWait>
+template <bool LONG = false>
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Control& sh)
 {
-  auto over = [&] { return __all_sync(kAll, W == kWaitForWrites ? try_wait_for_writes(bar, parity) : try_wait(bar, parity)); };
-  if (over())
+  if (__all_sync(kAll, try_wait(bar, parity)))
     return true;
   long long start = clock64();
-  uint32_t seen = W == kLongWait ? *(volatile uint32_t*)&sh.progress : 0;
+  uint32_t seen = LONG ? *(volatile uint32_t*)&sh.progress : 0;
   bool failed = false;
-  while (!over()) {
+  while (!__all_sync(kAll, try_wait(bar, parity))) {
     if (clock64() - start > sh.wait_limit) {
-      const uint32_t now = W == kLongWait ? *(volatile uint32_t*)&sh.progress : 0;
+      const uint32_t now = LONG ? *(volatile uint32_t*)&sh.progress : 0;
       if (now != seen) {
         seen = now;
         start = clock64();
@@ -296,10 +289,10 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Control& sh)
   }
   return true;
 }
-template <Wait W = kWait>
+template <bool LONG = false>
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Control& sh)
 {
-  return wait<W>(smem_addr(bar), parity, sh);
+  return wait<LONG>(smem_addr(bar), parity, sh);
 }
 
 // Whether that phase is over already; does not wait. Asked a step ahead, so
@@ -462,10 +455,20 @@ __device__ void find_tiles(const int64_t* offsets, const Sizes& z, Control& sh)
 // both; they may land before it says so, since the phase waits for that too.
 // An expert's rows come in boxes of kTileP, or of kBox where that is less; all
 // boxes are copied whole, whatever of them there is.
+//
+// kWeights: an expert's last block of rows has `left` of them, and the products
+// read that many in steps of kProduct. Those rows are copied in boxes of 8, 4, 2
+// and 1, and the ones up to the step from behind the tensor, where zeros are
+// read; so the rows of the next expert, or of none, never get here.
+// 65536 rows of 128 experts, 2048x1024: 226 us. (Copied whole, with zeros
+// written over them by each block for the products of both, they need a release
+// at cluster scope between the two, which also waits for results on their way
+// to memory: 253 us, and 220 without it, which nothing in the order of memory
+// allows.)
 __device__ __forceinline__ int boxed(int rows) { return rows > kTileP / 2 ? kTileP : pieces(max(rows, 0), kBox) * kBox; }
 
 template <Kind K, bool IS_P>
-__device__ void copy_operands(const CUtensorMap& map, const CUtensorMap& large, const Sizes& z, char* stages, Control& sh)
+__device__ void copy_operands(const MapsOf<K>& maps, const Sizes& z, char* stages, Control& sh)
 {
   constexpr int kStages = stages_of(K);
   constexpr bool kByRows = IS_P == eight(K) && K != kWeights; // these are the expert's rows
@@ -473,9 +476,9 @@ __device__ void copy_operands(const CUtensorMap& map, const CUtensorMap& large, 
   const uint32_t on = elected(), to = smem_addr(stages) + (IS_P ? 0 : kBytesP);
   const uint32_t full = at_first<K>(&sh.full[0]), empty = smem_addr(&sh.empty[0]);
   Ring<kStages> s;
-  int used = 0; // stages whose copies are under way or have landed
-  uint32_t end_parity = 0, end_last = 0; // kWeights, a bit for each stage: its last rows' next phase; they are its last copies
-  uint32_t begun = 0;                    // kWeights: blocks of rows
+  const CUtensorMap& map = IS_P ? maps.p : maps.q;
+  int used = 0;       // stages whose copies are under way or have landed
+  uint32_t begun = 0; // kWeights: blocks of rows
   bool ok = true, ready = false;
   for (int t = blockIdx.x / blocks_of(K); ok && t < tiles; t += gridDim.x / blocks_of(K)) {
     const Tile tile = tile_at<K>(t, z, sh);
@@ -498,7 +501,7 @@ __device__ void copy_operands(const CUtensorMap& map, const CUtensorMap& large, 
     const int box = K == kWeights || (IS_P && K == kForwardTurned) ? 64 : kByRows && !whole ? kBox : kTileP;
     const int first = uniform((IS_P ? tile.p + me * kTileP : tile.q + me * width) + (kByRows ? tile.row : 0));
     const int row = uniform(tile.row), matrix = uniform(kByRows ? 0 : tile.expert), blocks = uniform(tile.blocks);
-    const int end = K == kWeights && tile.rows % kDepth != 0 ? blocks - 1 : blocks; // kWeights: the block with last rows
+    const int left = uniform(K == kWeights ? tile.rows % kDepth : 0); // rows of the last block, if not all
     for (int b = 0; b < blocks; ++b) {
       if (!__all_sync(kAll, ready))
         ok = wait(empty + s.at * 8, s.parity ^ 1, sh);
@@ -511,80 +514,56 @@ __device__ void copy_operands(const CUtensorMap& map, const CUtensorMap& large, 
 #else
       constexpr int extra = 0;
 #endif
-      uint32_t bar = full + s.at * 8;
-      const uint32_t at = to + s.at * stage_bytes(K);
-      if (K == kWeights && b == end) {
-        // each block of the pair first takes out the rows of others
-        if (IS_P) {
-          if (me == 0 && on)
-            arrive(bar);
-          expect(on, smem_addr(&sh.end_full[0]) + s.at * 8, landing + extra);
-        }
-        bar = smem_addr(&sh.end_full[0]) + s.at * 8;
-        end_parity ^= 1u << s.at;
-        end_last |= 1u << s.at;
-      } else {
-        if (IS_P && me == 0)
-          expect(on, bar, expected + extra);
-        end_last &= ~(1u << s.at);
-      }
+      const uint32_t bar = full + s.at * 8, at = to + s.at * stage_bytes(K);
+      const bool end = K == kWeights && left > 0 && b == blocks - 1;
+      if (IS_P && me == 0)
+        expect(on, bar, (end ? expected / (kDepth / kProduct) * pieces(left, kProduct) : expected) + extra);
       used = min(used + 1, kStages);
       s.next();
       ready = over(empty + s.at * 8, s.parity ^ 1);
       if constexpr (K == kWeights) {
-        for (int i = 0; i < lines; i += 64)
-          tile_load<true>(on, at + i * 128, &map, first + i, row + b * kDepth, 0, bar);
+        if (!end) {
+          for (int i = 0; i < lines; i += 64)
+            tile_load<true>(on, at + i * 128, &map, first + i, row + b * kDepth, 0, bar);
+        } else {
+          const CUtensorMap* const boxes = IS_P ? maps.p_end : maps.q_end;
+          for (int i = 0; i < lines; i += 64) {
+            int r = 0;
+            auto copy = [&](int box, int y) {
+              tile_load<true>(on, at + (i + r) * 128, &boxes[box], first + i, y, 0, bar);
+              r += 8 >> box;
+            };
+            while (r + 8 <= left)
+              copy(0, row + b * kDepth + r);
+#pragma unroll
+            for (int box = 1; box < kEndBoxes; ++box)
+              if (left & 8 >> box)
+                copy(box, row + b * kDepth + r);
+#pragma unroll
+            for (int box = kEndBoxes - 1; box >= 0; --box) // 8 is half of kProduct
+              if (r & 8 >> box)
+                copy(box, (int)z.num_rows);
+          }
+        }
       } else if constexpr (K == kForwardTurned && IS_P) {
 #pragma unroll
         for (int i = 0; i < kTileP; i += 64)
           tile_load<true>(on, at + i * 128, &map, first + i, b * kDepth, matrix, bar);
       } else if (whole) {
-        tile_load<pair(K)>(on, at, &large, b * (eight(K) ? 128 : 64), first, 0, bar);
+        tile_load<pair(K)>(on, at, &maps.large, b * (eight(K) ? 128 : 64), first, 0, bar);
       } else {
         for (int i = 0; i < lines; i += box)
           tile_load<pair(K)>(on, at + i * 128, &map, b * (eight(K) ? 128 : 64), first + i, matrix, bar);
       }
     }
   }
-  if (!ok && IS_P) {
+  if (!ok && IS_P && me == 0) {
     // what is under way lands before the blocks end (a second each at most)
     for (int i = 0; i < used; ++i) {
       s.at = s.at == 0 ? kStages - 1 : s.at - 1;
       s.parity ^= s.at == kStages - 1;
-      if (end_last >> s.at & 1)
-        mbar_wait(&sh.end_full[s.at], ~end_parity >> s.at & 1, sh.wait_limit);
-      else if (me == 0)
-        mbar_wait(&sh.full[s.at], s.parity, sh.wait_limit);
+      mbar_wait(&sh.full[s.at], s.parity, sh.wait_limit);
     }
-  }
-}
-
-// kWeights, one warp of each block: in an expert's last block of rows, once it
-// has landed, the rows of the next expert, or of none, become zeros, as the
-// products read them.
-__device__ void clear_ends(const Sizes& z, char* stages, Control& sh)
-{
-  constexpr Kind K = kWeights;
-  const int lane = threadIdx.x & 31, tiles = sh.tile_start[z.experts];
-  int next = 0;        // stage
-  uint32_t before = 0; // a bit for each stage: the parity of its last blocks of rows
-  for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2) {
-    const Tile tile = tile_at<K>(t, z, sh);
-    const int copies = 2 + pieces(pieces(tile.width, kStepQ) * kStepQ / 2, 64), left = tile.rows % kDepth;
-    const int at = (next + tile.blocks - 1) % stages_of(K);
-    next = (next + tile.blocks) % stages_of(K);
-    if (left == 0)
-      continue;
-    if (!wait<kLongWait>(&sh.end_full[at], before >> at & 1, sh))
-      return;
-    before ^= 1u << at;
-    for (int i = 0; i < copies; ++i)
-      for (int byte = left * 128 + lane * 16; byte < kDepth * 128; byte += 512)
-        *reinterpret_cast<uint4*>(stages + at * stage_bytes(K) + i * kDepth * 128 + byte) = uint4{};
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (lane == 0)
-      arrive_after_writes(at_first<K>(&sh.end_ready[at]));
   }
 }
 
@@ -600,13 +579,13 @@ __device__ void issue_products(const Sizes& z, char* stages, Control& sh)
                  sums_empty = smem_addr(&sh.sums_empty[0]);
   Ring<stages_of(K)> s;
   Ring<2> d;
-  uint32_t ends_before = 0;
   bool ok = true, ready = false, sums_ready = false;
   for (int t = blockIdx.x / blocks_of(K); ok && t < tiles; t += gridDim.x / blocks_of(K)) {
     const Tile tile = tile_at<K>(t, z, sh);
     const uint32_t instruction = uniform((int)(z.instruction | (uint32_t)(pieces(tile.width, kStepQ) * kStepQ / 8) << 17));
     const int blocks = uniform(tile.blocks);
-    const int end = uniform(K == kWeights && tile.rows % kDepth != 0 ? blocks - 1 : blocks);
+    // four products: 32 bytes of c on, or 16 rows of 128 bytes; an expert's last rows may be fewer
+    const int last_products = uniform(K == kWeights && tile.rows > 0 ? pieces(tile.rows - (blocks - 1) * kDepth, kProduct) : 4);
     for (int b = 0; b < blocks; ++b) {
       // the sums of one block, or of all
       const bool first = eight(K) || b == 0, last = eight(K) || b == blocks - 1;
@@ -614,10 +593,6 @@ __device__ void issue_products(const Sizes& z, char* stages, Control& sh)
         ok = wait(sums_empty + d.at * 8, d.parity ^ 1, sh);
       if (ok && !__all_sync(kAll, ready))
         ok = wait(full + s.at * 8, s.parity, sh);
-      if (K == kWeights && ok && b == end) {
-        ok = wait<kWaitForWrites>(smem_addr(&sh.end_ready[0]) + s.at * 8, ends_before >> s.at & 1, sh);
-        ends_before ^= 1u << s.at;
-      }
       if (!ok)
         break;
       fence_after_sync();
@@ -629,11 +604,12 @@ __device__ void issue_products(const Sizes& z, char* stages, Control& sh)
         d.next();
         sums_ready = over(sums_empty + d.at * 8, d.parity ^ 1);
       }
-      // four products: 32 bytes of c on, or 16 rows of 128 bytes
+      const int products = K == kWeights && b == blocks - 1 ? last_products : 4;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        multiply<K>(on, sums, p + i * (p_by_rows(K) ? 2 : 128), q + i * (q_by_rows(K) ? 2 : 128), instruction,
-                    !first || i > 0);
+        if (K != kWeights || i < products)
+          multiply<K>(on, sums, p + i * (p_by_rows(K) ? 2 : 128), q + i * (q_by_rows(K) ? 2 : 128), instruction,
+                      !first || i > 0);
       commit<pair(K)>(on, free);
       if (last)
         commit<pair(K)>(on, done);
@@ -820,7 +796,7 @@ __device__ void write_sums(const Sizes& z, O* out, Control& sh)
     const int p = tile.p + rank<K>() * kTileP + quarter * 32 + lane;
     const bool any = tile.blocks > 0; // none: an expert without rows has a gradient of zeros
     if (any) {
-      if (!wait<K == kWeights ? kLongWait : kWait>(&sh.sums_full[d.at], d.parity, sh))
+      if (!wait<K == kWeights>(&sh.sums_full[d.at], d.parity, sh))
         return;
       fence_after_sync();
     }
@@ -857,8 +833,7 @@ __device__ void write_sums(const Sizes& z, O* out, Control& sh)
 
 template <Kind K, class O>
 __global__ void __cluster_dims__(blocks_of(K), 1, 1) __launch_bounds__(kThreads, 1)
-product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
-               const __grid_constant__ CUtensorMap large, const int64_t* offsets, const __grid_constant__ Sizes z, O* out)
+product_kernel(const __grid_constant__ MapsOf<K> maps, const int64_t* offsets, const __grid_constant__ Sizes z, O* out)
 {
   extern __shared__ char dynamic[];
   char* const stages = dynamic + (-smem_addr(dynamic) & 1023);
@@ -866,14 +841,12 @@ product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant_
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 32)
-    for (const CUtensorMap* map : {&p_map, &q_map, &large})
-      asm volatile("prefetch.tensormap [%0];" ::"l"(map));
+    for (size_t i = 0; i < sizeof(maps) / sizeof(CUtensorMap); ++i)
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.p + i));
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
-      mbar_init(&sh.end_full[i], 1);
-      mbar_init(&sh.end_ready[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.sums_full[i], 1);
@@ -909,14 +882,12 @@ product_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant_
     if constexpr (eight(K))
       asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
-      copy_operands<K, true>(p_map, large, z, stages, sh);
+      copy_operands<K, true>(maps, z, stages, sh);
     } else if (warp == 3) {
-      copy_operands<K, false>(q_map, large, z, stages, sh);
+      copy_operands<K, false>(maps, z, stages, sh);
     } else if (warp == 1) {
       if (rank<K>() == 0)
         issue_products<K>(z, stages, sh);
-    } else if (K == kWeights && warp == 2) {
-      clear_ends(z, stages, sh);
     }
   } else {
     if constexpr (eight(K)) {
@@ -1005,8 +976,7 @@ cudaError_t allow_shared()
 }
 
 template <Kind K, class O>
-int run(const CUtensorMap& p, const CUtensorMap& q, const CUtensorMap& large, const int64_t* offsets, Sizes z, void* out, int sms,
-        int64_t most_tiles, void* stream)
+int run(const MapsOf<K>& maps, const int64_t* offsets, Sizes z, void* out, int sms, int64_t most_tiles, void* stream)
 {
   uint32_t extra;
   test_hooks(&z.wait_limit, &extra);
@@ -1015,7 +985,7 @@ int run(const CUtensorMap& p, const CUtensorMap& q, const CUtensorMap& large, co
   if (e != cudaSuccess)
     return record_cuda_error(e);
   const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(sms / blocks_of(K), most_tiles)) * blocks_of(K);
-  return finish(launch(product_kernel<K, O>, dim3(grid), kThreads, kShared, (cudaStream_t)stream, p, q, large, offsets, z, (O*)out), 1);
+  return finish(launch(product_kernel<K, O>, dim3(grid), kThreads, kShared, (cudaStream_t)stream, maps, offsets, z, (O*)out), 1);
 }
 
 bool float_type_of(int dtype) { return dtype == SEGTOPK_F16 || dtype == SEGTOPK_BF16 || dtype == SEGTOPK_F32; }
@@ -1097,13 +1067,13 @@ extern "C" int segtopk_expert_matmul(segtopk_dtype dtype, const void* rows, int6
   int sms;
   if ((rc = check_device(&sms)) != SEGTOPK_SUCCESS)
     return rc;
-  CUtensorMap p, q, large = {};
-  cudaError_t e = turned ? describe(&p, map_type(dtype), 2, weights, out_width, width, experts, line, expert_stride, kDepth)
-                         : describe(&p, map_type(dtype), 2, weights, width, out_width, experts, line, expert_stride, kTileP);
+  Maps maps;
+  cudaError_t e = turned ? describe(&maps.p, map_type(dtype), 2, weights, out_width, width, experts, line, expert_stride, kDepth)
+                         : describe(&maps.p, map_type(dtype), 2, weights, width, out_width, experts, line, expert_stride, kTileP);
   if (e == cudaSuccess)
-    e = describe(&q, map_type(dtype), 2, rows, width, num_rows, 1, row_stride, row_stride, kBox);
+    e = describe(&maps.q, map_type(dtype), 2, rows, width, num_rows, 1, row_stride, row_stride, kBox);
   if (e == cudaSuccess)
-    e = describe(&large, map_type(dtype), 2, rows, width, num_rows, 1, row_stride, row_stride, kTileP);
+    e = describe(&maps.large, map_type(dtype), 2, rows, width, num_rows, 1, row_stride, row_stride, kTileP);
   if (e != cudaSuccess)
     return record_cuda_error(e);
   Sizes z = {};
@@ -1117,8 +1087,8 @@ extern "C" int segtopk_expert_matmul(segtopk_dtype dtype, const void* rows, int6
   return with_float_type(out_dtype, [&](auto zero) {
     using O = decltype(zero);
     z.out_vectors = rows_fit(out, out_width, out_width, sizeof(O), 16 / (int)sizeof(O));
-    return turned ? run<kForwardTurned, O>(p, q, large, offsets, z, out, sms, tiles, stream)
-                  : run<kForward, O>(p, q, large, offsets, z, out, sms, tiles, stream);
+    return turned ? run<kForwardTurned, O>(maps, offsets, z, out, sms, tiles, stream)
+                  : run<kForward, O>(maps, offsets, z, out, sms, tiles, stream);
   });
 }
 
@@ -1150,14 +1120,14 @@ extern "C" int segtopk_expert_matmul_f8(const void* rows, int64_t num_rows, int6
   int sms;
   if ((rc = check_device(&sms)) != SEGTOPK_SUCCESS)
     return rc;
-  CUtensorMap p, q, large = {};
-  cudaError_t e = describe(&p, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, width, num_rows, 1, row_stride,
+  Maps maps;
+  cudaError_t e = describe(&maps.p, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, width, num_rows, 1, row_stride,
                            row_stride, kBox);
   if (e == cudaSuccess)
-    e = describe(&large, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, width, num_rows, 1, row_stride, row_stride,
+    e = describe(&maps.large, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, width, num_rows, 1, row_stride, row_stride,
                  kTileP);
   if (e == cudaSuccess)
-    e = describe(&q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, weights, width, out_width, experts, line, expert_stride,
+    e = describe(&maps.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, weights, width, out_width, experts, line, expert_stride,
                  kTileP);
   if (e != cudaSuccess)
     return record_cuda_error(e);
@@ -1180,8 +1150,8 @@ extern "C" int segtopk_expert_matmul_f8(const void* rows, int64_t num_rows, int6
   return with_float_type(out_dtype, [&](auto zero) {
     using O = decltype(zero);
     z.out_vectors = rows_fit(out, out_width, out_width, sizeof(O), 16 / (int)sizeof(O));
-    return by_pairs ? run<kForward8Pair, O>(p, q, large, offsets, z, out, sms, tiles, stream)
-                    : run<kForward8, O>(p, q, large, offsets, z, out, sms, tiles, stream);
+    return by_pairs ? run<kForward8Pair, O>(maps, offsets, z, out, sms, tiles, stream)
+                    : run<kForward8, O>(maps, offsets, z, out, sms, tiles, stream);
   });
 }
 
@@ -1212,10 +1182,18 @@ extern "C" int segtopk_expert_matmul_weights(segtopk_dtype dtype, const void* a_
     const cudaError_t e = cudaMemsetAsync(out, 0, bytes, (cudaStream_t)stream);
     return e == cudaSuccess ? SEGTOPK_SUCCESS : record_cuda_error(e);
   }
-  CUtensorMap p, q;
-  cudaError_t e = describe(&p, map_type(dtype), 2, b_rows, b_width, num_rows, 1, b_stride, b_stride, kDepth);
-  if (e == cudaSuccess)
-    e = describe(&q, map_type(dtype), 2, a_rows, a_width, num_rows, 1, a_stride, a_stride, kDepth);
+  WeightsMaps maps;
+  cudaError_t e = cudaSuccess;
+  auto add = [&](CUtensorMap* map, const void* rows, int64_t width, int64_t stride, int box) {
+    if (e == cudaSuccess)
+      e = describe(map, map_type(dtype), 2, rows, width, num_rows, 1, stride, stride, box);
+  };
+  add(&maps.p, b_rows, b_width, b_stride, kDepth);
+  add(&maps.q, a_rows, a_width, a_stride, kDepth);
+  for (int i = 0; i < kEndBoxes; ++i) {
+    add(&maps.p_end[i], b_rows, b_width, b_stride, 8 >> i);
+    add(&maps.q_end[i], a_rows, a_width, a_stride, 8 >> i);
+  }
   if (e != cudaSuccess)
     return record_cuda_error(e);
   Sizes z = {};
@@ -1228,8 +1206,7 @@ extern "C" int segtopk_expert_matmul_weights(segtopk_dtype dtype, const void* a_
   return with_float_type(out_dtype, [&](auto zero) {
     using O = decltype(zero);
     z.out_vectors = rows_fit(out, b_width, b_width, sizeof(O), 16 / (int)sizeof(O));
-    // The kernel fetches three descriptors ahead and copies with two: the third is a valid one too.
-    return run<kWeights, O>(p, q, p, offsets, z, out, sms, tiles, stream);
+    return run<kWeights, O>(maps, offsets, z, out, sms, tiles, stream);
   });
 }
 

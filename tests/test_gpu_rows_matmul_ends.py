@@ -1,7 +1,6 @@
-"""The weights' gradient where every tile ends inside a block of rows, so that
-both blocks of a pair clear the rows of others at every tile just before the
-products read them: those rows hold NaN or very large values, and none of them
-may reach a result, however often it is computed."""
+"""The weights' gradient where every tile ends inside a block of rows, next to
+the rows of others: those hold NaN or very large values, and none of them may
+reach a result, however often it is computed."""
 import pytest
 import torch
 
