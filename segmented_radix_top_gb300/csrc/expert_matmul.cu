@@ -27,23 +27,34 @@
 // rows of which an expert has few go to single blocks.
 //
 // Operands come by TMA in blocks of 128 bytes of c, six of them under way (192
-// KB). Of a block's twelve warps one copies p, one q, one issues products and
-// eight take sums out of TMEM, which holds two sets of them, so that one is
-// taken out while the next is computed. Blocks stay on their SM and take tile
-// after tile; each finds its tiles from the experts' offsets, which the host
-// never reads.
+// KB), four in a single block with its 256 q. Of a block's twelve warps one
+// copies p, one q, one issues products and eight take sums out of TMEM, which
+// holds two sets of them, so that one is taken out while the next is computed.
+// Blocks stay on their SM and take tile after tile; each finds its tiles from
+// the experts' offsets, which the host never reads.
 //
-// Measured on GB300 (through the Python API, results of the type of the rows):
-//   16 bits, 8192^3, one expert                604 us, 1820 TFLOP/s (cuBLAS 545)
-//   16 bits, 65536 rows of 128 experts, 2048x1024   190 us forward, 193 the
-//     rows' gradient, 222 the weights'
-//   8 bits, 131072 rows of 128 experts, 4096x2048   975 us, 2257 TFLOP/s
-//   8 bits, 64 rows of 64 experts, 2048x1024         17 us (decode)
+// Measured on GB300 (two of them, through the Python API, results of the type of
+// the rows, us): 20 calls one after the other, and the same calls for 4 s, which
+// the GPU's power limit slows down.
+//   16 bits, 8192^3, one expert                       592 to 611   692
+//     cuBLAS                                          539 to 550   633
+//   16 bits, 65536 rows of 128 experts, 2048x1024
+//     forward                                         183 to 189   213
+//     rows' gradient                                  187 to 192   217
+//     weights' gradient                               226          251
+//   8 bits, 131072 rows of 128 experts, 4096x2048     975 to 980   1056 to 1070
+//   8 bits, 16384 rows of one expert, 8192x8192       864
+//   8 bits, 64 rows of 64 experts, 2048x1024          17
 // A block of the main loop takes 518 cycles of the tensor cores' 512 in the
-// first; the clock is then at 1.45 GHz of 2.07 by the GPU's power limit. In 8
-// bits it takes 920: products that are issued back to back end that far apart
-// while sums are loaded from TMEM, 530 while none are, and each block's 128 KB
-// of sums have to be loaded. With few rows the weights' bytes bound it.
+// first. At the power limit its clock is 1.37 to 1.40 GHz, the library's 1.47 to
+// 1.49: of the 9 % between the two 7 are the energy that a product takes here,
+// and 2 cycles. In 8 bits a block takes 920 cycles: products that are issued back
+// to back end that far apart while sums are loaded from TMEM, 530 while none are,
+// and each block's 128 KB of sums have to be loaded. Whether TMEM carries no
+// more, or the products wait for the release of one of the two sets, these
+// figures do not tell apart. Beside that an expert's last tile of 256 rows is
+// half empty on average, a ninth of the work at 1024 rows an expert. With few
+// rows the weights' bytes bound it.
 #include <atomic>
 #include <cuda.h>
 
@@ -1132,7 +1143,9 @@ extern "C" int segtopk_expert_matmul_f8(const void* rows, int64_t num_rows, int6
   if (e != cudaSuccess)
     return record_cuda_error(e);
   // Tiles of 128 columns where those of 256 would leave SMs idle. Pairs where
-  // experts have rows for both blocks.
+  // experts have rows for both blocks: 131072 rows of 128 experts, 4096x2048,
+  // 1073 us, 1143 by single blocks. The rows are counted as if all had an
+  // expert; the offsets are the device's.
   const int step = forward_tiles(num_rows, kTileP, out_width, kTileQ, experts) < 2 * sms ? kTileP : kTileQ;
   const bool by_pairs = step == kTileQ && num_rows / experts >= 256;
   const int64_t tiles = forward_tiles(num_rows, kTileP, out_width, step, experts);

@@ -87,7 +87,8 @@ __device__ __forceinline__ bool in_row(int lane, int lanes, int width, int i, in
 // 4096 in bf16 (65536 of them) took 205 us with 2 parts and 8 warps, 172 with 4
 // and 4, 178 with 8 and 2, 200 with 16 and one; of 2048 199, 170 (4 and 2) and
 // 158 (8 and one). A row read ahead into registers, or several into shared
-// memory, cost more warps than it hid latency.
+// memory, cost more warps than it hid latency. At 80 registers 8 parts in 16
+// bits spill 8 to 64 bytes a thread, which the figures above include.
 template <class T, class W, int N, int PARTS, int WARPS>
 __global__ void __launch_bounds__(threads_of(WARPS), std::max(1, (WARPS == 1 ? 768 : PARTS == 4 ? 1024 : 768) / threads_of(WARPS)))
 norm_kernel(const T* x, int64_t x_stride, uint32_t rows, int width, const W* weight, const W* bias, float eps, T* out,
@@ -182,6 +183,9 @@ norm_kernel(const T* x, int64_t x_stride, uint32_t rows, int width, const W* wei
 // row, it loads its next row while it works on one: 65536 rows of 4096 in
 // bf16 283 us, 315 without; with 4 parts and 4 warps 294. Groups of two warps
 // and single ones do not: rows of 2048 278 us, 354 with a row ahead.
+// Rows over 8192 values take a block of 32 warps, whose 64 registers a thread
+// spill 120 to 576 bytes: 16384 rows of 16384 in bf16 436 us, 237 at the copy
+// rate, in f32 1202 and 474.
 constexpr bool ahead(int warps) { return warps >= 8; }
 
 template <class T, class W, int N, int PARTS, int WARPS>
@@ -456,7 +460,7 @@ cudaError_t with_backward_group(int64_t parts, int64_t rows, F&& f)
 {
   if (parts <= 64)
     SEGTOPK_GROUP(2, 1);
-  // with few rows more warps for each: 1237 of 1001 in f32 9.5 us, 13.0 by (4, 2)
+  // with few rows more warps for each: 1237 of 1001 in f32 8.3 us, 13.0 by (4, 2); measured at that size alone
   const bool few = rows <= 152 * 16;
   if (parts <= 128 && !few)
     SEGTOPK_GROUP(4, 1);
