@@ -43,7 +43,7 @@
 //     rows' gradient                                  187 to 192   217
 //     weights' gradient                               226          251
 //   8 bits, 131072 rows of 128 experts, 4096x2048     975 to 980   1056 to 1070
-//   8 bits, 16384 rows of one expert, 8192x8192       864
+//   8 bits, 16384 rows of one expert, 8192x8192       864 to 888
 //   8 bits, 64 rows of 64 experts, 2048x1024          17
 // A block of the main loop takes 518 cycles of the tensor cores' 512 in the
 // first. At the power limit its clock is 1.37 to 1.40 GHz, the library's 1.47 to
@@ -217,13 +217,15 @@ __device__ __forceinline__ void expect(uint32_t on, uint32_t bar, int bytes)
                "r"(bytes), "r"(on)
                : "memory");
 }
-// At a barrier of either block of a pair. Without a release at cluster scope,
-// which waits until all of the block's writes are visible everywhere: once
-// every block of 8-bit operands that doubled the time of a product. What the
-// other block is told here is that it may write.
+// At a barrier of either block of a pair: that this warp's loads from TMEM are
+// done, so that products of the first block may write there. The fences for
+// TMEM around it (fence_before_sync, fence_after_sync) and the scope of the
+// cluster order the two; no memory is handed over, so it is no release, which
+// waits until all of the block's writes are visible everywhere: once every block
+// of 8-bit operands that doubled the time of a product.
 __device__ __forceinline__ void arrive(uint32_t bar)
 {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // The address of the first block's `bar`.
 template <Kind K>
@@ -261,29 +263,35 @@ __device__ __forceinline__ void sums_load(uint32_t (&v)[64], uint32_t at)
                : "memory");
 }
 
+// TMEM: for an arrive(), which hands over TMEM alone.
+template <bool TMEM>
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
 {
   uint32_t ok;
-  asm volatile(
-    "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-    : "=r"(ok)
-    : "r"(bar), "r"(parity)
-    : "memory");
+#define SEGTOPK_WAIT(HOW)                                                                                        \
+  asm volatile("{\n .reg .pred p;\n mbarrier." HOW ".shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"   \
+               : "=r"(ok)                                                                                        \
+               : "r"(bar), "r"(parity)                                                                           \
+               : "memory")
+  if constexpr (TMEM)
+    SEGTOPK_WAIT("try_wait.parity.relaxed.cluster");
+  else
+    SEGTOPK_WAIT("try_wait.parity");
   return ok != 0;
 }
 // One warp: waits for the phase of `bar` with this parity; false, for good,
 // after about a second, or once another wait of the block has run out. A
 // LONG wait lasts as long as an expert has rows: its second begins anew as
 // long as the block goes on to copy.
-template <bool LONG = false>
+template <bool LONG = false, bool TMEM = false>
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Control& sh)
 {
-  if (__all_sync(kAll, try_wait(bar, parity)))
+  if (__all_sync(kAll, try_wait<TMEM>(bar, parity)))
     return true;
   long long start = clock64();
   uint32_t seen = LONG ? *(volatile uint32_t*)&sh.progress : 0;
   bool failed = false;
-  while (!__all_sync(kAll, try_wait(bar, parity))) {
+  while (!__all_sync(kAll, try_wait<TMEM>(bar, parity))) {
     if (clock64() - start > sh.wait_limit) {
       const uint32_t now = LONG ? *(volatile uint32_t*)&sh.progress : 0;
       if (now != seen) {
@@ -308,16 +316,17 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Control& sh
 
 // Whether that phase is over already; does not wait. Asked a step ahead, so
 // that the answer is there when the step comes.
+template <bool TMEM = false>
 __device__ __forceinline__ bool over(uint32_t bar, uint32_t parity)
 {
   uint32_t ok;
-  asm volatile(
-    "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-    : "=r"(ok)
-    : "r"(bar), "r"(parity)
-    : "memory");
+  if constexpr (TMEM)
+    SEGTOPK_WAIT("test_wait.parity.relaxed.cluster");
+  else
+    SEGTOPK_WAIT("test_wait.parity");
   return ok != 0;
 }
+#undef SEGTOPK_WAIT
 
 // The same value in all lanes, known to be so.
 __device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(kAll, x); }
@@ -601,7 +610,7 @@ __device__ void issue_products(const Sizes& z, char* stages, Control& sh)
       // the sums of one block, or of all
       const bool first = eight(K) || b == 0, last = eight(K) || b == blocks - 1;
       if (first && !__all_sync(kAll, sums_ready))
-        ok = wait(sums_empty + d.at * 8, d.parity ^ 1, sh);
+        ok = wait<false, true>(sums_empty + d.at * 8, d.parity ^ 1, sh);
       if (ok && !__all_sync(kAll, ready))
         ok = wait(full + s.at * 8, s.parity, sh);
       if (!ok)
@@ -613,7 +622,7 @@ __device__ void issue_products(const Sizes& z, char* stages, Control& sh)
       ready = over(full + s.at * 8, s.parity);
       if (last) {
         d.next();
-        sums_ready = over(sums_empty + d.at * 8, d.parity ^ 1);
+        sums_ready = over<true>(sums_empty + d.at * 8, d.parity ^ 1);
       }
       const int products = K == kWeights && b == blocks - 1 ? last_products : 4;
 #pragma unroll
