@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 LIMIT, ROWS = 1 << 20, 1 << 21
 
 
-@pytest.mark.parametrize("last", [0, 5])  # rows of nobody in the last block of rows, which are cleared
+@pytest.mark.parametrize("last", [0, 5])  # rows of nobody behind those of the last block
 def test_rows_that_take_longer_than_the_bound(instr, last):  # noqa: F811
     a, b = whole(ROWS, 64, seed=1, dtype=torch.bfloat16, most=1), whole(ROWS, 128, seed=2, dtype=torch.bfloat16, most=1)
     if last:
